@@ -2,8 +2,6 @@
 // and kernel launches on the caller's stream.  No torch types, no exceptions across the ABI.
 #include <hip/hip_runtime.h>
 
-#include <cstdarg>
-#include <cstdio>
 #include <cstring>
 #include <map>
 #include <mutex>
@@ -11,6 +9,7 @@
 #include <vector>
 
 #include "../../include/ssm.h"
+#include "host_util.hpp"
 #include "scan_table.hpp"
 #include "scan_rows_table.hpp"
 #include "scan_time_table.hpp"
@@ -20,45 +19,9 @@
 #include "ssd_fwd.hpp"
 #include "scan_bwd_rows.hpp"
 
+using namespace ssm_host;
+
 namespace {
-
-thread_local char g_err[512] = "";
-
-ssm_status_t fail(ssm_status_t s, const char* fmt, ...) {
-  va_list ap;
-  va_start(ap, fmt);
-  vsnprintf(g_err, sizeof g_err, fmt, ap);
-  va_end(ap);
-  return s;
-}
-
-bool mul_ok(int64_t a, int64_t b, int64_t* out) { return !__builtin_mul_overflow(a, b, out); }
-
-struct Range {
-  const void* p;
-  int64_t bytes;
-};
-
-bool overlap(Range a, Range b) {
-  if (!a.p || !b.p || a.bytes <= 0 || b.bytes <= 0) return false;
-  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a.p), b0 = reinterpret_cast<uintptr_t>(b.p);
-  return a0 < b0 + static_cast<uintptr_t>(b.bytes) && b0 < a0 + static_cast<uintptr_t>(a.bytes);
-}
-
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-
-struct Arg {
-  const void* p;
-  int64_t align;
-  const char* name;
-};
-
-// first non-NULL argument not aligned to its element size, or NULL
-const Arg* misaligned(const Arg* args, size_t n) {
-  for (size_t i = 0; i < n; ++i)
-    if (args[i].p && !aligned(args[i].p, static_cast<uintptr_t>(args[i].align))) return &args[i];
-  return nullptr;
-}
 
 bool dstate_supported(int64_t n) {
   return n == 1 || n == 2 || n == 4 || n == 8 || n == 16 || n == 32 || n == 64;
@@ -79,19 +42,6 @@ int default_npl(int64_t n, int64_t workgroups) {
   int npl = n >= 4 ? 4 : static_cast<int>(n);
   while (n / npl > 8) npl *= 2;  // at most 8 scan waves per workgroup
   return npl;
-}
-
-// compute units of the current device, cached per device
-int device_cus() {
-  static int cache[64] = {};
-  int dev = 0;
-  if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 64) return 256;
-  int cus = __atomic_load_n(&cache[dev], __ATOMIC_RELAXED);
-  if (cus == 0) {
-    if (hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || cus <= 0) cus = 256;
-    __atomic_store_n(&cache[dev], cus, __ATOMIC_RELAXED);
-  }
-  return cus;
 }
 
 // ---- kernel tables -----------------------------------------------------------------------------
@@ -205,12 +155,6 @@ ssm_status_t get_scratch(hipStream_t stream, int64_t floats, float** out) {
     s.floats = floats;
   }
   *out = s.ptr;
-  return SSM_OK;
-}
-
-ssm_status_t check_launch(const char* what) {
-  const hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return fail(SSM_ERR_HIP, "%s launch failed: %s", what, hipGetErrorString(e));
   return SSM_OK;
 }
 
