@@ -498,6 +498,187 @@ SSM_API ssm_status_t ssm_ssd_state_update(int64_t batch, int64_t nheads, int64_t
                                           const float *D, const void *z, const float *dt_bias, int dt_softplus,
                                           void *y, void *stream);
 
+/*
+ * ---- Serving: packed prompts and a cache of slots ------------------------
+ *
+ * A server holds one state per sequence in a cache (one cache per layer and
+ * kind: the scan's states, the convolution's windows) and works on batches
+ * that change with every call: prompts of different lengths lying one behind
+ * another, and single tokens of many sequences.  "Mamba 论文精读" sec. 6: the
+ * fixed-size state is all that a sequence carries from token to token.
+ *
+ * The calls below are those of the same name above without "packed" or
+ * "cache", on such batches: the same formulas, dtypes, fp32 arithmetic,
+ * optional arguments, statuses and stream semantics, and (unless said
+ * otherwise) the input term SSM_BBAR_DELTA_B.  They allocate nothing, keep
+ * nothing between calls, and may be captured into a HIP graph.
+ *
+ * Indices that lie in device memory are checked by the kernels: a slot that
+ * is negative or not below the cache's slots is no slot (a negative one marks
+ * the padding of a batch), and cu_seqlens that do not rise, or leave
+ * 0..total, give unspecified outputs within the tensors; neither is read or
+ * written out of range, and neither gives an error.  Slots that one call
+ * writes must differ from one another: the content of a slot given twice,
+ * and the outputs of its entries, are unspecified.
+ */
+
+/* A cache: `slots` entries of contiguous elements, slot_stride elements apart
+ * (0: one directly behind the other; a larger stride serves a cache that is
+ * one layer of a common allocation).  slots at most 2^31 - 1.  The data of
+ * slots that a call does not name is left as it was.  reserved must be zero.
+ * dtype is the storage type of the entries.  A state is read as fp32, all
+ * arithmetic and the read-out use fp32, and an SSM_BF16 cache rounds each
+ * value once (to nearest, ties to even) when the call stores it: with bf16
+ * entries a decay so slow that a step changes a state by less than 2^-9 of
+ * its value is lost to that rounding, which fp32 entries avoid. */
+typedef struct {
+  void *data;
+  int64_t slots;
+  int64_t slot_stride;
+  int32_t dtype;
+  int32_t reserved;
+} ssm_cache_t;
+
+/* Packed sequences.  Sequence s is the rows cu_seqlens[s] .. cu_seqlens[s+1]-1
+ * of every packed tensor (of `total` rows); rows of no sequence (before the
+ * first, behind the last) are neither read nor written.
+ *   cu_seqlens   (sequences + 1) int32 on the device, not falling
+ *   cache_slots  (sequences) int32 on the device: each sequence's slot, or
+ *                NULL: sequence s has slot s
+ *   has_initial  (sequences) bytes on the device, or NULL: whether a sequence
+ *                starts from its slot's content (not 0) or from zeros (0, and
+ *                with NULL every one).  A sequence with no slot starts from
+ *                zeros.
+ *   max_seqlen   the longest sequence's length, 0 if it is not known (then
+ *                `total` is taken).  It only chooses the launch shape: any
+ *                value gives right results.
+ * After the call each sequence's slot holds its state after its last row.  A
+ * sequence of no rows leaves its slot as it was, has_initial or not.
+ * total, sequences and max_seqlen are at most 2^31 - 1. */
+typedef struct {
+  int64_t total;
+  int64_t sequences;
+  int64_t max_seqlen;
+  const int32_t *cu_seqlens;
+  const int32_t *cache_slots;
+  const uint8_t *has_initial;
+} ssm_packed_t;
+
+/* Elements between the rows (tokens) of each tensor, 0 for contiguous rows,
+ * at least the row's own elements otherwise: x, z, delta, B and C may be
+ * columns of a projection's wider output.  A row's own elements are
+ * contiguous.  For ssm_causal_conv1d_* only x and y count; for the SSD step
+ * delta is dt. */
+typedef struct {
+  int64_t x, delta, B, C, z, y;
+} ssm_row_strides_t;
+
+/*
+ * ssm_causal_conv1d_fwd over packed prompts.
+ *   x, y     (total, dim) dtype, rows strided;  weight, bias as there
+ *   cache    (slots, dim, width-1) dtype: the windows, oldest input first;
+ *            NULL: every sequence starts from zeros and no window is stored
+ *   strides  NULL: contiguous rows
+ * The spans of y and the cache must not overlap an input's or each other's
+ * (from the first to the last element).  No sequence reads another's rows.
+ * Bandwidth-bound: x is read once and y written once.
+ */
+SSM_API ssm_status_t ssm_causal_conv1d_packed_fwd(const ssm_packed_t *seqs, int64_t dim, int64_t width,
+                                                  ssm_dtype_t dtype, const void *x, const float *weight,
+                                                  const float *bias, int silu, void *y, const ssm_cache_t *cache,
+                                                  const ssm_row_strides_t *strides, void *stream);
+
+/*
+ * ssm_scan_fwd over packed prompts.
+ *   x, delta, z, y  (total, dim) dtype, rows strided; z may be NULL
+ *   B, C            (total, dstate) dtype, rows strided
+ *   A, D, delta_bias, delta_softplus as in ssm_scan_fwd
+ *   cache           (slots, dim, dstate) fp32 or bf16: the states; NULL: every
+ *                   sequence starts from zeros and no state is stored
+ *   workspace       of at least ssm_scan_packed_workspace bytes, 16-byte
+ *                   aligned, the caller's until the call's work is done (each
+ *                   call that may run at the same time needs its own); may be
+ *                   NULL where that is 0
+ * Tensors need their element's alignment only; rows that allow 16-byte access
+ * are faster.  The spans of y, the cache and the workspace must not overlap
+ * an input's or each other's.  Values of one sequence, NaN and infinity
+ * included, never reach another.
+ */
+SSM_API ssm_status_t ssm_scan_packed_fwd(const ssm_packed_t *seqs, int64_t dim, int64_t dstate, ssm_dtype_t dtype,
+                                         const void *x, const void *delta, const float *A, const void *B,
+                                         const void *C, const float *D, const void *z, const float *delta_bias,
+                                         int delta_softplus, void *y, const ssm_cache_t *cache,
+                                         const ssm_row_strides_t *strides, void *workspace, int64_t workspace_bytes,
+                                         void *stream);
+
+/* Bytes of workspace that ssm_scan_packed_fwd needs for these sizes (total,
+ * sequences and max_seqlen of seqs, whose pointers are not read), on the
+ * current device.  Long prompts that are too few to fill the device are cut
+ * into pieces scanned in parallel, whose states go there; 0 when none are. */
+SSM_API ssm_status_t ssm_scan_packed_workspace(const ssm_packed_t *seqs, int64_t dim, int64_t dstate,
+                                               ssm_dtype_t dtype, int64_t *bytes);
+
+/*
+ * ssm_causal_conv1d_update, ssm_state_update and ssm_ssd_state_update on a
+ * cache: one token of `batch` sequences, entry i on slot cache_slots[i] (int32
+ * on the device; NULL: slot i), which is read and updated in place.  An entry
+ * with no slot is skipped: its row of y is left as it was.
+ *   conv   cache (slots, dim, width-1) dtype (may be NULL when width == 1);
+ *          x, y (batch, dim), rows strided
+ *   scan   cache (slots, dim, dstate) fp32 or bf16; x, delta, z, y (batch,
+ *          dim), B, C (batch, dstate), rows strided
+ *   SSD    cache (slots, nheads, headdim, dstate) fp32 or bf16; x, z, y (batch,
+ *          nheads, headdim), dt (batch, nheads), B, C (batch, ngroups, dstate),
+ *          rows strided; dtype fp32 or bf16, dstate 16, 32, 64, 128 or 256
+ */
+SSM_API ssm_status_t ssm_causal_conv1d_update_cache(int64_t batch, int64_t dim, int64_t width, ssm_dtype_t dtype,
+                                                    const ssm_cache_t *cache, const int32_t *cache_slots,
+                                                    const void *x, const float *weight, const float *bias, int silu,
+                                                    void *y, const ssm_row_strides_t *strides, void *stream);
+SSM_API ssm_status_t ssm_state_update_cache(int64_t batch, int64_t dim, int64_t dstate, ssm_dtype_t dtype,
+                                            const ssm_cache_t *cache, const int32_t *cache_slots, const void *x,
+                                            const void *delta, const float *A, const void *B, const void *C,
+                                            const float *D, const void *z, const float *delta_bias,
+                                            int delta_softplus, void *y, const ssm_row_strides_t *strides,
+                                            void *stream);
+SSM_API ssm_status_t ssm_ssd_state_update_cache(int64_t batch, int64_t nheads, int64_t headdim, int64_t dstate,
+                                                int64_t ngroups, ssm_dtype_t dtype, const ssm_cache_t *cache,
+                                                const int32_t *cache_slots, const void *x, const void *dt,
+                                                const float *A, const void *B, const void *C, const float *D,
+                                                const void *z, const float *dt_bias, int dt_softplus, void *y,
+                                                const ssm_row_strides_t *strides, void *stream);
+
+/*
+ * States set aside in 8 bits: the states of slots whose sequence waits (a
+ * shared prompt prefix, a preempted sequence), stored as int8 codes with one
+ * fp32 scale per row of dstate values, and read back into a cache.  For a row
+ * v of the cache's slot:
+ *
+ *   scale = max_n |v[n]| / 127, rounded to fp32
+ *   code[n] = v[n] / scale, the exact quotient rounded to the nearest integer
+ *             (ties to even), within -127..127; 0 where scale is 0
+ *   read back: code[n] * scale, rounded to fp32 (and to bf16 for such a cache)
+ *
+ * so a value is off by at most scale / 2 (and that rounding).  A row that
+ * holds a NaN or an infinity gets the scale NaN and reads back as NaN.  It is
+ * a form to keep states in, not to step them in: rounding every step to 8
+ * bits would stop slow decays.
+ *
+ *   cache   (slots, rows, dstate) fp32 or bf16; rows is dim, or nheads *
+ *           headdim; dstate 1, 2, 4, ..., 256 (a power of two)
+ *   codes   (stored, rows, dstate) int8, scales (stored, rows) fp32: contiguous
+ *   pair i of `count` is cache slot cache_slots[i] and stored entry
+ *   store_slots[i] (int32 on the device; NULL: i); a pair whose slot or entry
+ *   is out of range is skipped.  The written slots (entries) must differ; the
+ *   ones read may repeat, so that several sequences start from one entry.
+ */
+SSM_API ssm_status_t ssm_cache_store_q8(int64_t count, int64_t rows, int64_t dstate, const ssm_cache_t *cache,
+                                        const int32_t *cache_slots, int64_t stored, int8_t *codes, float *scales,
+                                        const int32_t *store_slots, void *stream);
+SSM_API ssm_status_t ssm_cache_load_q8(int64_t count, int64_t rows, int64_t dstate, int64_t stored,
+                                       const int8_t *codes, const float *scales, const int32_t *store_slots,
+                                       const ssm_cache_t *cache, const int32_t *cache_slots, void *stream);
+
 /* Static string naming a status code ("SSM_OK", ...); never NULL. */
 SSM_API const char *ssm_status_string(ssm_status_t status);
 

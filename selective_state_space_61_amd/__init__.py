@@ -13,6 +13,9 @@ every call raises: there is no fallback implementation.
 Shapes: x, delta, z (batch, seqlen, dim); A (dim, dstate) fp32; B, C (batch, seqlen, dstate);
 D, delta_bias (dim,) fp32; y like x; last_state / state (batch, dim, dstate) fp32.  x, delta, B, C,
 z and y share one dtype: torch.float32 or torch.bfloat16.
+
+For serving (packed prompts, single tokens on a cache of slots, states set aside in 8 bits) see
+``serving.py``, whose functions this module exports too.
 """
 from __future__ import annotations
 
@@ -31,7 +34,10 @@ STATUS_NAMES = {0: "SSM_OK", 1: "SSM_ERR_INVALID_ARG", 2: "SSM_ERR_UNSUPPORTED",
 EXPORTED = ("ssm_scan_fwd", "ssm_scan_fwd_ex", "ssm_scan_fwd_noalloc", "ssm_scan_fwd_ckpt", "ssm_scan_bwd",
             "ssm_scan_bwd_ex", "ssm_scan_bwd_ckpt", "ssm_state_update", "ssm_state_update_ex",
             "ssm_causal_conv1d_fwd",
-            "ssm_causal_conv1d_update", "ssm_ssd_fwd", "ssm_ssd_state_update", "ssm_status_string", "ssm_last_error", "ssm_abi_version")
+            "ssm_causal_conv1d_update", "ssm_ssd_fwd", "ssm_ssd_state_update", "ssm_status_string", "ssm_last_error", "ssm_abi_version",
+            "ssm_causal_conv1d_packed_fwd", "ssm_scan_packed_fwd", "ssm_scan_packed_workspace",
+            "ssm_causal_conv1d_update_cache", "ssm_state_update_cache", "ssm_ssd_state_update_cache",
+            "ssm_cache_store_q8", "ssm_cache_load_q8")
 
 
 class SsmError(RuntimeError):
@@ -57,6 +63,20 @@ class BwdOpts(ctypes.Structure):
 class SsdOpts(ctypes.Structure):
     _fields_ = [("head_slice", ctypes.c_int32), ("segments", ctypes.c_int32), ("gram", ctypes.c_int32),
                 ("reserved", ctypes.c_int32 * 5)]
+
+
+class Cache(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("slots", ctypes.c_int64), ("slot_stride", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class Packed(ctypes.Structure):
+    _fields_ = [("total", ctypes.c_int64), ("sequences", ctypes.c_int64), ("max_seqlen", ctypes.c_int64),
+                ("cu_seqlens", ctypes.c_void_p), ("cache_slots", ctypes.c_void_p), ("has_initial", ctypes.c_void_p)]
+
+
+class RowStrides(ctypes.Structure):
+    _fields_ = [(k, ctypes.c_int64) for k in ("x", "delta", "B", "C", "z", "y")]
 
 
 SSM_BBAR_DELTA_B, SSM_BBAR_ZOH = 0, 1
@@ -106,6 +126,20 @@ def load_library(path: str = LIBRARY) -> ctypes.CDLL:
     lib.ssm_ssd_fwd.restype = i32
     lib.ssm_ssd_state_update.argtypes = [i64, i64, i64, i64, i64, i32, vp, vp, vp, vp, vp, vp, vp, vp, vp, i32, vp, vp]
     lib.ssm_ssd_state_update.restype = i32
+    cache, packed, strides = (ctypes.POINTER(t) for t in (Cache, Packed, RowStrides))
+    lib.ssm_causal_conv1d_packed_fwd.argtypes = [packed, i64, i64, i32, vp, vp, vp, i32, vp, cache, strides, vp]
+    lib.ssm_scan_packed_fwd.argtypes = [packed, i64, i64, i32, vp, vp, vp, vp, vp, vp, vp, vp, i32, vp, cache, strides,
+                                        vp, i64, vp]
+    lib.ssm_scan_packed_workspace.argtypes = [packed, i64, i64, i32, ctypes.POINTER(i64)]
+    lib.ssm_causal_conv1d_update_cache.argtypes = [i64, i64, i64, i32, cache, vp, vp, vp, vp, i32, vp, strides, vp]
+    lib.ssm_state_update_cache.argtypes = [i64, i64, i64, i32, cache, vp, vp, vp, vp, vp, vp, vp, vp, vp, i32, vp,
+                                           strides, vp]
+    lib.ssm_ssd_state_update_cache.argtypes = [i64, i64, i64, i64, i64, i32, cache, vp, vp, vp, vp, vp, vp, vp, vp, vp,
+                                               i32, vp, strides, vp]
+    lib.ssm_cache_store_q8.argtypes = [i64, i64, i64, cache, vp, i64, vp, vp, vp, vp]
+    lib.ssm_cache_load_q8.argtypes = [i64, i64, i64, i64, vp, vp, vp, cache, vp, vp]
+    for name in EXPORTED[-8:]:
+        getattr(lib, name).restype = i32
     lib.ssm_status_string.argtypes = [i32]
     lib.ssm_status_string.restype = ctypes.c_char_p
     lib.ssm_last_error.argtypes = []
@@ -489,7 +523,14 @@ def abi_version() -> int:
     return load_library().ssm_abi_version()
 
 
+from .serving import (ssm_cache_load_q8, ssm_cache_store_q8, ssm_causal_conv1d_packed_fwd,  # noqa: E402
+                      ssm_causal_conv1d_update_cache, ssm_scan_packed_fwd, ssm_scan_packed_workspace,
+                      ssm_ssd_state_update_cache, ssm_state_update_cache)
+
 __all__ = ["ssm_scan_fwd", "ssm_scan_bwd", "ssm_state_update", "ssm_causal_conv1d_fwd", "ssm_causal_conv1d_update",
            "ssm_ssd_fwd", "ssm_ssd_state_update", "SsdOpts", "BwdOpts", "abi_version", "load_library", "SsmError", "ScanOpts", "UpdateOpts",
            "ssm_scan_fwd_ckpt", "ssm_scan_bwd_ckpt", "checkpoint_shape",
+           "ssm_causal_conv1d_packed_fwd", "ssm_scan_packed_fwd", "ssm_scan_packed_workspace",
+           "ssm_causal_conv1d_update_cache", "ssm_state_update_cache", "ssm_ssd_state_update_cache",
+           "ssm_cache_store_q8", "ssm_cache_load_q8",
            "LIBRARY", "EXPORTED"]

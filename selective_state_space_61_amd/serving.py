@@ -1,0 +1,359 @@
+"""Serving calls of the binding: prompts packed one behind another, single tokens on a cache of
+slots, and cached states set aside in 8 bits (include/ssm.h, "Serving").
+
+    y = ssm_causal_conv1d_packed_fwd(x, weight, cu_seqlens, bias, cache=windows, cache_slots=slots)
+    y = ssm_scan_packed_fwd(x, delta, A, B, C, cu_seqlens, D=D, z=z, cache=states, cache_slots=slots)
+    y = ssm_causal_conv1d_update_cache(windows, slots, x, weight, bias)
+    y = ssm_state_update_cache(states, slots, x, delta, A, B, C, D=D, z=z)
+    y = ssm_ssd_state_update_cache(states, slots, x, dt, A, B, C, D=D, z=z)
+    ssm_cache_store_q8(states, slots, codes, scales, entries)
+    ssm_cache_load_q8(codes, scales, entries, states, slots)
+
+Sequence s of a packed tensor is its rows cu_seqlens[s] .. cu_seqlens[s + 1] - 1; cu_seqlens,
+cache_slots and the entries are int32, has_initial bool or uint8, all on the tensors' device.
+cache_slots None: sequence (entry) i has slot i.  A negative slot is the padding of a batch: a step
+leaves that entry's row of y as it was, a prompt starts from zeros and stores no state.  Caches are
+(slots, dim, dstate) and the like, fp32 or bf16, updated in place; x, delta, B, C, z, dt and y are
+rows that may lie apart (columns of a wider tensor), each row contiguous.  A call allocates only
+what it returns, and the packed scan its workspace when none is passed in; both on the stream that
+it runs on, so that calls may be captured into a graph.
+"""
+from __future__ import annotations
+
+import contextlib
+import ctypes
+from typing import Optional
+
+import torch
+
+from . import (SSM_BF16, SSM_F32, Cache, Packed, RowStrides, _check, _dtype_code, _need, _ptr, _stream, load_library)
+
+
+def _row_stride(t: torch.Tensor, name: str, shape, dtype, device) -> int:
+    """Elements between the rows of t (0 for at most one row), whose rows must be contiguous."""
+    if t is None:
+        raise ValueError(f"{name} is required")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.is_contiguous():
+        return 0
+    width = 1
+    for n, s in zip(reversed(shape[1:]), reversed(t.stride()[1:])):
+        if n > 1 and s != width:
+            raise ValueError(f"the rows of {name} must be contiguous")
+        width *= n
+    if shape[0] <= 1:
+        return 0
+    if t.stride(0) < width:
+        raise ValueError(f"the rows of {name} must not overlap")
+    return t.stride(0)
+
+
+def _cache(t: Optional[torch.Tensor], name: str, entry, device, dtype=None) -> Cache:
+    """The cache's descriptor: (slots,) + entry, each slot contiguous."""
+    if t is None:
+        raise ValueError(f"{name} is required")
+    if t.dim() != 1 + len(entry) or tuple(t.shape[1:]) != tuple(entry):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected (slots, {', '.join(map(str, entry))})")
+    if t.dtype not in (torch.float32, torch.bfloat16) or (dtype is not None and t.dtype != dtype):
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype or 'float32 or bfloat16'}")
+    stride = _row_stride(t, name, t.shape, t.dtype, device)
+    return Cache(t.data_ptr(), t.shape[0], stride, SSM_BF16 if t.dtype == torch.bfloat16 else SSM_F32, 0)
+
+
+def _indices(t: Optional[torch.Tensor], name: str, count: int, device, slots: int) -> None:
+    if t is None:
+        if slots < count:
+            raise ValueError(f"without {name} there must be at least {count} slots, not {slots}")
+        return
+    _need(t, name, (count,), torch.int32, device)
+
+
+def _packed(cu_seqlens, cache_slots, has_initial, total: int, slots: Optional[int], max_seqlen: int, device) -> Packed:
+    if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
+        raise ValueError("cu_seqlens must hold one more entry than there are sequences")
+    nseq = cu_seqlens.numel() - 1
+    _need(cu_seqlens, "cu_seqlens", (nseq + 1,), torch.int32, device)
+    if slots is None:
+        if cache_slots is not None or has_initial is not None:
+            raise ValueError("cache_slots and has_initial need a cache")
+    else:
+        _indices(cache_slots, "cache_slots", nseq, device, slots)
+    if has_initial is not None:
+        if has_initial.dtype not in (torch.bool, torch.uint8):
+            raise TypeError(f"has_initial has dtype {has_initial.dtype}, expected bool or uint8")
+        _need(has_initial, "has_initial", (nseq,), has_initial.dtype, device)
+    return Packed(total, nseq, int(max_seqlen), cu_seqlens.data_ptr(), _ptr(cache_slots), _ptr(has_initial))
+
+
+@contextlib.contextmanager
+def _other(device: torch.device, stream):
+    """The tensors' device current, and the given stream, where they are not already."""
+    with torch.cuda.device(device):
+        if stream is None:
+            yield
+            return
+        if not hasattr(stream, "cuda_stream"):
+            stream = (torch.cuda.ExternalStream(int(stream), device=device) if int(stream)
+                      else torch.cuda.default_stream(device))
+        with torch.cuda.stream(stream):
+            yield
+
+
+def _run(call, device: torch.device, stream):
+    """call() with the tensors' device current and, when one is given, on that stream: what it
+    allocates then belongs to the stream that uses it."""
+    if device.type != "cuda":
+        raise ValueError(f"the tensors are on {device}, expected a GPU")
+    if stream is None and torch.cuda.current_device() == device.index:
+        return call()
+    with _other(device, stream):
+        return call()
+
+
+def ssm_causal_conv1d_packed_fwd(x: torch.Tensor, weight: torch.Tensor, cu_seqlens: torch.Tensor,
+                                 bias: Optional[torch.Tensor] = None, silu: bool = True, *,
+                                 cache: Optional[torch.Tensor] = None, cache_slots: Optional[torch.Tensor] = None,
+                                 has_initial: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None,
+                                 stream=None) -> torch.Tensor:
+    """The causal convolution of every packed sequence (include/ssm.h: ssm_causal_conv1d_packed_fwd).
+    x, y: (total, dim); weight: (dim, width) fp32; bias: (dim,) fp32; cache: (slots, dim, width - 1) in
+    x's dtype or None.  Returns y; rows of no sequence are left as they were (as allocated)."""
+    lib = load_library()
+    if x.dim() != 2 or weight.dim() != 2:
+        raise ValueError("x must be (total, dim) and weight (dim, width)")
+    total, dim = x.shape
+    width = weight.shape[1]
+    dev, dt = x.device, x.dtype
+    code = _dtype_code(x)
+    strides = RowStrides(x=_row_stride(x, "x", x.shape, dt, dev))
+    _need(weight, "weight", (dim, width), torch.float32, dev)
+    _need(bias, "bias", (dim,), torch.float32, dev, optional=True)
+    ref = _cache(cache, "cache", (dim, width - 1), dev, dt) if cache is not None else None
+    seqs = _packed(cu_seqlens, cache_slots, has_initial, total, None if ref is None else ref.slots, 0, dev)
+    if y is not None:
+        strides.y = _row_stride(y, "y", x.shape, dt, dev)
+
+    def call():
+        out = torch.empty((total, dim), dtype=dt, device=dev) if y is None else y
+        _check(lib.ssm_causal_conv1d_packed_fwd(seqs, dim, width, code, x.data_ptr(), weight.data_ptr(), _ptr(bias),
+                                                int(bool(silu)), out.data_ptr(), ref, strides, _stream(dev, stream)))
+        return out
+
+    return _run(call, dev, stream)
+
+
+def ssm_scan_packed_workspace(total: int, sequences: int, max_seqlen: int, dim: int, dstate: int,
+                              dtype: torch.dtype) -> int:
+    """Bytes of workspace of ssm_scan_packed_fwd for these sizes, on the current device."""
+    lib = load_library()
+    n = ctypes.c_int64(0)
+    _check(lib.ssm_scan_packed_workspace(Packed(total, sequences, max_seqlen, None, None, None), dim, dstate,
+                                         SSM_BF16 if dtype == torch.bfloat16 else SSM_F32, ctypes.byref(n)))
+    return n.value
+
+
+def ssm_scan_packed_fwd(x: torch.Tensor, delta: torch.Tensor, A: torch.Tensor, B: torch.Tensor, C: torch.Tensor,
+                        cu_seqlens: torch.Tensor, D: Optional[torch.Tensor] = None, z: Optional[torch.Tensor] = None,
+                        delta_bias: Optional[torch.Tensor] = None, delta_softplus: bool = False, *,
+                        cache: Optional[torch.Tensor] = None, cache_slots: Optional[torch.Tensor] = None,
+                        has_initial: Optional[torch.Tensor] = None, max_seqlen: int = 0,
+                        y: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                        stream=None) -> torch.Tensor:
+    """The selective scan of every packed sequence (include/ssm.h: ssm_scan_packed_fwd).  x, delta, z, y:
+    (total, dim); B, C: (total, dstate); A: (dim, dstate) fp32; D, delta_bias: (dim,) fp32; cache: (slots,
+    dim, dstate) fp32 or bf16, or None.  max_seqlen (the longest sequence; 0: not known) only chooses the
+    launch shape.  workspace: a uint8 tensor of ssm_scan_packed_workspace bytes, allocated here when None.
+    Returns y; rows of no sequence are left as they were (as allocated)."""
+    lib = load_library()
+    if x.dim() != 2 or A.dim() != 2:
+        raise ValueError("x must be (total, dim) and A (dim, dstate)")
+    total, dim = x.shape
+    dstate = A.shape[1]
+    dev, dt = x.device, x.dtype
+    code = _dtype_code(x)
+    bc = (total, dstate)
+    strides = RowStrides(_row_stride(x, "x", x.shape, dt, dev), _row_stride(delta, "delta", x.shape, dt, dev),
+                         _row_stride(B, "B", bc, dt, dev), _row_stride(C, "C", bc, dt, dev),
+                         0 if z is None else _row_stride(z, "z", x.shape, dt, dev),
+                         0 if y is None else _row_stride(y, "y", x.shape, dt, dev))
+    _need(A, "A", (dim, dstate), torch.float32, dev)
+    _need(D, "D", (dim,), torch.float32, dev, optional=True)
+    _need(delta_bias, "delta_bias", (dim,), torch.float32, dev, optional=True)
+    ref = _cache(cache, "cache", (dim, dstate), dev) if cache is not None else None
+    seqs = _packed(cu_seqlens, cache_slots, has_initial, total, None if ref is None else ref.slots, max_seqlen, dev)
+    if workspace is not None:
+        _need(workspace, "workspace", (workspace.numel(),), torch.uint8, dev)
+
+    def call():
+        out = torch.empty((total, dim), dtype=dt, device=dev) if y is None else y
+        ws = workspace
+        if ws is None:
+            n = ctypes.c_int64(0)
+            _check(lib.ssm_scan_packed_workspace(seqs, dim, dstate, code, ctypes.byref(n)))
+            ws = torch.empty(n.value, dtype=torch.uint8, device=dev) if n.value else None
+        _check(lib.ssm_scan_packed_fwd(seqs, dim, dstate, code, x.data_ptr(), delta.data_ptr(), A.data_ptr(),
+                                       B.data_ptr(), C.data_ptr(), _ptr(D), _ptr(z), _ptr(delta_bias),
+                                       int(bool(delta_softplus)), out.data_ptr(), ref, strides, _ptr(ws),
+                                       0 if ws is None else ws.numel(), _stream(dev, stream)))
+        return out
+
+    return _run(call, dev, stream)
+
+
+def ssm_causal_conv1d_update_cache(cache: Optional[torch.Tensor], cache_slots: Optional[torch.Tensor],
+                                   x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] = None,
+                                   silu: bool = True, *, y: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """One token of the convolution on a cache (include/ssm.h: ssm_causal_conv1d_update_cache).  cache:
+    (slots, dim, width - 1) in x's dtype, updated in place; x, y: (batch, dim).  Returns y."""
+    lib = load_library()
+    if x.dim() != 2 or weight.dim() != 2:
+        raise ValueError("x must be (batch, dim) and weight (dim, width)")
+    batch, dim = x.shape
+    width = weight.shape[1]
+    dev, dt = x.device, x.dtype
+    code = _dtype_code(x)
+    strides = RowStrides(x=_row_stride(x, "x", x.shape, dt, dev))
+    _need(weight, "weight", (dim, width), torch.float32, dev)
+    _need(bias, "bias", (dim,), torch.float32, dev, optional=True)
+    ref = None
+    if cache is not None or width != 1:
+        ref = _cache(cache, "cache", (dim, width - 1), dev, dt)
+    _indices(cache_slots, "cache_slots", batch, dev, batch if ref is None else ref.slots)
+    if y is not None:
+        strides.y = _row_stride(y, "y", x.shape, dt, dev)
+
+    def call():
+        out = torch.empty((batch, dim), dtype=dt, device=dev) if y is None else y
+        _check(lib.ssm_causal_conv1d_update_cache(batch, dim, width, code, ref, _ptr(cache_slots), x.data_ptr(),
+                                                  weight.data_ptr(), _ptr(bias), int(bool(silu)), out.data_ptr(),
+                                                  strides, _stream(dev, stream)))
+        return out
+
+    return _run(call, dev, stream)
+
+
+def ssm_state_update_cache(cache: torch.Tensor, cache_slots: Optional[torch.Tensor], x: torch.Tensor,
+                           delta: torch.Tensor, A: torch.Tensor, B: torch.Tensor, C: torch.Tensor,
+                           D: Optional[torch.Tensor] = None, z: Optional[torch.Tensor] = None,
+                           delta_bias: Optional[torch.Tensor] = None, delta_softplus: bool = False, *,
+                           y: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """One token of the selective scan on a cache (include/ssm.h: ssm_state_update_cache).  cache: (slots,
+    dim, dstate) fp32 or bf16, updated in place; x, delta, z, y: (batch, dim); B, C: (batch, dstate).
+    Returns y."""
+    lib = load_library()
+    if x.dim() != 2 or A.dim() != 2:
+        raise ValueError("x must be (batch, dim) and A (dim, dstate)")
+    batch, dim = x.shape
+    dstate = A.shape[1]
+    dev, dt = x.device, x.dtype
+    code = _dtype_code(x)
+    bc = (batch, dstate)
+    strides = RowStrides(_row_stride(x, "x", x.shape, dt, dev), _row_stride(delta, "delta", x.shape, dt, dev),
+                         _row_stride(B, "B", bc, dt, dev), _row_stride(C, "C", bc, dt, dev),
+                         0 if z is None else _row_stride(z, "z", x.shape, dt, dev),
+                         0 if y is None else _row_stride(y, "y", x.shape, dt, dev))
+    _need(A, "A", (dim, dstate), torch.float32, dev)
+    _need(D, "D", (dim,), torch.float32, dev, optional=True)
+    _need(delta_bias, "delta_bias", (dim,), torch.float32, dev, optional=True)
+    ref = _cache(cache, "cache", (dim, dstate), dev)
+    _indices(cache_slots, "cache_slots", batch, dev, ref.slots)
+
+    def call():
+        out = torch.empty((batch, dim), dtype=dt, device=dev) if y is None else y
+        _check(lib.ssm_state_update_cache(batch, dim, dstate, code, ref, _ptr(cache_slots), x.data_ptr(),
+                                          delta.data_ptr(), A.data_ptr(), B.data_ptr(), C.data_ptr(), _ptr(D),
+                                          _ptr(z), _ptr(delta_bias), int(bool(delta_softplus)), out.data_ptr(),
+                                          strides, _stream(dev, stream)))
+        return out
+
+    return _run(call, dev, stream)
+
+
+def ssm_ssd_state_update_cache(cache: torch.Tensor, cache_slots: Optional[torch.Tensor], x: torch.Tensor,
+                               dt: torch.Tensor, A: torch.Tensor, B: torch.Tensor, C: torch.Tensor,
+                               D: Optional[torch.Tensor] = None, z: Optional[torch.Tensor] = None,
+                               dt_bias: Optional[torch.Tensor] = None, dt_softplus: bool = False, *,
+                               y: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """One token of the Mamba-2 SSD layer on a cache (include/ssm.h: ssm_ssd_state_update_cache).  cache:
+    (slots, nheads, headdim, dstate) fp32 or bf16, updated in place; x, z, y: (batch, nheads, headdim);
+    dt: (batch, nheads); B, C: (batch, ngroups, dstate); A, D, dt_bias: (nheads,) fp32.  Returns y."""
+    lib = load_library()
+    if x.dim() != 3 or B.dim() != 3:
+        raise ValueError("x must be (batch, nheads, headdim) and B (batch, ngroups, dstate)")
+    batch, nheads, headdim = x.shape
+    ngroups, dstate = B.shape[1], B.shape[2]
+    dev, ty = x.device, x.dtype
+    code = _dtype_code(x)
+    strides = RowStrides(_row_stride(x, "x", x.shape, ty, dev), _row_stride(dt, "dt", (batch, nheads), ty, dev),
+                         _row_stride(B, "B", B.shape, ty, dev), _row_stride(C, "C", B.shape, ty, dev),
+                         0 if z is None else _row_stride(z, "z", x.shape, ty, dev),
+                         0 if y is None else _row_stride(y, "y", x.shape, ty, dev))
+    _need(A, "A", (nheads,), torch.float32, dev)
+    _need(D, "D", (nheads,), torch.float32, dev, optional=True)
+    _need(dt_bias, "dt_bias", (nheads,), torch.float32, dev, optional=True)
+    ref = _cache(cache, "cache", (nheads, headdim, dstate), dev)
+    _indices(cache_slots, "cache_slots", batch, dev, ref.slots)
+
+    def call():
+        out = torch.empty((batch, nheads, headdim), dtype=ty, device=dev) if y is None else y
+        _check(lib.ssm_ssd_state_update_cache(batch, nheads, headdim, dstate, ngroups, code, ref, _ptr(cache_slots),
+                                              x.data_ptr(), dt.data_ptr(), A.data_ptr(), B.data_ptr(), C.data_ptr(),
+                                              _ptr(D), _ptr(z), _ptr(dt_bias), int(bool(dt_softplus)),
+                                              out.data_ptr(), strides, _stream(dev, stream)))
+        return out
+
+    return _run(call, dev, stream)
+
+
+def _q8(cache, cache_slots, codes, scales, store_slots):
+    """(cache descriptor, pairs, rows, dstate, stored entries) of a store or load, checked.  The cache's
+    entries are (rows, dstate) or (nheads, headdim, dstate)."""
+    if cache.dim() not in (3, 4):
+        raise ValueError("cache must be (slots, dim, dstate) or (slots, nheads, headdim, dstate)")
+    dev = cache.device
+    entry = tuple(cache.shape[1:])
+    ref = _cache(cache, "cache", entry, dev)
+    stored = codes.shape[0]
+    _need(codes, "codes", (stored,) + entry, torch.int8, dev)
+    _need(scales, "scales", (stored,) + entry[:-1], torch.float32, dev)
+    if cache_slots is None and store_slots is None:
+        count = min(ref.slots, stored)
+    else:
+        count = (cache_slots if cache_slots is not None else store_slots).numel()
+    _indices(cache_slots, "cache_slots", count, dev, ref.slots)
+    _indices(store_slots, "store_slots", count, dev, stored)
+    rows = 1
+    for n in entry[:-1]:
+        rows *= n
+    return ref, count, rows, entry[-1], stored
+
+
+def ssm_cache_store_q8(cache: torch.Tensor, cache_slots: Optional[torch.Tensor], codes: torch.Tensor,
+                       scales: torch.Tensor, store_slots: Optional[torch.Tensor] = None, *, stream=None) -> None:
+    """Sets the states of cache_slots aside as int8 codes with one scale per row of dstate values, in the
+    entries store_slots of codes and scales (include/ssm.h: ssm_cache_store_q8).  cache: (slots, dim,
+    dstate) or (slots, nheads, headdim, dstate); codes: (stored,) + a slot's shape, int8; scales: the same
+    without dstate, fp32.  Without either index pair i is slot i and entry i."""
+    lib = load_library()
+    ref, count, rows, dstate, stored = _q8(cache, cache_slots, codes, scales, store_slots)
+    dev = cache.device
+    _run(lambda: _check(lib.ssm_cache_store_q8(count, rows, dstate, ref, _ptr(cache_slots), stored, codes.data_ptr(),
+                                               scales.data_ptr(), _ptr(store_slots), _stream(dev, stream))),
+         dev, stream)
+
+
+def ssm_cache_load_q8(codes: torch.Tensor, scales: torch.Tensor, store_slots: Optional[torch.Tensor],
+                      cache: torch.Tensor, cache_slots: Optional[torch.Tensor] = None, *, stream=None) -> None:
+    """Reads entries store_slots of codes and scales back into cache_slots of the cache (include/ssm.h:
+    ssm_cache_load_q8); an entry may be read into several slots."""
+    lib = load_library()
+    ref, count, rows, dstate, stored = _q8(cache, cache_slots, codes, scales, store_slots)
+    dev = cache.device
+    _run(lambda: _check(lib.ssm_cache_load_q8(count, rows, dstate, stored, codes.data_ptr(), scales.data_ptr(),
+                                              _ptr(store_slots), ref, _ptr(cache_slots), _stream(dev, stream))),
+         dev, stream)
