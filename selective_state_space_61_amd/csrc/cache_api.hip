@@ -2,6 +2,8 @@
 // slots, states set aside in 8 bits): host-side validation, launch shapes and launches.
 #include <hip/hip_runtime.h>
 
+#include <cmath>
+
 #include "../../include/ssm.h"
 #include "cache_q8.hpp"
 #include "cache_step.hpp"
@@ -48,9 +50,8 @@ ssm_status_t check_rows(Rows* r, size_t n, int64_t rows, int64_t es) {
   return SSM_OK;
 }
 
-// The cache's fields, its entries of `entry` elements.  piece: bytes that a lane reads at a
-// multiple of them from the entry's start.
-ssm_status_t check_cache(const ssm_cache_t* c, int64_t entry, int64_t piece, ssm::CacheRef* ref, Range* range) {
+// The cache's fields, its entries of `entry` elements
+ssm_status_t check_cache(const ssm_cache_t* c, int64_t entry, ssm::CacheRef* ref, Range* range) {
   if (c->reserved != 0) return fail(SSM_ERR_INVALID_ARG, "ssm_cache_t.reserved must be zero");
   if (c->dtype != SSM_F32 && c->dtype != SSM_BF16)
     return fail(SSM_ERR_UNSUPPORTED, "unknown cache dtype %d", (int)c->dtype);
@@ -69,7 +70,6 @@ ssm_status_t check_cache(const ssm_cache_t* c, int64_t entry, int64_t piece, ssm
   ref->data = c->data;
   ref->slots = c->slots;
   ref->stride = stride;
-  ref->vec_ok = aligned(c->data, static_cast<uintptr_t>(piece)) && (stride * es) % piece == 0;
   *range = {c->data, bytes};
   return SSM_OK;
 }
@@ -107,10 +107,6 @@ ssm_status_t check_overlap(const Range* outs, size_t n_out, const Range* ins, si
 template <size_t N>
 constexpr size_t count_of(const Range (&)[N]) {
   return N;
-}
-
-bool rows_allow(const void* p, int64_t stride, int64_t es, int64_t bytes) {
-  return aligned(p, static_cast<uintptr_t>(bytes)) && (stride * es) % bytes == 0;
 }
 
 ssm_row_strides_t strides_or_zero(const ssm_row_strides_t* s) { return s ? *s : ssm_row_strides_t{}; }
@@ -166,11 +162,6 @@ template <bool BF16, bool CB16, int N>
 struct SsdStep {
   static auto get() { return &ssm::ssd_state_update_cache_kernel<BF16, CB16, N>; }
 };
-template <bool BF16, bool CB16, int N>
-struct ScanPacked {
-  static auto get() { return &ssm::scan_packed_kernel<BF16, CB16, N>; }
-};
-
 using Q8Kernel = void (*)(const ssm::Q8Args);
 template <bool CB16>
 Q8Kernel q8_kernel(bool store, int64_t n) {
@@ -207,8 +198,7 @@ ssm_status_t q8_call(bool store, int64_t count, int64_t rows, int64_t dstate, co
     return fail(SSM_ERR_INVALID_ARG, "tensor size overflows int64");
   ssm::Q8Args a{};
   Range rc;
-  SSM_TRY(check_cache(cache, entry, cb16 ? (dstate < 8 ? dstate * 2 : 16) : (dstate < 4 ? dstate * 4 : 16), &a.cache,
-                      &rc));
+  SSM_TRY(check_cache(cache, entry, &a.cache, &rc));
   if (count == 0 || rows == 0 || stored == 0 || cache->slots == 0) return SSM_OK;
   if (!codes || !scales) return fail(SSM_ERR_INVALID_ARG, "NULL codes or scales");
   if (!aligned(scales, 4) || !aligned(cache_slots, 4) || !aligned(store_slots, 4))
@@ -223,7 +213,6 @@ ssm_status_t q8_call(bool store, int64_t count, int64_t rows, int64_t dstate, co
   if (blocks > kMaxBlocks) return fail(SSM_ERR_UNSUPPORTED, "grid too large");
   a.cache_slots = cache_slots; a.codes = codes; a.scales = scales; a.store_slots = store_slots;
   a.stored = stored; a.count = count; a.rows = rows;
-  a.codes_vec_ok = aligned(codes, 4) && dstate % 4 == 0;
   hipLaunchKernelGGL(k, dim3(static_cast<unsigned>(blocks), grid_y(count)), dim3(ssm::kQ8Threads), 0,
                      static_cast<hipStream_t>(stream), a);
   return check_launch(store ? "cache store (8 bits)" : "cache load (8 bits)");
@@ -235,8 +224,67 @@ ssm_status_t check_scan_packed(const ssm_packed_t* seqs, int64_t dim, int64_t ds
   if (dim < 0 || dstate < 0)
     return fail(SSM_ERR_INVALID_ARG, "negative size (dim=%lld dstate=%lld)", (long long)dim, (long long)dstate);
   if (dtype != SSM_F32 && dtype != SSM_BF16) return fail(SSM_ERR_UNSUPPORTED, "unknown dtype %d", (int)dtype);
-  if (dstate < 1 || dstate > 64 || (dstate & (dstate - 1)) != 0)
+  if (!ssm::scan_packed_kernels(dtype == SSM_BF16, dstate))
     return fail(SSM_ERR_UNSUPPORTED, "dstate %lld not in {1,2,4,8,16,32,64}", (long long)dstate);
+  return SSM_OK;
+}
+
+// Launch shape of the packed scan: rows per piece (0: whole sequences), the bound on the pieces of
+// all sequences and the workspace that they need.
+struct ScanPackedShape {
+  int64_t piece, pieces, ncb, floats;
+};
+
+// Rows per piece (0: whole sequences), by a model of the two launches from what was measured on MI355X
+// (dstate 16, bf16; other dstates by the factor `scale`): a wave alone on its SIMD takes 84 ns a row
+// and waves that share one 65 ns each (full pass), 60 and 50 ns without read-outs; the second launch
+// and the pieces' set-up take 9 us; composing the states of 8 pieces takes 2 us.  Both sides,
+// whole | in pieces of the chosen length, in us: one sequence of 8192 x 1536: 678 | 96; of 512: 47 | 19;
+// 11 ragged ones of 11003 x 1536: 224 | 120; 16 of 512 x 1536: 74 | 77 (whole is chosen); 32 of 2048 x
+// 1536: 395 | 606 (whole).
+int64_t scan_packed_piece(int64_t total, int64_t sequences, int64_t longest, int64_t waves, int64_t dstate) {
+  const double simds = 4.0 * device_cus();
+  const double scale = 0.45 + 0.55 * static_cast<double>(dstate) / 16.0;
+  const double rows = static_cast<double>(total) * static_cast<double>(waves) / simds;  // per SIMD
+  // time of a pass over pieces of `length` rows, `n` of them in all
+  auto pass = [&](double length, double n, double alone, double shared) {
+    const double per_simd = n * static_cast<double>(waves) / simds;
+    // pieces of about one length that all run at once take as long as the SIMD with the most of them
+    const bool even = n * length < 1.2 * static_cast<double>(total) && per_simd <= 4.0;
+    const double queue = even ? length * std::ceil(per_simd) : rows + 0.5 * length;
+    const double busy = per_simd <= 1.0 ? 0.0 : shared * queue;
+    return scale * (busy > alone * length ? busy : alone * length);
+  };
+  double best = pass(static_cast<double>(longest), static_cast<double>(sequences), 0.084, 0.065);
+  int64_t piece = 0;
+  for (int64_t p : {32, 48, 64, 96, 128, 160, 192, 256, 384, 512, 768, 1024}) {
+    if (p >= longest) break;
+    const double n = sequences == 1 ? static_cast<double>((total + p - 1) / p)
+                                    : static_cast<double>(total) / p + 0.5 * sequences;
+    const double length = static_cast<double>(p);
+    const double t = pass(length, n, 0.084, 0.065) + pass(length, n, 0.060, 0.050) + 9.0 +
+                     2.0 * static_cast<double>(longest) / (8.0 * length);
+    if (t < best) {
+      best = t;
+      piece = p;
+    }
+  }
+  return piece;
+}
+
+ssm_status_t scan_packed_shape(const ssm_packed_t* seqs, int64_t dim, int64_t dstate, ssm_dtype_t dtype,
+                               ScanPackedShape* out) {
+  const int64_t ncb = (dim + 16 * ssm::kPackedWaves - 1) / (16 * ssm::kPackedWaves);
+  const int64_t longest =
+      seqs->max_seqlen > 0 && seqs->max_seqlen < seqs->total ? seqs->max_seqlen : seqs->total;
+  const int64_t piece = scan_packed_piece(seqs->total, seqs->sequences, longest, (dim + 15) / 16, dstate);
+  out->piece = piece;
+  out->ncb = ncb;
+  out->pieces = piece ? seqs->total / piece + seqs->sequences : seqs->sequences;
+  out->floats = 0;
+  if (piece && (!mul_ok(out->pieces, dim, &out->floats) || !mul_ok(out->floats, (dstate + 1) * 4, &out->floats)))
+    return fail(SSM_ERR_INVALID_ARG, "workspace size overflows int64");
+  out->floats /= 4;
   return SSM_OK;
 }
 
@@ -261,7 +309,7 @@ ssm_status_t ssm_causal_conv1d_packed_fwd(const ssm_packed_t* seqs, int64_t dim,
   Range rc{nullptr, 0};
   if (cache) {
     if (cache->dtype != dtype) return fail(SSM_ERR_INVALID_ARG, "the cache's dtype differs from x's");
-    SSM_TRY(check_cache(cache, entry, es, &a.cache, &rc));
+    SSM_TRY(check_cache(cache, entry, &a.cache, &rc));
   }
   ssm_row_strides_t rs = strides_or_zero(strides);
   Rows t[] = {{x, dim, &rs.x, "x", 0}, {y, dim, &rs.y, "y", 0}};
@@ -281,7 +329,6 @@ ssm_status_t ssm_causal_conv1d_packed_fwd(const ssm_packed_t* seqs, int64_t dim,
   a.cu = seqs->cu_seqlens; a.slots = seqs->cache_slots; a.has_initial = seqs->has_initial;
   a.total = seqs->total; a.nseq = seqs->sequences; a.dim = dim; a.sx = rs.x; a.sy = rs.y;
   a.silu = silu ? 1 : 0;
-  a.vec_ok = rows_allow(x, rs.x, es, ssm::kConvVecBytes) && rows_allow(y, rs.y, es, ssm::kConvVecBytes);
   const int64_t ncv = (dim + vec - 1) / vec;
   const int64_t ncb = (ncv + ssm::kConvThreads - 1) / ssm::kConvThreads;
   const int64_t ntiles = (seqs->total + ssm::kPackTile - 1) / ssm::kPackTile;
@@ -301,6 +348,10 @@ ssm_status_t ssm_scan_packed_workspace(const ssm_packed_t* seqs, int64_t dim, in
   if (!bytes) return fail(SSM_ERR_INVALID_ARG, "NULL bytes");
   SSM_TRY(check_scan_packed(seqs, dim, dstate, dtype));
   *bytes = 0;
+  if (seqs->total == 0 || seqs->sequences == 0 || dim == 0) return SSM_OK;
+  ScanPackedShape shape;
+  SSM_TRY(scan_packed_shape(seqs, dim, dstate, dtype, &shape));
+  *bytes = shape.floats * 4;
   return SSM_OK;
 }
 
@@ -318,7 +369,7 @@ ssm_status_t ssm_scan_packed_fwd(const ssm_packed_t* seqs, int64_t dim, int64_t 
   ssm::ScanPackedArgs a{};
   Range rc{nullptr, 0};
   const bool cb16 = cache && cache->dtype == SSM_BF16;
-  if (cache) SSM_TRY(check_cache(cache, entry, (dstate < 4 ? dstate : 4) * (cb16 ? 2 : 4), &a.cache, &rc));
+  if (cache) SSM_TRY(check_cache(cache, entry, &a.cache, &rc));
   ssm_row_strides_t rs = strides_or_zero(strides);
   Rows t[] = {{x, dim, &rs.x, "x", 0},        {delta, dim, &rs.delta, "delta", 0}, {B, dstate, &rs.B, "B", 0},
               {C, dstate, &rs.C, "C", 0},     {z, dim, &rs.z, "z", 0},             {y, dim, &rs.y, "y", 0}};
@@ -330,24 +381,46 @@ ssm_status_t ssm_scan_packed_fwd(const ssm_packed_t* seqs, int64_t dim, int64_t 
   SSM_TRY(check_packed_pointers(seqs, idx));
   if (!aligned(A, 4) || !aligned(D, 4) || !aligned(delta_bias, 4))
     return fail(SSM_ERR_MISALIGNED, "A, D or delta_bias is not 4-byte aligned");
-  const Range outs[] = {{y, t[5].bytes}, rc};
+  for (const Rows& r : t)
+    if (*r.stride >= ssm::kScanPackedMaxStride)
+      return fail(SSM_ERR_UNSUPPORTED, "row stride %lld of %s is not below 2^24", (long long)*r.stride, r.name);
+  ScanPackedShape shape;
+  SSM_TRY(scan_packed_shape(seqs, dim, dstate, dtype, &shape));
+  if (shape.floats > 0) {
+    if (!workspace || workspace_bytes < shape.floats * 4)
+      return fail(SSM_ERR_INVALID_ARG, "workspace of %lld bytes, %lld are needed",
+                  (long long)(workspace ? workspace_bytes : 0), (long long)(shape.floats * 4));
+    if (!aligned(workspace, 16)) return fail(SSM_ERR_MISALIGNED, "workspace (%p) is not 16-byte aligned", workspace);
+  }
+  const Range outs[] = {{y, t[5].bytes}, rc, {workspace, shape.floats * 4}};
   const Range ins[] = {{x, t[0].bytes}, {delta, t[1].bytes}, {B, t[2].bytes}, {C, t[3].bytes}, {z, t[4].bytes},
                        {A, n_dn},       {D, dim * 4},        {delta_bias, dim * 4}, idx[0], idx[1], idx[2]};
   SSM_TRY(check_overlap(outs, count_of(outs), ins, count_of(ins)));
-  (void)workspace; (void)workspace_bytes;
 
   a.x = x; a.delta = delta; a.A = A; a.B = B; a.C = C; a.Dskip = D; a.z = z; a.delta_bias = delta_bias; a.y = y;
   a.cu = seqs->cu_seqlens; a.slots = seqs->cache_slots; a.has_initial = seqs->has_initial;
   a.total = seqs->total; a.nseq = seqs->sequences; a.dim = dim;
   a.sx = rs.x; a.sdelta = rs.delta; a.sB = rs.B; a.sC = rs.C; a.sz = rs.z; a.sy = rs.y;
   a.softplus = delta_softplus ? 1 : 0;
-  if (seqs->sequences > 65535) return fail(SSM_ERR_UNSUPPORTED, "more than 65535 sequences");
-  const int64_t spt = dstate < 4 ? dstate : 4;
-  const int64_t blocks = (dim * (dstate / spt) + ssm::kScanSimpleThreads - 1) / ssm::kScanSimpleThreads;
-  if (blocks > kMaxBlocks) return fail(SSM_ERR_UNSUPPORTED, "grid too large");
-  const auto k = by_dstate<ScanPacked, 1, 2, 4, 8, 16, 32, 64>(dtype == SSM_BF16, cb16, dstate);
-  hipLaunchKernelGGL(k, dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(seqs->sequences)),
-                     dim3(ssm::kScanSimpleThreads), 0, static_cast<hipStream_t>(stream), a);
+  a.cache_bf16 = cb16 ? 1 : 0;
+  a.piece = static_cast<int32_t>(shape.piece);
+  a.pieces = shape.pieces;
+  a.ncb = static_cast<int32_t>(shape.ncb);
+  if (shape.piece) {
+    a.seg_state = static_cast<float*>(workspace);
+    a.seg_dsum = a.seg_state + shape.pieces * dim * dstate;
+  }
+  int64_t blocks;
+  if (!mul_ok(shape.pieces, shape.ncb, &blocks) || blocks > kMaxBlocks)
+    return fail(SSM_ERR_UNSUPPORTED, "grid of %lld x %lld workgroups is too large", (long long)shape.pieces,
+                (long long)shape.ncb);
+  const ssm::ScanPackedKernels& k = *ssm::scan_packed_kernels(dtype == SSM_BF16, dstate);
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  if (shape.piece) {
+    hipLaunchKernelGGL(k.agg, dim3(static_cast<unsigned>(blocks)), dim3(64 * ssm::kPackedWaves), 0, st, a);
+    SSM_TRY(check_launch("scan (packed, pieces' states)"));
+  }
+  hipLaunchKernelGGL(k.full, dim3(static_cast<unsigned>(blocks)), dim3(64 * ssm::kPackedWaves), 0, st, a);
   return check_launch("scan (packed)");
 }
 
@@ -370,7 +443,7 @@ ssm_status_t ssm_causal_conv1d_update_cache(int64_t batch, int64_t dim, int64_t 
   Range rc{nullptr, 0};
   if (width > 1) {
     if (cache->dtype != dtype) return fail(SSM_ERR_INVALID_ARG, "the cache's dtype differs from x's");
-    SSM_TRY(check_cache(cache, entry, dtype == SSM_BF16 ? 8 : 16, &a.cache, &rc));
+    SSM_TRY(check_cache(cache, entry, &a.cache, &rc));
   }
   ssm_row_strides_t rs = strides_or_zero(strides);
   Rows t[] = {{x, dim, &rs.x, "x", 0}, {y, dim, &rs.y, "y", 0}};
@@ -384,8 +457,6 @@ ssm_status_t ssm_causal_conv1d_update_cache(int64_t batch, int64_t dim, int64_t 
   SSM_TRY(check_overlap(outs, count_of(outs), ins, count_of(ins)));
   a.slots = cache_slots; a.x = x; a.weight = weight; a.bias = bias; a.y = y;
   a.batch = batch; a.dim = dim; a.sx = rs.x; a.sy = rs.y; a.silu = silu ? 1 : 0;
-  const int64_t vb = ssm::kConvStepVec * es;
-  a.vec_ok = rows_allow(x, rs.x, es, vb) && rows_allow(y, rs.y, es, vb);
   const int64_t per = static_cast<int64_t>(ssm::kStepThreads) * ssm::kConvStepVec;
   const int64_t blocks = (dim + per - 1) / per;
   if (blocks > kMaxBlocks) return fail(SSM_ERR_UNSUPPORTED, "grid too large");
@@ -416,7 +487,7 @@ ssm_status_t ssm_state_update_cache(int64_t batch, int64_t dim, int64_t dstate, 
     return fail(SSM_ERR_INVALID_ARG, "tensor size overflows int64");
   ssm::StepArgs a{};
   Range rc;
-  SSM_TRY(check_cache(cache, entry, spt * (cb16 ? 2 : 4), &a.cache, &rc));
+  SSM_TRY(check_cache(cache, entry, &a.cache, &rc));
   ssm_row_strides_t rs = strides_or_zero(strides);
   Rows t[] = {{x, dim, &rs.x, "x", 0},    {delta, dim, &rs.delta, "delta", 0}, {B, dstate, &rs.B, "B", 0},
               {C, dstate, &rs.C, "C", 0}, {z, dim, &rs.z, "z", 0},             {y, dim, &rs.y, "y", 0}};
@@ -434,10 +505,6 @@ ssm_status_t ssm_state_update_cache(int64_t batch, int64_t dim, int64_t dstate, 
   a.delta_bias = delta_bias; a.y = y; a.batch = batch; a.dim = dim;
   a.sx = rs.x; a.sdelta = rs.delta; a.sB = rs.B; a.sC = rs.C; a.sz = rs.z; a.sy = rs.y;
   a.softplus = delta_softplus ? 1 : 0;
-  // pieces of a lane's states: 16 bytes of A, up to 16 bytes of B and C
-  a.a_vec_ok = aligned(A, 16);
-  const int64_t bcb = spt * es < 16 ? spt * es : 16;
-  a.bc_vec_ok = rows_allow(B, rs.B, es, bcb) && rows_allow(C, rs.C, es, bcb);
   const int64_t blocks = (dim * (dstate / spt) + ssm::kStepThreads - 1) / ssm::kStepThreads;
   if (blocks > kMaxBlocks) return fail(SSM_ERR_UNSUPPORTED, "grid too large");
   hipLaunchKernelGGL(k, dim3(static_cast<unsigned>(blocks), grid_y(batch)), dim3(ssm::kStepThreads), 0,
@@ -471,7 +538,7 @@ ssm_status_t ssm_ssd_state_update_cache(int64_t batch, int64_t nheads, int64_t h
     return fail(SSM_ERR_INVALID_ARG, "tensor size overflows int64");
   ssm::SsdStepArgs a{};
   Range rc;
-  SSM_TRY(check_cache(cache, entry, 16, &a.cache, &rc));
+  SSM_TRY(check_cache(cache, entry, &a.cache, &rc));
   ssm_row_strides_t rs = strides_or_zero(strides);
   Rows t[] = {{x, width, &rs.x, "x", 0}, {dt, nheads, &rs.delta, "dt", 0}, {B, bc, &rs.B, "B", 0},
               {C, bc, &rs.C, "C", 0},    {z, width, &rs.z, "z", 0},        {y, width, &rs.y, "y", 0}};
@@ -490,8 +557,6 @@ ssm_status_t ssm_ssd_state_update_cache(int64_t batch, int64_t nheads, int64_t h
   a.nheads = static_cast<int32_t>(nheads); a.headdim = static_cast<int32_t>(headdim);
   a.ngroups = static_cast<int32_t>(ngroups); a.softplus = dt_softplus ? 1 : 0;
   const int64_t spt = cb16 ? 8 : 4;
-  const int64_t bcb = spt * es < 16 ? spt * es : 16;
-  a.bc_vec_ok = rows_allow(B, rs.B, es, bcb) && rows_allow(C, rs.C, es, bcb);
   const int64_t per = ssm::kSsdStepUnroll * ssm::kStepThreads * spt / dstate;
   const int64_t chunks = (headdim + per - 1) / per;
   int64_t blocks;

@@ -24,7 +24,6 @@ struct Q8Args {
   int64_t stored;
   int64_t count;
   int64_t rows;
-  int32_t codes_vec_ok;
 };
 
 constexpr int kQ8Threads = 256;
@@ -45,18 +44,16 @@ __device__ __forceinline__ float q8_code(float v, float scale, float inv) {
 
 // NV codes, the lowest byte first
 template <int NV>
-__device__ __forceinline__ void store_codes(int8_t* p, const int (&q)[NV], bool vec) {
+__device__ __forceinline__ void store_codes(int8_t* p, const int (&q)[NV]) {
   if constexpr (NV % 4 == 0) {
-    if (vec) {
 #pragma unroll
-      for (int i = 0; i < NV / 4; ++i)
-        reinterpret_cast<uint32_t*>(p)[i] = (q[4 * i] & 0xff) | (q[4 * i + 1] & 0xff) << 8 | (q[4 * i + 2] & 0xff) << 16 |
-                                            static_cast<uint32_t>(q[4 * i + 3]) << 24;
-      return;
-    }
+    for (int i = 0; i < NV / 4; ++i)
+      reinterpret_cast<Words<1>::U1*>(p)[i] = (q[4 * i] & 0xff) | (q[4 * i + 1] & 0xff) << 8 | (q[4 * i + 2] & 0xff) << 16 |
+                                              static_cast<uint32_t>(q[4 * i + 3]) << 24;
+  } else {
+#pragma unroll
+    for (int v = 0; v < NV; ++v) p[v] = static_cast<int8_t>(q[v]);
   }
-#pragma unroll
-  for (int v = 0; v < NV; ++v) p[v] = static_cast<int8_t>(q[v]);
 }
 
 template <bool CB16, int N>
@@ -72,7 +69,7 @@ __global__ __launch_bounds__(kQ8Threads) void cache_store_q8_kernel(const Q8Args
     const int64_t to = p.store_slots ? p.store_slots[i] : i;
     if (at < 0 || to < 0 || to >= p.stored) continue;
     Run<CB16, V, true> r;
-    r.load(p.cache.data, at + row * N + n0, p.cache.vec_ok);
+    r.load(p.cache.data, at + row * N + n0);
     // |v| as bits: their order is the values', with infinity and then NaN above every number
     uint32_t top = 0;
 #pragma unroll
@@ -99,7 +96,7 @@ __global__ __launch_bounds__(kQ8Threads) void cache_store_q8_kernel(const Q8Args
     }
     if (ok) {
       const int64_t o = (to * p.rows + row) * N + n0;
-      store_codes<V>(p.codes + o, q, p.codes_vec_ok);
+      store_codes<V>(p.codes + o, q);
       if (n0 == 0) p.scales[to * p.rows + row] = scale;
     }
   }
@@ -119,26 +116,20 @@ __global__ __launch_bounds__(kQ8Threads) void cache_load_q8_kernel(const Q8Args 
     const int8_t* c = p.codes + (from * p.rows + row) * N + n0;
     const float scale = p.scales[from * p.rows + row];
     float val[V];
-    bool done = false;
     if constexpr (V % 4 == 0) {
-      if (p.codes_vec_ok) {
 #pragma unroll
-        for (int k = 0; k < V / 4; ++k) {
-          const uint32_t w = reinterpret_cast<const uint32_t*>(c)[k];
+      for (int k = 0; k < V / 4; ++k) {
+        const uint32_t w = reinterpret_cast<const Words<1>::U1*>(c)[k];
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            val[4 * k + j] = static_cast<float>(static_cast<int8_t>(w >> (8 * j))) * scale;
-        }
-        done = true;
+        for (int j = 0; j < 4; ++j) val[4 * k + j] = static_cast<float>(static_cast<int8_t>(w >> (8 * j))) * scale;
       }
-    }
-    if (!done) {
+    } else {
 #pragma unroll
       for (int v = 0; v < V; ++v) val[v] = static_cast<float>(c[v]) * scale;
     }
     Run<CB16, V, true> r;
     r.set(val);
-    r.store(p.cache.data, at + row * N + n0, p.cache.vec_ok);
+    r.store(p.cache.data, at + row * N + n0);
   }
 }
 

@@ -30,8 +30,6 @@ struct StepArgs {
   int64_t dim;
   int64_t sx, sdelta, sB, sC, sz, sy;  // elements between rows
   int32_t softplus;
-  int32_t a_vec_ok;   // A allows 16-byte access
-  int32_t bc_vec_ok;  // rows of B and C allow 16-byte access
 };
 
 // A thread owns SPT consecutive states of a channel (16 bytes), N / SPT lanes a channel.
@@ -44,7 +42,7 @@ __global__ __launch_bounds__(kStepThreads) void state_update_cache_kernel(const 
   const int64_t d = ok ? t / TPC : p.dim - 1;
   const int n0 = static_cast<int>(t % TPC) * SPT;
   Run<false, SPT> a;
-  a.load(p.A, d * N + n0, p.a_vec_ok);
+  a.load(p.A, d * N + n0);
   const float bias = p.delta_bias ? p.delta_bias[d] : 0.0f;
   const float dsk = p.Dskip ? p.Dskip[d] : 0.0f;
   for (int64_t b = blockIdx.y; b < p.batch; b += gridDim.y) {
@@ -52,9 +50,9 @@ __global__ __launch_bounds__(kStepThreads) void state_update_cache_kernel(const 
     if (at < 0) continue;
     Run<CB16, SPT, true> st;
     Run<BF16, SPT> bv, cv;
-    st.load(p.cache.data, at + d * N + n0, p.cache.vec_ok);
-    bv.load(p.B, b * p.sB + n0, p.bc_vec_ok);
-    cv.load(p.C, b * p.sC + n0, p.bc_vec_ok);
+    st.load(p.cache.data, at + d * N + n0);
+    bv.load(p.B, b * p.sB + n0);
+    cv.load(p.C, b * p.sC + n0);
     const float xv = load_one<BF16>(p.x, b * p.sx + d);
     const float vb = load_one<BF16>(p.delta, b * p.sdelta + d) + bias;
     const float zv = p.z ? load_one<BF16>(p.z, b * p.sz + d) : 0.0f;
@@ -67,7 +65,7 @@ __global__ __launch_bounds__(kStepThreads) void state_update_cache_kernel(const 
       yp = fmaf(cv.get(j), h[j], yp);
     }
     st.set(h);
-    if (ok) st.store(p.cache.data, at + d * N + n0, p.cache.vec_ok);
+    if (ok) st.store(p.cache.data, at + d * N + n0);
 #pragma unroll
     for (int off = 1; off < TPC; off <<= 1) yp += __shfl_xor(yp, off, 64);
     if (ok && n0 == 0) {
@@ -89,7 +87,6 @@ struct ConvStepArgs {
   int64_t dim;
   int64_t sx, sy;
   int32_t silu;
-  int32_t vec_ok;  // rows of x and y allow a thread's whole vector
 };
 
 constexpr int kConvStepVec = 4;  // channels per thread
@@ -108,8 +105,8 @@ __global__ __launch_bounds__(kStepThreads) void conv1d_update_cache_kernel(const
     if (nv == V) {
       Run<BF16, V> xr;
       Run<BF16, V * W + (W == 0)> win;
-      xr.load(p.x, b * p.sx + d0, p.vec_ok);
-      if constexpr (W > 0) win.load(p.cache.data, at + d0 * W, p.cache.vec_ok);
+      xr.load(p.x, b * p.sx + d0);
+      if constexpr (W > 0) win.load(p.cache.data, at + d0 * W);
       float out[V], keep[V * W + (W == 0)];
 #pragma unroll
       for (int v = 0; v < V; ++v) {
@@ -124,10 +121,10 @@ __global__ __launch_bounds__(kStepThreads) void conv1d_update_cache_kernel(const
       }
       Run<BF16, V> yr;
       yr.set(out);
-      yr.store(p.y, b * p.sy + d0, p.vec_ok);
+      yr.store(p.y, b * p.sy + d0);
       if constexpr (W > 0) {
         win.set(keep);
-        win.store(p.cache.data, at + d0 * W, p.cache.vec_ok);
+        win.store(p.cache.data, at + d0 * W);
       }
       continue;
     }
@@ -164,7 +161,6 @@ struct SsdStepArgs {
   int32_t nheads, headdim, ngroups;
   int32_t chunks;  // workgroups per head
   int32_t softplus;
-  int32_t bc_vec_ok;
 };
 
 // channels of a head that one workgroup takes: U per 16-byte state access of its four waves
@@ -201,13 +197,13 @@ __global__ __launch_bounds__(kStepThreads) void ssd_state_update_cache_kernel(co
       ok[u] = pc < P;
       const int64_t c = static_cast<int64_t>(h) * P + (ok[u] ? pc : 0);
       off[u] = at + c * N + n0;
-      st[u].load(p.cache.data, off[u], p.cache.vec_ok);
+      st[u].load(p.cache.data, off[u]);
       xv[u] = load_one<BF16>(p.x, b * p.sx + c);
       zv[u] = p.z ? load_one<BF16>(p.z, b * p.sz + c) : 0.0f;
     }
     Run<BF16, SPT> bv, cv;
-    bv.load(p.B, b * p.sB + static_cast<int64_t>(g) * N + n0, p.bc_vec_ok);
-    cv.load(p.C, b * p.sC + static_cast<int64_t>(g) * N + n0, p.bc_vec_ok);
+    bv.load(p.B, b * p.sB + static_cast<int64_t>(g) * N + n0);
+    cv.load(p.C, b * p.sC + static_cast<int64_t>(g) * N + n0);
     const float v = load_one<BF16>(p.dt, b * p.sdt + h) + bias;
     const float dtv = p.softplus ? softplus_f32(v) : v;
     const float a = hw_exp2(dtv * al);
@@ -221,7 +217,7 @@ __global__ __launch_bounds__(kStepThreads) void ssd_state_update_cache_kernel(co
         yp = fmaf(cv.get(j), s[j], yp);
       }
       st[u].set(s);
-      if (ok[u]) st[u].store(p.cache.data, off[u], p.cache.vec_ok);
+      if (ok[u]) st[u].store(p.cache.data, off[u]);
 #pragma unroll
       for (int o = 1; o < TPC; o <<= 1) yp += __shfl_xor(yp, o, 64);
       if (ok[u] && n0 == 0) {

@@ -33,7 +33,6 @@ struct ConvPackedArgs {
   int64_t sx, sy;
   int32_t ncb;  // workgroups per tile
   int32_t silu;
-  int32_t vec_ok;
 };
 
 constexpr int kPackTile = 32;
@@ -47,7 +46,6 @@ __global__ __launch_bounds__(kConvThreads) void conv1d_packed_kernel(const ConvP
   const int64_t t1 = t0 + T < p.total ? t0 + T : p.total;
   // lanes without channels (nv 0) take part in the search for sequences
   const int nv = d0 >= p.dim ? 0 : static_cast<int>(p.dim - d0 < V ? p.dim - d0 : V);
-  const bool vec = p.vec_ok != 0 && nv == V;
   float w[K][V], bias[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) {
@@ -65,9 +63,8 @@ __global__ __launch_bounds__(kConvThreads) void conv1d_packed_kernel(const ConvP
 #pragma unroll
       for (int j = 0; j < W; ++j) {
         const int64_t s = row - W + j;  // row of the sequence; negative: of the slot's window
-        RawVec<BF16, V> q;
-        q.zero();
-        if (s >= 0) q.load(p.x, (o.start + s) * p.sx + d0, nv, vec);
+        Run<BF16, V> q;
+        q.load_some(p.x, (o.start + (s >= 0 ? s : 0)) * p.sx + d0, s >= 0 ? nv : 0);
 #pragma unroll
         for (int v = 0; v < V; ++v) {
           win[j][v] = q.get(v);
@@ -86,9 +83,8 @@ __global__ __launch_bounds__(kConvThreads) void conv1d_packed_kernel(const ConvP
 #pragma unroll
       for (int j = 0; j < W; ++j) {
         const int64_t s = len - W + j;
-        RawVec<BF16, V> q;
-        q.zero();
-        if (s >= 0) q.load(p.x, (o.start + s) * p.sx + d0, nv, vec);
+        Run<BF16, V> q;
+        q.load_some(p.x, (o.start + (s >= 0 ? s : 0)) * p.sx + d0, s >= 0 ? nv : 0);
 #pragma unroll
         for (int v = 0; v < V; ++v) {
           fin[j][v] = q.get(v);
@@ -119,10 +115,13 @@ __global__ __launch_bounds__(kConvThreads) void conv1d_packed_kernel(const ConvP
     take_window(own, t - own.start);
     if (t == own.start) leave_window(own);
     for (; t < end; t += kConvUnroll) {
-      RawVec<BF16, V> r[kConvUnroll];
+      Run<BF16, V> r[kConvUnroll];
 #pragma unroll
-      for (int u = 0; u < kConvUnroll; ++u)
-        r[u].load(p.x, (t + u < end ? t + u : end - 1) * p.sx + d0, nv, vec);
+      for (int u = 0; u < kConvUnroll; ++u) {
+        const int64_t at = (t + u < end ? t + u : end - 1) * p.sx + d0;
+        if (nv == V) r[u].load(p.x, at);
+        else r[u].load_some(p.x, at, nv);
+      }
 #pragma unroll
       for (int u = 0; u < kConvUnroll; ++u) {
         if (t + u >= end) break;
@@ -139,8 +138,10 @@ __global__ __launch_bounds__(kConvThreads) void conv1d_packed_kernel(const ConvP
           for (int j = 0; j + 1 < W; ++j) win[j][v] = win[j + 1][v];
           if constexpr (W > 0) win[W - 1][v] = xv;
         }
-        if (vec) store_row_stream<BF16>(p.y, (t + u) * p.sy + d0, out);
-        else store_vec<BF16, V>(p.y, (t + u) * p.sy + d0, out, nv, false);
+        Run<BF16, V, true> o;  // written once and read by the next kernel
+        o.set(out);
+        if (nv == V) o.store(p.y, (t + u) * p.sy + d0);
+        else o.store_some(p.y, (t + u) * p.sy + d0, nv);
       }
     }
     t = end;
