@@ -155,29 +155,101 @@ struct Run {
   }
 };
 
-// The sequence of packed row t: `start` and `end` its rows (within 0..total, whatever cu holds),
-// s its index, or -1 where the row is of none; then `end` is the first row that may be of one.
-// Every lane of a wave calls it with the same t: 64 lanes compare 64 entries of cu at a time and
-// count those not above t, so up to 63 sequences take one load.
+// A reduction over groups of LANES neighbouring lanes (a power of two), its result in every lane:
+// DPP within a row of 16 (quad permutations, half-row and row mirrors), lane swaps across rows.  All
+// of it VALU work; the shuffles through the LDS that it replaces set the pace of the 8-bit store.
+template <int LANES, typename T, typename F>
+__device__ __forceinline__ T group_reduce(T v, F op) {
+  static_assert(sizeof(T) == 4 && LANES >= 1 && LANES <= 64 && (LANES & (LANES - 1)) == 0, "lanes of a wave");
+  auto dpp = [&](auto CTRL) {
+    return __builtin_bit_cast(T, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), decltype(CTRL)::value, 0xF, 0xF, true));
+  };
+  if constexpr (LANES >= 2) v = op(v, dpp(std::integral_constant<int, 0xB1>{}));    // lane ^ 1
+  if constexpr (LANES >= 4) v = op(v, dpp(std::integral_constant<int, 0x4E>{}));    // lane ^ 2
+  if constexpr (LANES >= 8) v = op(v, dpp(std::integral_constant<int, 0x141>{}));   // the other half of 8
+  if constexpr (LANES >= 16) v = op(v, dpp(std::integral_constant<int, 0x140>{}));  // the other half of 16
+  auto swapped = [&](auto q) {
+    const uint32_t a = q[0], b = q[1];
+    return op(__builtin_bit_cast(T, a), __builtin_bit_cast(T, b));
+  };
+  if constexpr (LANES >= 32) {
+    const uint32_t u = __builtin_bit_cast(uint32_t, v);
+    v = swapped(__builtin_amdgcn_permlane16_swap(u, u, false, false));
+  }
+  if constexpr (LANES >= 64) {
+    const uint32_t u = __builtin_bit_cast(uint32_t, v);
+    v = swapped(__builtin_amdgcn_permlane32_swap(u, u, false, false));
+  }
+  return v;
+}
+
+template <int LANES>
+__device__ __forceinline__ float group_sum(float v) {
+  return group_reduce<LANES>(v, [](float a, float b) { return a + b; });
+}
+
+// The sequence of a packed row: `start` and `end` its rows (within 0..total, whatever cu holds), s its
+// index, or -1 where the row is of none.
 struct RowOwner {
   int64_t s, start, end;
 };
-__device__ __forceinline__ RowOwner row_owner(const int32_t* cu, int64_t nseq, int64_t total, int64_t t) {
-  const int lane = threadIdx.x & 63;
-  int64_t n = 0;
-  for (int64_t i = 0; i <= nseq; i += 64) {
-    const bool in = i + lane <= nseq && cu[i + lane] <= t;
-    n += __popcll(__ballot(in));
+
+// The sequences from row t on, 64 of them at a time in a wave's registers: entry s0 + lane of cu, its slot
+// and its flag.  Every lane of the wave makes the same calls, with rows that do not fall.
+class Sequences {
+ public:
+  __device__ __forceinline__ Sequences(const int32_t* cu, const int32_t* slots, const uint8_t* has_initial,
+                                       int64_t nseq, int64_t total, int64_t t)
+      : cu_(cu), slots_(slots), has_initial_(has_initial), nseq_(nseq), total_(total), s0_(0) {
+    const int lane = threadIdx.x & 63;
+    int64_t n = 0;  // entries not above t: 64 compared at a time
+    for (int64_t i = 0; i <= nseq; i += 64) n += __popcll(__ballot(i + lane <= nseq && cu[i + lane] <= t));
+    read(n > 0 ? n - 1 : 0);
   }
-  RowOwner r;
-  r.s = n - 1;
-  // with n == nseq + 1 the row lies behind the last sequence
-  r.start = n > 0 ? cu[n - 1] : 0;
-  r.end = n <= nseq ? cu[n] : total;
-  if (n > nseq) r.s = -1;
-  r.start = r.start < 0 ? 0 : (r.start > t ? t : r.start);
-  r.end = r.end <= t ? t + 1 : (r.end > total ? total : r.end);
-  return r;
-}
+
+  __device__ __forceinline__ RowOwner owner(int64_t t) {
+    int c = not_above(t);
+    while (c == 64) {  // (ends: entries past nseq are above every row)
+      read(s0_ + 63);
+      c = not_above(t);
+    }
+    RowOwner r;
+    const int64_t s = s0_ + c - 1;
+    // with none the row lies before the first sequence, with all nseq + 1 behind the last
+    r.s = c > 0 && s < nseq_ ? s : -1;
+    r.start = c > 0 ? __builtin_amdgcn_readlane(entry_, c - 1) : 0;
+    r.end = s < nseq_ ? __builtin_amdgcn_readlane(entry_, c) : total_;
+    r.start = r.start < 0 ? 0 : (r.start > t ? t : r.start);
+    r.end = r.end <= t ? t + 1 : (r.end > total_ ? total_ : r.end);
+    return r;
+  }
+
+  // first element of the slot of sequence s (one that owner() gave last), -1: none
+  __device__ __forceinline__ int64_t slot_offset(const CacheRef& c, int64_t s) const {
+    const int64_t slot = slots_ ? __builtin_amdgcn_readlane(slot_, static_cast<int>(s - s0_)) : s;
+    return slot >= 0 && slot < c.slots ? slot * c.stride : -1;
+  }
+  __device__ __forceinline__ bool initial(int64_t s) const {
+    return __builtin_amdgcn_readlane(flag_, static_cast<int>(s - s0_)) != 0;
+  }
+
+ private:
+  __device__ __forceinline__ int not_above(int64_t t) const {
+    return __popcll(__ballot(static_cast<int64_t>(entry_) <= t));
+  }
+  __device__ __forceinline__ void read(int64_t s0) {
+    s0_ = s0;
+    const int64_t i = s0 + (threadIdx.x & 63);
+    entry_ = i <= nseq_ ? cu_[i] : INT32_MAX;
+    slot_ = slots_ && i < nseq_ ? slots_[i] : -1;
+    flag_ = has_initial_ && i < nseq_ ? has_initial_[i] : 0;
+  }
+  const int32_t* cu_;
+  const int32_t* slots_;
+  const uint8_t* has_initial_;
+  int64_t nseq_, total_, s0_;
+  int32_t entry_, slot_;
+  int32_t flag_;
+};
 
 }  // namespace ssm

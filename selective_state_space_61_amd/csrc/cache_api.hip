@@ -67,7 +67,7 @@ ssm_status_t check_cache(const ssm_cache_t* c, int64_t entry, ssm::CacheRef* ref
     return fail(SSM_ERR_MISALIGNED, "cache (%p) is not aligned to its element size", c->data);
   const int64_t bytes = span_bytes(c->slots, stride, entry, es);
   if (bytes < 0) return fail(SSM_ERR_INVALID_ARG, "tensor size overflows int64");
-  ref->data = c->data;
+  ref->data = c->slots > 0 ? c->data : nullptr;
   ref->slots = c->slots;
   ref->stride = stride;
   *range = {c->data, bytes};
@@ -111,6 +111,12 @@ constexpr size_t count_of(const Range (&)[N]) {
 
 ssm_row_strides_t strides_or_zero(const ssm_row_strides_t* s) { return s ? *s : ssm_row_strides_t{}; }
 
+// Entries of a batch that a thread of a step takes: several once that leaves a few workgroups per CU.
+constexpr int kStepEntries = 4;
+int step_entries(int64_t blocks, int64_t batch) {
+  return blocks * ((batch + kStepEntries - 1) / kStepEntries) >= device_cus() ? kStepEntries : 1;
+}
+
 // rows of a batch along gridDim.y, whose limit the kernels' loops step over
 unsigned grid_y(int64_t rows) { return static_cast<unsigned>(rows < 65535 ? rows : 65535); }
 
@@ -121,25 +127,25 @@ unsigned grid_y(int64_t rows) { return static_cast<unsigned>(rows < 65535 ? rows
   } while (0)
 
 using ConvPackedKernel = void (*)(const ssm::ConvPackedArgs);
-template <bool BF16>
+template <bool BF16, int T>
 ConvPackedKernel conv_packed_kernel(int64_t width) {
   switch (width) {
-    case 1: return ssm::conv1d_packed_kernel<BF16, 1>;
-    case 2: return ssm::conv1d_packed_kernel<BF16, 2>;
-    case 3: return ssm::conv1d_packed_kernel<BF16, 3>;
-    case 4: return ssm::conv1d_packed_kernel<BF16, 4>;
+    case 1: return ssm::conv1d_packed_kernel<BF16, 1, T>;
+    case 2: return ssm::conv1d_packed_kernel<BF16, 2, T>;
+    case 3: return ssm::conv1d_packed_kernel<BF16, 3, T>;
+    case 4: return ssm::conv1d_packed_kernel<BF16, 4, T>;
     default: return nullptr;
   }
 }
 
 using ConvStepKernel = void (*)(const ssm::ConvStepArgs);
-template <bool BF16>
+template <bool BF16, int R>
 ConvStepKernel conv_step_kernel(int64_t width) {
   switch (width) {
-    case 1: return ssm::conv1d_update_cache_kernel<BF16, 1>;
-    case 2: return ssm::conv1d_update_cache_kernel<BF16, 2>;
-    case 3: return ssm::conv1d_update_cache_kernel<BF16, 3>;
-    case 4: return ssm::conv1d_update_cache_kernel<BF16, 4>;
+    case 1: return ssm::conv1d_update_cache_kernel<BF16, 1, R>;
+    case 2: return ssm::conv1d_update_cache_kernel<BF16, 2, R>;
+    case 3: return ssm::conv1d_update_cache_kernel<BF16, 3, R>;
+    case 4: return ssm::conv1d_update_cache_kernel<BF16, 4, R>;
     default: return nullptr;
   }
 }
@@ -154,9 +160,12 @@ auto by_dstate(bool bf16, bool cb16, int64_t n) {
    ...);
   return k;
 }
-template <bool BF16, bool CB16, int N>
-struct StateStep {
-  static auto get() { return &ssm::state_update_cache_kernel<BF16, CB16, N>; }
+template <int R>
+struct StateStepOf {
+  template <bool BF16, bool CB16, int N>
+  struct K {
+    static auto get() { return &ssm::state_update_cache_kernel<BF16, CB16, N, R>; }
+  };
 };
 template <bool BF16, bool CB16, int N>
 struct SsdStep {
@@ -209,7 +218,8 @@ ssm_status_t q8_call(bool store, int64_t count, int64_t rows, int64_t dstate, co
   if (store) SSM_TRY(check_overlap(kept, 2, in_s, 3));
   else SSM_TRY(check_overlap(live, 1, in_l, 4));
   const int64_t v = cb16 ? (dstate < 8 ? dstate : 8) : (dstate < 4 ? dstate : 4);
-  const int64_t blocks = (rows * (dstate / v) + ssm::kQ8Threads - 1) / ssm::kQ8Threads;
+  const int64_t per = static_cast<int64_t>(ssm::kQ8Threads) / (dstate / v) * ssm::kQ8Rows;
+  const int64_t blocks = (rows + per - 1) / per;
   if (blocks > kMaxBlocks) return fail(SSM_ERR_UNSUPPORTED, "grid too large");
   a.cache_slots = cache_slots; a.codes = codes; a.scales = scales; a.store_slots = store_slots;
   a.stored = stored; a.count = count; a.rows = rows;
@@ -331,12 +341,17 @@ ssm_status_t ssm_causal_conv1d_packed_fwd(const ssm_packed_t* seqs, int64_t dim,
   a.silu = silu ? 1 : 0;
   const int64_t ncv = (dim + vec - 1) / vec;
   const int64_t ncb = (ncv + ssm::kConvThreads - 1) / ssm::kConvThreads;
-  const int64_t ntiles = (seqs->total + ssm::kPackTile - 1) / ssm::kPackTile;
+  const int64_t large = (seqs->total + ssm::kPackTile - 1) / ssm::kPackTile;
+  const bool small = large * ncb < 2 * device_cus() || seqs->sequences > large;
+  const int64_t ntiles = small ? (seqs->total + ssm::kPackTileSmall - 1) / ssm::kPackTileSmall : large;
   int64_t grid;
   if (ncb > kMaxBlocks || !mul_ok(ncb, ntiles, &grid) || grid > kMaxBlocks)
     return fail(SSM_ERR_UNSUPPORTED, "grid too large");
   a.ncb = static_cast<int32_t>(ncb);
-  const ConvPackedKernel k = dtype == SSM_BF16 ? conv_packed_kernel<true>(width) : conv_packed_kernel<false>(width);
+  const bool bf16 = dtype == SSM_BF16;
+  const ConvPackedKernel k =
+      small ? (bf16 ? conv_packed_kernel<true, ssm::kPackTileSmall>(width) : conv_packed_kernel<false, ssm::kPackTileSmall>(width))
+            : (bf16 ? conv_packed_kernel<true, ssm::kPackTile>(width) : conv_packed_kernel<false, ssm::kPackTile>(width));
   hipLaunchKernelGGL(k, dim3(static_cast<unsigned>(grid)), dim3(ssm::kConvThreads), 0,
                      static_cast<hipStream_t>(stream), a);
   return check_launch("causal conv1d (packed)");
@@ -460,8 +475,12 @@ ssm_status_t ssm_causal_conv1d_update_cache(int64_t batch, int64_t dim, int64_t 
   const int64_t per = static_cast<int64_t>(ssm::kStepThreads) * ssm::kConvStepVec;
   const int64_t blocks = (dim + per - 1) / per;
   if (blocks > kMaxBlocks) return fail(SSM_ERR_UNSUPPORTED, "grid too large");
-  const ConvStepKernel k = dtype == SSM_BF16 ? conv_step_kernel<true>(width) : conv_step_kernel<false>(width);
-  hipLaunchKernelGGL(k, dim3(static_cast<unsigned>(blocks), grid_y(batch)), dim3(ssm::kStepThreads), 0,
+  const int R = step_entries(blocks, batch);
+  const bool bf16 = dtype == SSM_BF16;
+  const ConvStepKernel k =
+      R > 1 ? (bf16 ? conv_step_kernel<true, kStepEntries>(width) : conv_step_kernel<false, kStepEntries>(width))
+            : (bf16 ? conv_step_kernel<true, 1>(width) : conv_step_kernel<false, 1>(width));
+  hipLaunchKernelGGL(k, dim3(static_cast<unsigned>(blocks), grid_y((batch + R - 1) / R)), dim3(ssm::kStepThreads), 0,
                      static_cast<hipStream_t>(stream), a);
   return check_launch("causal conv1d step (cache)");
 }
@@ -478,10 +497,10 @@ ssm_status_t ssm_state_update_cache(int64_t batch, int64_t dim, int64_t dstate, 
   if (dtype != SSM_F32 && dtype != SSM_BF16) return fail(SSM_ERR_UNSUPPORTED, "unknown dtype %d", (int)dtype);
   if (!cache) return fail(SSM_ERR_INVALID_ARG, "NULL cache");
   const bool cb16 = cache->dtype == SSM_BF16;
-  const auto k = by_dstate<StateStep, 1, 2, 4, 8, 16, 32, 64>(dtype == SSM_BF16, cb16, dstate);
+  auto k = by_dstate<StateStepOf<1>::K, 1, 2, 4, 8, 16, 32, 64>(dtype == SSM_BF16, cb16, dstate);
   if (!k) return fail(SSM_ERR_UNSUPPORTED, "dstate %lld not in {1,2,4,8,16,32,64}", (long long)dstate);
   const int64_t es = dtype == SSM_BF16 ? 2 : 4;
-  const int64_t spt = cb16 ? (dstate < 8 ? dstate : 8) : (dstate < 4 ? dstate : 4);
+  const int64_t spt = cb16 ? (dstate < 8 ? dstate : 8) : (dstate < 4 ? dstate : 4);  // kStepStates
   int64_t entry, n_dn;
   if (!mul_ok(dim, dstate, &entry) || !mul_ok(entry, 4, &n_dn))
     return fail(SSM_ERR_INVALID_ARG, "tensor size overflows int64");
@@ -507,7 +526,9 @@ ssm_status_t ssm_state_update_cache(int64_t batch, int64_t dim, int64_t dstate, 
   a.softplus = delta_softplus ? 1 : 0;
   const int64_t blocks = (dim * (dstate / spt) + ssm::kStepThreads - 1) / ssm::kStepThreads;
   if (blocks > kMaxBlocks) return fail(SSM_ERR_UNSUPPORTED, "grid too large");
-  hipLaunchKernelGGL(k, dim3(static_cast<unsigned>(blocks), grid_y(batch)), dim3(ssm::kStepThreads), 0,
+  const int R = step_entries(blocks, batch);
+  if (R > 1) k = by_dstate<StateStepOf<kStepEntries>::K, 1, 2, 4, 8, 16, 32, 64>(dtype == SSM_BF16, cb16, dstate);
+  hipLaunchKernelGGL(k, dim3(static_cast<unsigned>(blocks), grid_y((batch + R - 1) / R)), dim3(ssm::kStepThreads), 0,
                      static_cast<hipStream_t>(stream), a);
   return check_launch("scan step (cache)");
 }

@@ -56,80 +56,97 @@ __device__ __forceinline__ void store_codes(int8_t* p, const int (&q)[NV]) {
   }
 }
 
+template <int NV>
+struct Codes {
+  uint32_t w[(NV + 3) / 4];
+  __device__ __forceinline__ void load(const int8_t* p) {
+    if constexpr (NV % 4 == 0) {
+#pragma unroll
+      for (int i = 0; i < NV / 4; ++i) w[i] = reinterpret_cast<const Words<1>::U1*>(p)[i];
+    } else {
+      w[0] = 0;
+#pragma unroll
+      for (int v = 0; v < NV; ++v) w[0] |= static_cast<uint32_t>(static_cast<uint8_t>(p[v])) << (8 * v);
+    }
+  }
+  __device__ __forceinline__ int get(int v) const { return static_cast<int8_t>(w[v / 4] >> (8 * (v % 4))); }
+};
+
+// rows that a thread takes: their loads are in flight together
+constexpr int kQ8Rows = 4;
+
 template <bool CB16, int N>
 __global__ __launch_bounds__(kQ8Threads) void cache_store_q8_kernel(const Q8Args p) {
-  constexpr int V = kQ8Values<CB16, N>, LPR = N / V;
+  constexpr int V = kQ8Values<CB16, N>, LPR = N / V, RPB = kQ8Threads / LPR;
   static_assert(LPR <= 64, "a row's lanes share one wave");
-  const int64_t t = static_cast<int64_t>(blockIdx.x) * kQ8Threads + threadIdx.x;
-  const bool ok = t / LPR < p.rows;
-  const int64_t row = ok ? t / LPR : p.rows - 1;
-  const int n0 = static_cast<int>(t % LPR) * V;
+  const int64_t row0 = static_cast<int64_t>(blockIdx.x) * (RPB * kQ8Rows) + threadIdx.x / LPR;
+  const int n0 = static_cast<int>(threadIdx.x % LPR) * V;
   for (int64_t i = blockIdx.y; i < p.count; i += gridDim.y) {
     const int64_t at = cache_offset(p.cache, p.cache_slots, i);
     const int64_t to = p.store_slots ? p.store_slots[i] : i;
     if (at < 0 || to < 0 || to >= p.stored) continue;
-    Run<CB16, V, true> r;
-    r.load(p.cache.data, at + row * N + n0);
-    // |v| as bits: their order is the values', with infinity and then NaN above every number
-    uint32_t top = 0;
+    Run<CB16, V, true> r[kQ8Rows];
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const uint32_t b = __builtin_bit_cast(uint32_t, r.get(v)) & 0x7fffffffu;
-      top = b > top ? b : top;
+    for (int u = 0; u < kQ8Rows; ++u) {
+      const int64_t row = row0 + u * RPB;
+      r[u].load(p.cache.data, at + (row < p.rows ? row : p.rows - 1) * N + n0);
     }
 #pragma unroll
-    for (int off = 1; off < LPR; off <<= 1) {
-      const uint32_t o = __shfl_xor(top, off, 64);
-      top = o > top ? o : top;
-    }
-    const bool bad = top >= 0x7f800000u;
-    const float scale = bad ? __builtin_nanf("") : __builtin_bit_cast(float, top) / 127.0f;
-    int q[V];
-    if (bad || scale == 0.0f) {
+    for (int u = 0; u < kQ8Rows; ++u) {
+      const int64_t row = row0 + u * RPB;
+      // |v| as bits: their order is the values', with infinity and then NaN above every number
+      uint32_t top = 0;
 #pragma unroll
-      for (int v = 0; v < V; ++v) q[v] = 0;
-    } else {
+      for (int v = 0; v < V; ++v) {
+        const uint32_t b = __builtin_bit_cast(uint32_t, r[u].get(v)) & 0x7fffffffu;
+        top = b > top ? b : top;
+      }
+      top = group_reduce<LPR>(top, [](uint32_t a, uint32_t b) { return a > b ? a : b; });
+      const bool bad = top >= 0x7f800000u;
+      const float scale = bad ? __builtin_nanf("") : __builtin_bit_cast(float, top) / 127.0f;
       const float up = scale < 1.17549435e-38f ? 1.2676506e30f : 1.0f;  // 2^100 where 1 / scale overflows
       const float sc = scale * up, inv = 1.0f / sc;
+      int q[V];
 #pragma unroll
-      for (int v = 0; v < V; ++v) q[v] = static_cast<int>(q8_code(r.get(v) * up, sc, inv));
-    }
-    if (ok) {
-      const int64_t o = (to * p.rows + row) * N + n0;
-      store_codes<V>(p.codes + o, q);
-      if (n0 == 0) p.scales[to * p.rows + row] = scale;
+      for (int v = 0; v < V; ++v)
+        q[v] = bad || scale == 0.0f ? 0 : static_cast<int>(q8_code(r[u].get(v) * up, sc, inv));
+      if (row < p.rows) {
+        const int64_t o = (to * p.rows + row) * N + n0;
+        store_codes<V>(p.codes + o, q);
+        if (n0 == 0) p.scales[to * p.rows + row] = scale;
+      }
     }
   }
 }
 
 template <bool CB16, int N>
 __global__ __launch_bounds__(kQ8Threads) void cache_load_q8_kernel(const Q8Args p) {
-  constexpr int V = kQ8Values<CB16, N>, LPR = N / V;
-  const int64_t t = static_cast<int64_t>(blockIdx.x) * kQ8Threads + threadIdx.x;
-  if (t / LPR >= p.rows) return;
-  const int64_t row = t / LPR;
-  const int n0 = static_cast<int>(t % LPR) * V;
+  constexpr int V = kQ8Values<CB16, N>, LPR = N / V, RPB = kQ8Threads / LPR;
+  const int64_t row0 = static_cast<int64_t>(blockIdx.x) * (RPB * kQ8Rows) + threadIdx.x / LPR;
+  const int n0 = static_cast<int>(threadIdx.x % LPR) * V;
   for (int64_t i = blockIdx.y; i < p.count; i += gridDim.y) {
     const int64_t at = cache_offset(p.cache, p.cache_slots, i);
     const int64_t from = p.store_slots ? p.store_slots[i] : i;
     if (at < 0 || from < 0 || from >= p.stored) continue;
-    const int8_t* c = p.codes + (from * p.rows + row) * N + n0;
-    const float scale = p.scales[from * p.rows + row];
-    float val[V];
-    if constexpr (V % 4 == 0) {
+    Codes<V> c[kQ8Rows];
+    float scale[kQ8Rows];
 #pragma unroll
-      for (int k = 0; k < V / 4; ++k) {
-        const uint32_t w = reinterpret_cast<const Words<1>::U1*>(c)[k];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) val[4 * k + j] = static_cast<float>(static_cast<int8_t>(w >> (8 * j))) * scale;
-      }
-    } else {
-#pragma unroll
-      for (int v = 0; v < V; ++v) val[v] = static_cast<float>(c[v]) * scale;
+    for (int u = 0; u < kQ8Rows; ++u) {
+      const int64_t row = from * p.rows + (row0 + u * RPB < p.rows ? row0 + u * RPB : p.rows - 1);
+      c[u].load(p.codes + row * N + n0);
+      scale[u] = p.scales[row];
     }
-    Run<CB16, V, true> r;
-    r.set(val);
-    r.store(p.cache.data, at + row * N + n0);
+#pragma unroll
+    for (int u = 0; u < kQ8Rows; ++u) {
+      const int64_t row = row0 + u * RPB;
+      if (row >= p.rows) break;
+      float val[V];
+#pragma unroll
+      for (int v = 0; v < V; ++v) val[v] = static_cast<float>(c[u].get(v)) * scale[u];
+      Run<CB16, V, true> r;
+      r.set(val);
+      r.store(p.cache.data, at + row * N + n0);
+    }
   }
 }
 

@@ -14,6 +14,34 @@ namespace ssm {
 
 constexpr int kStepThreads = 256;
 
+// The step's functions by the inputs' type.  bf16: the hardware exp2 with log2(e) in its factor and
+// fused multiply-adds, as in the scan.  fp32: the library's exp and log1p and the formula's own
+// roundings: exp2(dt (A log2 e)) is off by up to |dt A| 2^-24 more, which fp32 outputs would show,
+// and a step is bound by its states' traffic, not by these.
+template <bool BF16>
+struct StepMath {
+  static __device__ __forceinline__ float softplus(float v) {
+    if constexpr (BF16) return softplus_f32(v);
+    else return fmaxf(v, 0.0f) + log1pf(expf(-fabsf(v)));
+  }
+  static __device__ __forceinline__ float decay(float dt, float a) {
+    if constexpr (BF16) return hw_exp2(dt * (a * kLog2e));
+    else return expf(dt * a);
+  }
+  static __device__ __forceinline__ float state(float a, float h, float w, float b) {
+    if constexpr (BF16) {
+      return fmaf(a, h, w * b);
+    } else {
+#pragma clang fp contract(off)
+      return a * h + w * b;
+    }
+  }
+  static __device__ __forceinline__ float gate(float z) {
+    if constexpr (BF16) return silu_f32(z);
+    else return z / (1.0f + expf(-z));
+  }
+};
+
 struct StepArgs {
   CacheRef cache;
   const int32_t* slots;
@@ -32,46 +60,66 @@ struct StepArgs {
   int32_t softplus;
 };
 
-// A thread owns SPT consecutive states of a channel (16 bytes), N / SPT lanes a channel.
-template <bool BF16, bool CB16, int N>
+// States of a channel that a lane takes: 16 bytes
+template <bool CB16, int N>
+constexpr int kStepStates = CB16 ? (N < 8 ? N : 8) : (N < 4 ? N : 4);
+
+// A thread owns SPT consecutive states of a channel, N / SPT lanes a channel, in R entries of
+// the batch: A, D and the bias serve all of them, and their states' loads are in flight together.
+template <bool BF16, bool CB16, int N, int R>
 __global__ __launch_bounds__(kStepThreads) void state_update_cache_kernel(const StepArgs p) {
-  constexpr int SPT = CB16 ? (N < 8 ? N : 8) : (N < 4 ? N : 4);
-  constexpr int TPC = N / SPT;
+  constexpr int SPT = kStepStates<CB16, N>, TPC = N / SPT;
+  using M = StepMath<BF16>;
   const int64_t t = static_cast<int64_t>(blockIdx.x) * kStepThreads + threadIdx.x;
   const bool ok = t / TPC < p.dim;
   const int64_t d = ok ? t / TPC : p.dim - 1;
   const int n0 = static_cast<int>(t % TPC) * SPT;
-  Run<false, SPT> a;
-  a.load(p.A, d * N + n0);
-  const float bias = p.delta_bias ? p.delta_bias[d] : 0.0f;
-  const float dsk = p.Dskip ? p.Dskip[d] : 0.0f;
-  for (int64_t b = blockIdx.y; b < p.batch; b += gridDim.y) {
-    const int64_t at = cache_offset(p.cache, p.slots, b);
-    if (at < 0) continue;
-    Run<CB16, SPT, true> st;
-    Run<BF16, SPT> bv, cv;
-    st.load(p.cache.data, at + d * N + n0);
-    bv.load(p.B, b * p.sB + n0);
-    cv.load(p.C, b * p.sC + n0);
-    const float xv = load_one<BF16>(p.x, b * p.sx + d);
-    const float vb = load_one<BF16>(p.delta, b * p.sdelta + d) + bias;
-    const float zv = p.z ? load_one<BF16>(p.z, b * p.sz + d) : 0.0f;
-    const float dt = p.softplus ? softplus_f32(vb) : vb;
-    const float w = dt * xv;
-    float h[SPT], yp = 0.0f;
+  const bool has_z = p.z != nullptr;
+  const void* zsrc = has_z ? p.z : p.x;
+  const int64_t zstride = has_z ? p.sz : p.sx;
+  for (int64_t b0 = static_cast<int64_t>(blockIdx.y) * R; b0 < p.batch; b0 += static_cast<int64_t>(gridDim.y) * R) {
+    // every load on every path: an entry past the batch or without a slot reads entry b0 and slot 0
+    int64_t at[R], b[R];
+    Run<CB16, SPT, true> st[R];
+    Run<BF16, SPT> bv[R], cv[R];
+    Run<BF16, 1> xr[R], dr[R], zr[R];
 #pragma unroll
-    for (int j = 0; j < SPT; ++j) {
-      h[j] = fmaf(hw_exp2(dt * (a.get(j) * kLog2e)), st.get(j), w * bv.get(j));
-      yp = fmaf(cv.get(j), h[j], yp);
+    for (int i = 0; i < R; ++i) {
+      b[i] = b0 + i < p.batch ? b0 + i : b0;
+      at[i] = b0 + i < p.batch ? cache_offset(p.cache, p.slots, b0 + i) : -1;
     }
-    st.set(h);
-    if (ok) st.store(p.cache.data, at + d * N + n0);
 #pragma unroll
-    for (int off = 1; off < TPC; off <<= 1) yp += __shfl_xor(yp, off, 64);
-    if (ok && n0 == 0) {
-      float yv = fmaf(dsk, xv, yp);
-      if (p.z) yv *= silu_f32(zv);
-      store_one<BF16>(p.y, b * p.sy + d, yv);
+    for (int i = 0; i < R; ++i) {
+      st[i].load(p.cache.data, (at[i] < 0 ? 0 : at[i]) + d * N + n0);
+      xr[i].load(p.x, b[i] * p.sx + d);
+      dr[i].load(p.delta, b[i] * p.sdelta + d);
+      zr[i].load(zsrc, b[i] * zstride + d);
+      bv[i].load(p.B, b[i] * p.sB + n0);
+      cv[i].load(p.C, b[i] * p.sC + n0);
+    }
+    Run<false, SPT> a;
+    a.load(p.A, d * N + n0);
+    const float bias = p.delta_bias ? p.delta_bias[d] : 0.0f;
+    const float dsk = p.Dskip ? p.Dskip[d] : 0.0f;
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      const float xv = xr[i].get(0), vb = dr[i].get(0) + bias;
+      const float dt = p.softplus ? M::softplus(vb) : vb;
+      const float w = dt * xv;
+      float h[SPT], yp = 0.0f;
+#pragma unroll
+      for (int j = 0; j < SPT; ++j) {
+        h[j] = M::state(M::decay(dt, a.get(j)), st[i].get(j), w, bv[i].get(j));
+        yp = fmaf(cv[i].get(j), h[j], yp);
+      }
+      st[i].set(h);
+      if (ok && at[i] >= 0) st[i].store(p.cache.data, at[i] + d * N + n0);
+      yp = group_sum<TPC>(yp);
+      if (ok && at[i] >= 0 && n0 == 0) {
+        float yv = fmaf(dsk, xv, yp);
+        if (has_z) yv *= M::gate(zr[i].get(0));
+        store_one<BF16>(p.y, b[i] * p.sy + d, yv);
+      }
     }
   }
 }
@@ -91,55 +139,69 @@ struct ConvStepArgs {
 
 constexpr int kConvStepVec = 4;  // channels per thread
 
-// A thread owns 4 channels of an entry: its windows are 4 (K - 1) consecutive elements.
-template <bool BF16, int K>
+// A thread owns 4 channels of R entries: an entry's windows are 4 (K - 1) consecutive elements, and the
+// weights serve all R.
+template <bool BF16, int K, int R>
 __global__ __launch_bounds__(kStepThreads) void conv1d_update_cache_kernel(const ConvStepArgs p) {
-  constexpr int V = kConvStepVec, W = K - 1;
+  constexpr int V = kConvStepVec, W = K - 1, E = W > 0 ? V * W : 2;
   const int64_t d0 = (static_cast<int64_t>(blockIdx.x) * kStepThreads + threadIdx.x) * V;
   if (d0 >= p.dim) return;
   const int nv = static_cast<int>(p.dim - d0 < V ? p.dim - d0 : V);
-  for (int64_t b = blockIdx.y; b < p.batch; b += gridDim.y) {
-    // without windows (K 1) there is no slot to look up: only padding is skipped
-    const int64_t at = W > 0 ? cache_offset(p.cache, p.slots, b) : (p.slots && p.slots[b] < 0 ? -1 : 0);
-    if (at < 0) continue;
+  for (int64_t b0 = static_cast<int64_t>(blockIdx.y) * R; b0 < p.batch; b0 += static_cast<int64_t>(gridDim.y) * R) {
+    int64_t at[R], b[R];
+    Run<BF16, V> xr[R];
+    Run<BF16, E> win[R];
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      // without windows (K 1) there is no slot to look up: only padding is skipped
+      b[i] = b0 + i < p.batch ? b0 + i : b0;
+      at[i] = b0 + i >= p.batch ? -1 : W > 0 ? cache_offset(p.cache, p.slots, b0 + i) : (p.slots && p.slots[b0 + i] < 0 ? -1 : 0);
+    }
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      const int64_t from = (at[i] < 0 ? 0 : at[i]) + d0 * W;
+      if (nv == V) {
+        xr[i].load(p.x, b[i] * p.sx + d0);
+        if constexpr (W > 0) win[i].load(p.cache.data, from);
+      } else {
+        xr[i].load_some(p.x, b[i] * p.sx + d0, nv);
+        if constexpr (W > 0) win[i].load_some(p.cache.data, from, nv * W);
+      }
+    }
+    Run<false, V * K> wt;
+    Run<false, V> bias;
     if (nv == V) {
-      Run<BF16, V> xr;
-      Run<BF16, V * W + (W == 0)> win;
-      xr.load(p.x, b * p.sx + d0);
-      if constexpr (W > 0) win.load(p.cache.data, at + d0 * W);
-      float out[V], keep[V * W + (W == 0)];
+      wt.load(p.weight, d0 * K);
+      if (p.bias) bias.load(p.bias, d0);
+      else bias.load_some(p.weight, 0, 0);
+    } else {
+      wt.load_some(p.weight, d0 * K, nv * K);
+      bias.load_some(p.bias, d0, p.bias ? nv : 0);
+    }
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      if (at[i] < 0) continue;
+      float out[V], keep[E] = {};
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        const float* wt = p.weight + (d0 + v) * K;
-        float acc = p.bias ? p.bias[d0 + v] : 0.0f;
+        float acc = bias.get(v);
 #pragma unroll
-        for (int j = 0; j < W; ++j) acc = fmaf(wt[j], win.get(v * W + j), acc);
-        acc = fmaf(wt[W], xr.get(v), acc);
+        for (int j = 0; j < W; ++j) acc = fmaf(wt.get(v * K + j), win[i].get(v * W + j), acc);
+        acc = fmaf(wt.get(v * K + W), xr[i].get(v), acc);
         out[v] = p.silu ? silu_f32(acc) : acc;
 #pragma unroll
-        for (int j = 0; j < W; ++j) keep[v * W + j] = j + 1 < W ? win.get(v * W + j + 1) : xr.get(v);
+        for (int j = 0; j < W; ++j) keep[v * W + j] = j + 1 < W ? win[i].get(v * W + j + 1) : xr[i].get(v);
       }
       Run<BF16, V> yr;
       yr.set(out);
-      yr.store(p.y, b * p.sy + d0);
-      if constexpr (W > 0) {
-        win.set(keep);
-        win.store(p.cache.data, at + d0 * W);
+      win[i].set(keep);
+      if (nv == V) {
+        yr.store(p.y, b[i] * p.sy + d0);
+        if constexpr (W > 0) win[i].store(p.cache.data, at[i] + d0 * W);
+      } else {
+        yr.store_some(p.y, b[i] * p.sy + d0, nv);
+        if constexpr (W > 0) win[i].store_some(p.cache.data, at[i] + d0 * W, nv * W);
       }
-      continue;
-    }
-    for (int v = 0; v < nv; ++v) {
-      const int64_t d = d0 + v;
-      const float xv = load_one<BF16>(p.x, b * p.sx + d);
-      float acc = p.bias ? p.bias[d] : 0.0f;
-#pragma unroll
-      for (int j = 0; j < W; ++j) acc = fmaf(p.weight[d * K + j], load_one<BF16>(p.cache.data, at + d * W + j), acc);
-      acc = fmaf(p.weight[d * K + W], xv, acc);
-      store_one<BF16>(p.y, b * p.sy + d, p.silu ? silu_f32(acc) : acc);
-#pragma unroll
-      for (int j = 0; j < W; ++j)
-        store_one<BF16>(p.cache.data, at + d * W + j,
-                        j + 1 < W ? load_one<BF16>(p.cache.data, at + d * W + j + 1) : xv);
     }
   }
 }
@@ -181,7 +243,8 @@ __global__ __launch_bounds__(kStepThreads) void ssd_state_update_cache_kernel(co
   const int64_t p0 = static_cast<int64_t>(blockIdx.x % p.chunks) * kSsdStepChannels<CB16, N> + threadIdx.x / TPC;
   const int n0 = static_cast<int>(threadIdx.x % TPC) * SPT;
   const int g = h / (p.nheads / p.ngroups);
-  const float al = p.A[h] * kLog2e;
+  using M = StepMath<BF16>;
+  const float ah = p.A[h];
   const float bias = p.dt_bias ? p.dt_bias[h] : 0.0f;
   const float dsk = p.D ? p.D[h] : 0.0f;
   for (int64_t b = blockIdx.y; b < p.batch; b += gridDim.y) {
@@ -205,24 +268,23 @@ __global__ __launch_bounds__(kStepThreads) void ssd_state_update_cache_kernel(co
     bv.load(p.B, b * p.sB + static_cast<int64_t>(g) * N + n0);
     cv.load(p.C, b * p.sC + static_cast<int64_t>(g) * N + n0);
     const float v = load_one<BF16>(p.dt, b * p.sdt + h) + bias;
-    const float dtv = p.softplus ? softplus_f32(v) : v;
-    const float a = hw_exp2(dtv * al);
+    const float dtv = p.softplus ? M::softplus(v) : v;
+    const float a = M::decay(dtv, ah);
 #pragma unroll
     for (int u = 0; u < kSsdStepUnroll; ++u) {
       const float w = dtv * xv[u];
       float s[SPT], yp = 0.0f;
 #pragma unroll
       for (int j = 0; j < SPT; ++j) {
-        s[j] = fmaf(a, st[u].get(j), w * bv.get(j));
+        s[j] = M::state(a, st[u].get(j), w, bv.get(j));
         yp = fmaf(cv.get(j), s[j], yp);
       }
       st[u].set(s);
       if (ok[u]) st[u].store(p.cache.data, off[u]);
-#pragma unroll
-      for (int o = 1; o < TPC; o <<= 1) yp += __shfl_xor(yp, o, 64);
+      yp = group_sum<TPC>(yp);
       if (ok[u] && n0 == 0) {
         float yv = fmaf(dsk, xv[u], yp);
-        if (p.z) yv *= silu_f32(zv[u]);
+        if (p.z) yv *= M::gate(zv[u]);
         store_one<BF16>(p.y, b * p.sy + static_cast<int64_t>(h) * P + p0 + u * CPB, yv);
       }
     }

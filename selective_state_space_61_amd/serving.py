@@ -26,72 +26,95 @@ from typing import Optional
 
 import torch
 
-from . import (SSM_BF16, SSM_F32, Cache, Packed, RowStrides, _check, _dtype_code, _need, _ptr, _stream, load_library)
+from . import SSM_BF16, SSM_F32, Cache, Packed, RowStrides, _check, _dtype_code, load_library
+
+# A decode step's kernel takes a few microseconds, so the checks are written to cost little: devices
+# are compared by index, and what is wrong is worked out only once something is.
 
 
-def _row_stride(t: torch.Tensor, name: str, shape, dtype, device) -> int:
-    """Elements between the rows of t (0 for at most one row), whose rows must be contiguous."""
+def _refuse(t, name: str, shape, dtype, device: int) -> None:
     if t is None:
         raise ValueError(f"{name} is required")
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     if t.dtype != dtype:
         raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on {t.device}, not on the other tensors' device")
+    raise ValueError(f"{name} must be contiguous")
+
+
+def _dense(t: Optional[torch.Tensor], name: str, shape, dtype, device: int) -> int:
+    """The address of a contiguous tensor of this shape, dtype and device."""
+    if (t is None or t.shape != shape or t.dtype is not dtype or t.get_device() != device or not t.is_contiguous()):
+        _refuse(t, name, shape, dtype, device)
+    return t.data_ptr()
+
+
+def _optional(t: Optional[torch.Tensor], name: str, shape, dtype, device: int) -> Optional[int]:
+    return None if t is None else _dense(t, name, shape, dtype, device)
+
+
+def _row_stride(t: Optional[torch.Tensor], name: str, shape, dtype, device: int) -> int:
+    """Elements between the rows of t (0: contiguous or at most one), whose rows must be contiguous."""
+    if t is None or t.shape != shape or t.dtype is not dtype or t.get_device() != device:
+        _refuse(t, name, shape, dtype, device)
     if t.is_contiguous():
         return 0
+    stride = t.stride()
     width = 1
-    for n, s in zip(reversed(shape[1:]), reversed(t.stride()[1:])):
+    for n, s in zip(reversed(shape[1:]), reversed(stride[1:])):
         if n > 1 and s != width:
             raise ValueError(f"the rows of {name} must be contiguous")
         width *= n
     if shape[0] <= 1:
         return 0
-    if t.stride(0) < width:
+    if stride[0] < width:
         raise ValueError(f"the rows of {name} must not overlap")
-    return t.stride(0)
+    return stride[0]
 
 
-def _cache(t: Optional[torch.Tensor], name: str, entry, device, dtype=None) -> Cache:
+def _cache(t: Optional[torch.Tensor], name: str, entry, device: int, dtype=None) -> Cache:
     """The cache's descriptor: (slots,) + entry, each slot contiguous."""
     if t is None:
         raise ValueError(f"{name} is required")
-    if t.dim() != 1 + len(entry) or tuple(t.shape[1:]) != tuple(entry):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected (slots, {', '.join(map(str, entry))})")
-    if t.dtype not in (torch.float32, torch.bfloat16) or (dtype is not None and t.dtype != dtype):
-        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype or 'float32 or bfloat16'}")
-    stride = _row_stride(t, name, t.shape, t.dtype, device)
-    return Cache(t.data_ptr(), t.shape[0], stride, SSM_BF16 if t.dtype == torch.bfloat16 else SSM_F32, 0)
+    shape = t.shape
+    if shape[1:] != entry:
+        raise ValueError(f"{name} has shape {tuple(shape)}, expected (slots, {', '.join(map(str, entry))})")
+    ty = t.dtype
+    if ty is not dtype and (dtype is not None or ty not in (torch.float32, torch.bfloat16)):
+        raise TypeError(f"{name} has dtype {ty}, expected {dtype or 'float32 or bfloat16'}")
+    return Cache(t.data_ptr(), shape[0], _row_stride(t, name, shape, ty, device),
+                 SSM_BF16 if ty is torch.bfloat16 else SSM_F32, 0)
 
 
-def _indices(t: Optional[torch.Tensor], name: str, count: int, device, slots: int) -> None:
+def _indices(t: Optional[torch.Tensor], name: str, count: int, device: int, slots: int) -> Optional[int]:
     if t is None:
         if slots < count:
             raise ValueError(f"without {name} there must be at least {count} slots, not {slots}")
-        return
-    _need(t, name, (count,), torch.int32, device)
+        return None
+    return _dense(t, name, (count,), torch.int32, device)
 
 
-def _packed(cu_seqlens, cache_slots, has_initial, total: int, slots: Optional[int], max_seqlen: int, device) -> Packed:
+def _packed(cu_seqlens, cache_slots, has_initial, total: int, ref: Optional[Cache], max_seqlen: int, device: int) -> Packed:
     if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
         raise ValueError("cu_seqlens must hold one more entry than there are sequences")
     nseq = cu_seqlens.numel() - 1
-    _need(cu_seqlens, "cu_seqlens", (nseq + 1,), torch.int32, device)
-    if slots is None:
+    cu = _dense(cu_seqlens, "cu_seqlens", (nseq + 1,), torch.int32, device)
+    if ref is None:
         if cache_slots is not None or has_initial is not None:
             raise ValueError("cache_slots and has_initial need a cache")
-    else:
-        _indices(cache_slots, "cache_slots", nseq, device, slots)
+        return Packed(total, nseq, max_seqlen, cu, None, None)
+    slots = _indices(cache_slots, "cache_slots", nseq, device, ref.slots)
     if has_initial is not None:
         if has_initial.dtype not in (torch.bool, torch.uint8):
             raise TypeError(f"has_initial has dtype {has_initial.dtype}, expected bool or uint8")
-        _need(has_initial, "has_initial", (nseq,), has_initial.dtype, device)
-    return Packed(total, nseq, int(max_seqlen), cu_seqlens.data_ptr(), _ptr(cache_slots), _ptr(has_initial))
+        has_initial = _dense(has_initial, "has_initial", (nseq,), has_initial.dtype, device)
+    return Packed(total, nseq, max_seqlen, cu, slots, has_initial)
 
 
 @contextlib.contextmanager
-def _other(device: torch.device, stream):
+def _other(device: int, stream):
     """The tensors' device current, and the given stream, where they are not already."""
     with torch.cuda.device(device):
         if stream is None:
@@ -104,15 +127,15 @@ def _other(device: torch.device, stream):
             yield
 
 
-def _run(call, device: torch.device, stream):
-    """call() with the tensors' device current and, when one is given, on that stream: what it
-    allocates then belongs to the stream that uses it."""
-    if device.type != "cuda":
-        raise ValueError(f"the tensors are on {device}, expected a GPU")
-    if stream is None and torch.cuda.current_device() == device.index:
-        return call()
+def _run(call, device: int, stream):
+    """call(stream handle) with the tensors' device current and, when one is given, on that stream: what
+    it allocates then belongs to the stream that uses it."""
+    if device < 0:
+        raise ValueError("the tensors are on the host, expected a GPU")
+    if stream is None and torch.cuda.current_device() == device:
+        return call(torch.cuda.current_stream(device).cuda_stream)
     with _other(device, stream):
-        return call()
+        return call(torch.cuda.current_stream(device).cuda_stream)
 
 
 def ssm_causal_conv1d_packed_fwd(x: torch.Tensor, weight: torch.Tensor, cu_seqlens: torch.Tensor,
@@ -128,20 +151,19 @@ def ssm_causal_conv1d_packed_fwd(x: torch.Tensor, weight: torch.Tensor, cu_seqle
         raise ValueError("x must be (total, dim) and weight (dim, width)")
     total, dim = x.shape
     width = weight.shape[1]
-    dev, dt = x.device, x.dtype
-    code = _dtype_code(x)
+    dev, dt, code = x.get_device(), x.dtype, _dtype_code(x)
     strides = RowStrides(x=_row_stride(x, "x", x.shape, dt, dev))
-    _need(weight, "weight", (dim, width), torch.float32, dev)
-    _need(bias, "bias", (dim,), torch.float32, dev, optional=True)
+    w = _dense(weight, "weight", (dim, width), torch.float32, dev)
+    b = _optional(bias, "bias", (dim,), torch.float32, dev)
     ref = _cache(cache, "cache", (dim, width - 1), dev, dt) if cache is not None else None
-    seqs = _packed(cu_seqlens, cache_slots, has_initial, total, None if ref is None else ref.slots, 0, dev)
+    seqs = _packed(cu_seqlens, cache_slots, has_initial, total, ref, 0, dev)
     if y is not None:
         strides.y = _row_stride(y, "y", x.shape, dt, dev)
 
-    def call():
-        out = torch.empty((total, dim), dtype=dt, device=dev) if y is None else y
-        _check(lib.ssm_causal_conv1d_packed_fwd(seqs, dim, width, code, x.data_ptr(), weight.data_ptr(), _ptr(bias),
-                                                int(bool(silu)), out.data_ptr(), ref, strides, _stream(dev, stream)))
+    def call(st):
+        out = x.new_empty((total, dim)) if y is None else y
+        _check(lib.ssm_causal_conv1d_packed_fwd(seqs, dim, width, code, x.data_ptr(), w, b, int(bool(silu)),
+                                                out.data_ptr(), ref, strides, st))
         return out
 
     return _run(call, dev, stream)
@@ -174,32 +196,31 @@ def ssm_scan_packed_fwd(x: torch.Tensor, delta: torch.Tensor, A: torch.Tensor, B
         raise ValueError("x must be (total, dim) and A (dim, dstate)")
     total, dim = x.shape
     dstate = A.shape[1]
-    dev, dt = x.device, x.dtype
-    code = _dtype_code(x)
+    dev, dt, code = x.get_device(), x.dtype, _dtype_code(x)
     bc = (total, dstate)
     strides = RowStrides(_row_stride(x, "x", x.shape, dt, dev), _row_stride(delta, "delta", x.shape, dt, dev),
                          _row_stride(B, "B", bc, dt, dev), _row_stride(C, "C", bc, dt, dev),
                          0 if z is None else _row_stride(z, "z", x.shape, dt, dev),
                          0 if y is None else _row_stride(y, "y", x.shape, dt, dev))
-    _need(A, "A", (dim, dstate), torch.float32, dev)
-    _need(D, "D", (dim,), torch.float32, dev, optional=True)
-    _need(delta_bias, "delta_bias", (dim,), torch.float32, dev, optional=True)
+    a = _dense(A, "A", (dim, dstate), torch.float32, dev)
+    d = _optional(D, "D", (dim,), torch.float32, dev)
+    bias = _optional(delta_bias, "delta_bias", (dim,), torch.float32, dev)
     ref = _cache(cache, "cache", (dim, dstate), dev) if cache is not None else None
-    seqs = _packed(cu_seqlens, cache_slots, has_initial, total, None if ref is None else ref.slots, max_seqlen, dev)
+    seqs = _packed(cu_seqlens, cache_slots, has_initial, total, ref, int(max_seqlen), dev)
     if workspace is not None:
-        _need(workspace, "workspace", (workspace.numel(),), torch.uint8, dev)
+        _dense(workspace, "workspace", workspace.shape, torch.uint8, dev)
 
-    def call():
-        out = torch.empty((total, dim), dtype=dt, device=dev) if y is None else y
+    def call(st):
+        out = x.new_empty((total, dim)) if y is None else y
         ws = workspace
         if ws is None:
             n = ctypes.c_int64(0)
             _check(lib.ssm_scan_packed_workspace(seqs, dim, dstate, code, ctypes.byref(n)))
-            ws = torch.empty(n.value, dtype=torch.uint8, device=dev) if n.value else None
-        _check(lib.ssm_scan_packed_fwd(seqs, dim, dstate, code, x.data_ptr(), delta.data_ptr(), A.data_ptr(),
-                                       B.data_ptr(), C.data_ptr(), _ptr(D), _ptr(z), _ptr(delta_bias),
-                                       int(bool(delta_softplus)), out.data_ptr(), ref, strides, _ptr(ws),
-                                       0 if ws is None else ws.numel(), _stream(dev, stream)))
+            ws = x.new_empty(n.value, dtype=torch.uint8) if n.value else None
+        _check(lib.ssm_scan_packed_fwd(seqs, dim, dstate, code, x.data_ptr(), delta.data_ptr(), a, B.data_ptr(),
+                                       C.data_ptr(), d, None if z is None else z.data_ptr(), bias,
+                                       int(bool(delta_softplus)), out.data_ptr(), ref, strides,
+                                       None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(), st))
         return out
 
     return _run(call, dev, stream)
@@ -215,23 +236,21 @@ def ssm_causal_conv1d_update_cache(cache: Optional[torch.Tensor], cache_slots: O
         raise ValueError("x must be (batch, dim) and weight (dim, width)")
     batch, dim = x.shape
     width = weight.shape[1]
-    dev, dt = x.device, x.dtype
-    code = _dtype_code(x)
+    dev, dt, code = x.get_device(), x.dtype, _dtype_code(x)
     strides = RowStrides(x=_row_stride(x, "x", x.shape, dt, dev))
-    _need(weight, "weight", (dim, width), torch.float32, dev)
-    _need(bias, "bias", (dim,), torch.float32, dev, optional=True)
+    w = _dense(weight, "weight", (dim, width), torch.float32, dev)
+    b = _optional(bias, "bias", (dim,), torch.float32, dev)
     ref = None
     if cache is not None or width != 1:
         ref = _cache(cache, "cache", (dim, width - 1), dev, dt)
-    _indices(cache_slots, "cache_slots", batch, dev, batch if ref is None else ref.slots)
+    slots = _indices(cache_slots, "cache_slots", batch, dev, batch if ref is None else ref.slots)
     if y is not None:
         strides.y = _row_stride(y, "y", x.shape, dt, dev)
 
-    def call():
-        out = torch.empty((batch, dim), dtype=dt, device=dev) if y is None else y
-        _check(lib.ssm_causal_conv1d_update_cache(batch, dim, width, code, ref, _ptr(cache_slots), x.data_ptr(),
-                                                  weight.data_ptr(), _ptr(bias), int(bool(silu)), out.data_ptr(),
-                                                  strides, _stream(dev, stream)))
+    def call(st):
+        out = x.new_empty((batch, dim)) if y is None else y
+        _check(lib.ssm_causal_conv1d_update_cache(batch, dim, width, code, ref, slots, x.data_ptr(), w, b,
+                                                  int(bool(silu)), out.data_ptr(), strides, st))
         return out
 
     return _run(call, dev, stream)
@@ -250,25 +269,23 @@ def ssm_state_update_cache(cache: torch.Tensor, cache_slots: Optional[torch.Tens
         raise ValueError("x must be (batch, dim) and A (dim, dstate)")
     batch, dim = x.shape
     dstate = A.shape[1]
-    dev, dt = x.device, x.dtype
-    code = _dtype_code(x)
+    dev, dt, code = x.get_device(), x.dtype, _dtype_code(x)
     bc = (batch, dstate)
     strides = RowStrides(_row_stride(x, "x", x.shape, dt, dev), _row_stride(delta, "delta", x.shape, dt, dev),
                          _row_stride(B, "B", bc, dt, dev), _row_stride(C, "C", bc, dt, dev),
                          0 if z is None else _row_stride(z, "z", x.shape, dt, dev),
                          0 if y is None else _row_stride(y, "y", x.shape, dt, dev))
-    _need(A, "A", (dim, dstate), torch.float32, dev)
-    _need(D, "D", (dim,), torch.float32, dev, optional=True)
-    _need(delta_bias, "delta_bias", (dim,), torch.float32, dev, optional=True)
+    a = _dense(A, "A", (dim, dstate), torch.float32, dev)
+    d = _optional(D, "D", (dim,), torch.float32, dev)
+    bias = _optional(delta_bias, "delta_bias", (dim,), torch.float32, dev)
     ref = _cache(cache, "cache", (dim, dstate), dev)
-    _indices(cache_slots, "cache_slots", batch, dev, ref.slots)
+    slots = _indices(cache_slots, "cache_slots", batch, dev, ref.slots)
 
-    def call():
-        out = torch.empty((batch, dim), dtype=dt, device=dev) if y is None else y
-        _check(lib.ssm_state_update_cache(batch, dim, dstate, code, ref, _ptr(cache_slots), x.data_ptr(),
-                                          delta.data_ptr(), A.data_ptr(), B.data_ptr(), C.data_ptr(), _ptr(D),
-                                          _ptr(z), _ptr(delta_bias), int(bool(delta_softplus)), out.data_ptr(),
-                                          strides, _stream(dev, stream)))
+    def call(st):
+        out = x.new_empty((batch, dim)) if y is None else y
+        _check(lib.ssm_state_update_cache(batch, dim, dstate, code, ref, slots, x.data_ptr(), delta.data_ptr(), a,
+                                          B.data_ptr(), C.data_ptr(), d, None if z is None else z.data_ptr(), bias,
+                                          int(bool(delta_softplus)), out.data_ptr(), strides, st))
         return out
 
     return _run(call, dev, stream)
@@ -287,50 +304,49 @@ def ssm_ssd_state_update_cache(cache: torch.Tensor, cache_slots: Optional[torch.
         raise ValueError("x must be (batch, nheads, headdim) and B (batch, ngroups, dstate)")
     batch, nheads, headdim = x.shape
     ngroups, dstate = B.shape[1], B.shape[2]
-    dev, ty = x.device, x.dtype
-    code = _dtype_code(x)
+    dev, ty, code = x.get_device(), x.dtype, _dtype_code(x)
     strides = RowStrides(_row_stride(x, "x", x.shape, ty, dev), _row_stride(dt, "dt", (batch, nheads), ty, dev),
-                         _row_stride(B, "B", B.shape, ty, dev), _row_stride(C, "C", B.shape, ty, dev),
+                         _row_stride(B, "B", B.shape, ty, dev), _row_stride(C, "C", (batch, ngroups, dstate), ty, dev),
                          0 if z is None else _row_stride(z, "z", x.shape, ty, dev),
                          0 if y is None else _row_stride(y, "y", x.shape, ty, dev))
-    _need(A, "A", (nheads,), torch.float32, dev)
-    _need(D, "D", (nheads,), torch.float32, dev, optional=True)
-    _need(dt_bias, "dt_bias", (nheads,), torch.float32, dev, optional=True)
+    if B.shape[0] != batch:
+        raise ValueError(f"B has shape {tuple(B.shape)}, expected {(batch, ngroups, dstate)}")
+    a = _dense(A, "A", (nheads,), torch.float32, dev)
+    d = _optional(D, "D", (nheads,), torch.float32, dev)
+    bias = _optional(dt_bias, "dt_bias", (nheads,), torch.float32, dev)
     ref = _cache(cache, "cache", (nheads, headdim, dstate), dev)
-    _indices(cache_slots, "cache_slots", batch, dev, ref.slots)
+    slots = _indices(cache_slots, "cache_slots", batch, dev, ref.slots)
 
-    def call():
-        out = torch.empty((batch, nheads, headdim), dtype=ty, device=dev) if y is None else y
-        _check(lib.ssm_ssd_state_update_cache(batch, nheads, headdim, dstate, ngroups, code, ref, _ptr(cache_slots),
-                                              x.data_ptr(), dt.data_ptr(), A.data_ptr(), B.data_ptr(), C.data_ptr(),
-                                              _ptr(D), _ptr(z), _ptr(dt_bias), int(bool(dt_softplus)),
-                                              out.data_ptr(), strides, _stream(dev, stream)))
+    def call(st):
+        out = x.new_empty((batch, nheads, headdim)) if y is None else y
+        _check(lib.ssm_ssd_state_update_cache(batch, nheads, headdim, dstate, ngroups, code, ref, slots, x.data_ptr(),
+                                              dt.data_ptr(), a, B.data_ptr(), C.data_ptr(), d,
+                                              None if z is None else z.data_ptr(), bias, int(bool(dt_softplus)),
+                                              out.data_ptr(), strides, st))
         return out
 
     return _run(call, dev, stream)
 
 
 def _q8(cache, cache_slots, codes, scales, store_slots):
-    """(cache descriptor, pairs, rows, dstate, stored entries) of a store or load, checked.  The cache's
-    entries are (rows, dstate) or (nheads, headdim, dstate)."""
+    """What a store or load needs, checked.  The cache's entries are (rows, dstate) or (nheads, headdim,
+    dstate)."""
     if cache.dim() not in (3, 4):
         raise ValueError("cache must be (slots, dim, dstate) or (slots, nheads, headdim, dstate)")
-    dev = cache.device
+    dev = cache.get_device()
     entry = tuple(cache.shape[1:])
     ref = _cache(cache, "cache", entry, dev)
     stored = codes.shape[0]
-    _need(codes, "codes", (stored,) + entry, torch.int8, dev)
-    _need(scales, "scales", (stored,) + entry[:-1], torch.float32, dev)
+    q = _dense(codes, "codes", (stored,) + entry, torch.int8, dev)
+    sc = _dense(scales, "scales", (stored,) + entry[:-1], torch.float32, dev)
     if cache_slots is None and store_slots is None:
         count = min(ref.slots, stored)
     else:
         count = (cache_slots if cache_slots is not None else store_slots).numel()
-    _indices(cache_slots, "cache_slots", count, dev, ref.slots)
-    _indices(store_slots, "store_slots", count, dev, stored)
-    rows = 1
-    for n in entry[:-1]:
-        rows *= n
-    return ref, count, rows, entry[-1], stored
+    slots = _indices(cache_slots, "cache_slots", count, dev, ref.slots)
+    where = _indices(store_slots, "store_slots", count, dev, stored)
+    rows = entry[0] if len(entry) == 2 else entry[0] * entry[1]
+    return dev, ref, count, rows, entry[-1], stored, q, sc, slots, where
 
 
 def ssm_cache_store_q8(cache: torch.Tensor, cache_slots: Optional[torch.Tensor], codes: torch.Tensor,
@@ -340,11 +356,8 @@ def ssm_cache_store_q8(cache: torch.Tensor, cache_slots: Optional[torch.Tensor],
     dstate) or (slots, nheads, headdim, dstate); codes: (stored,) + a slot's shape, int8; scales: the same
     without dstate, fp32.  Without either index pair i is slot i and entry i."""
     lib = load_library()
-    ref, count, rows, dstate, stored = _q8(cache, cache_slots, codes, scales, store_slots)
-    dev = cache.device
-    _run(lambda: _check(lib.ssm_cache_store_q8(count, rows, dstate, ref, _ptr(cache_slots), stored, codes.data_ptr(),
-                                               scales.data_ptr(), _ptr(store_slots), _stream(dev, stream))),
-         dev, stream)
+    dev, ref, count, rows, dstate, stored, q, sc, slots, where = _q8(cache, cache_slots, codes, scales, store_slots)
+    _run(lambda st: _check(lib.ssm_cache_store_q8(count, rows, dstate, ref, slots, stored, q, sc, where, st)), dev, stream)
 
 
 def ssm_cache_load_q8(codes: torch.Tensor, scales: torch.Tensor, store_slots: Optional[torch.Tensor],
@@ -352,8 +365,5 @@ def ssm_cache_load_q8(codes: torch.Tensor, scales: torch.Tensor, store_slots: Op
     """Reads entries store_slots of codes and scales back into cache_slots of the cache (include/ssm.h:
     ssm_cache_load_q8); an entry may be read into several slots."""
     lib = load_library()
-    ref, count, rows, dstate, stored = _q8(cache, cache_slots, codes, scales, store_slots)
-    dev = cache.device
-    _run(lambda: _check(lib.ssm_cache_load_q8(count, rows, dstate, stored, codes.data_ptr(), scales.data_ptr(),
-                                              _ptr(store_slots), ref, _ptr(cache_slots), _stream(dev, stream))),
-         dev, stream)
+    dev, ref, count, rows, dstate, stored, q, sc, slots, where = _q8(cache, cache_slots, codes, scales, store_slots)
+    _run(lambda st: _check(lib.ssm_cache_load_q8(count, rows, dstate, stored, q, sc, where, ref, slots, st)), dev, stream)
