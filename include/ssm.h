@@ -599,8 +599,10 @@ SSM_API ssm_status_t ssm_causal_conv1d_packed_fwd(const ssm_packed_t *seqs, int6
  *                   aligned, the caller's until the call's work is done (each
  *                   call that may run at the same time needs its own); may be
  *                   NULL where that is 0
- * Tensors need their element's alignment only; rows that allow 16-byte access
- * are faster.  The spans of y, the cache and the workspace must not overlap
+ * Tensors need their element's alignment only.  Row strides (and dim) are below
+ * 2^24 elements (else SSM_ERR_UNSUPPORTED).  dstate is 1, 2, 4, ..., 64.  The
+ * number of pieces, and so the last bits of a result, depends on total,
+ * sequences, max_seqlen and dim, never on what other sequences hold.  The spans of y, the cache and the workspace must not overlap
  * an input's or each other's.  Values of one sequence, NaN and infinity
  * included, never reach another.
  */

@@ -201,10 +201,16 @@ class Sequences {
   __device__ __forceinline__ Sequences(const int32_t* cu, const int32_t* slots, const uint8_t* has_initial,
                                        int64_t nseq, int64_t total, int64_t t)
       : cu_(cu), slots_(slots), has_initial_(has_initial), nseq_(nseq), total_(total), s0_(0) {
-    const int lane = threadIdx.x & 63;
-    int64_t n = 0;  // entries not above t: 64 compared at a time
-    for (int64_t i = 0; i <= nseq; i += 64) n += __popcll(__ballot(i + lane <= nseq && cu[i + lane] <= t));
-    read(n > 0 ? n - 1 : 0);
+    // the last entry not above t, 64 probes at a time: none up to 63 sequences, one round up to 4095
+    int64_t first = 0;
+    for (int64_t left = nseq + 1; left > 64;) {
+      const int64_t step = (left + 63) / 64, i = (threadIdx.x & 63) * step;
+      const int c = __popcll(__ballot(i < left && cu[first + (i < left ? i : 0)] <= t));
+      const int64_t skip = c > 0 ? (c - 1) * step : 0;
+      first += skip;
+      left = left - skip < step ? left - skip : step;
+    }
+    read(first);
   }
 
   __device__ __forceinline__ RowOwner owner(int64_t t) {

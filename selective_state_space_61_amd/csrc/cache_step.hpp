@@ -116,7 +116,7 @@ __global__ __launch_bounds__(kStepThreads) void state_update_cache_kernel(const 
       if (ok && at[i] >= 0) st[i].store(p.cache.data, at[i] + d * N + n0);
       yp = group_sum<TPC>(yp);
       if (ok && at[i] >= 0 && n0 == 0) {
-        float yv = fmaf(dsk, xv, yp);
+        float yv = p.Dskip ? fmaf(dsk, xv, yp) : yp;
         if (has_z) yv *= M::gate(zr[i].get(0));
         store_one<BF16>(p.y, b[i] * p.sy + d, yv);
       }
@@ -283,7 +283,7 @@ __global__ __launch_bounds__(kStepThreads) void ssd_state_update_cache_kernel(co
       if (ok[u]) st[u].store(p.cache.data, off[u]);
       yp = group_sum<TPC>(yp);
       if (ok[u] && n0 == 0) {
-        float yv = fmaf(dsk, xv[u], yp);
+        float yv = p.D ? fmaf(dsk, xv[u], yp) : yp;
         if (p.z) yv *= M::gate(zv[u]);
         store_one<BF16>(p.y, b * p.sy + static_cast<int64_t>(h) * P + p0 + u * CPB, yv);
       }

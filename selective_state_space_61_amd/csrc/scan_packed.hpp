@@ -188,8 +188,8 @@ __global__ __launch_bounds__(64 * kPackedWaves, packed_states(N) <= 16 ? 4 : 2) 
   const int64_t rows = uniform64(pc.r1) - row_base;
   if (seq < 0 || rows <= 0) return;
   if (AGG && kth + 1 == npieces) return;
-  const int64_t nchunks = (rows + CH - 1) / CH;
-  const int last_row = static_cast<int>(rows - 1 - (nchunks - 1) * CH);  // of the last chunk
+  const int nchunks = static_cast<int>((rows + CH - 1) / CH);
+  const int last_row = static_cast<int>(rows - 1 - static_cast<int64_t>(nchunks - 1) * CH);  // of the last chunk
 
   // the lane's channel and states in the recurrence
   const int r = lane >> 4, k = lane & 15;
@@ -263,7 +263,7 @@ __global__ __launch_bounds__(64 * kPackedWaves, packed_states(N) <= 16 ? 4 : 2) 
     return static_cast<uint32_t>(row) * static_cast<uint32_t>(stride * ES) + static_cast<uint32_t>(col * ES);
   };
   const int lrow = lane >> 2, lcol = (lane & 3) * V;  // the row and channels that this lane loads
-  const bool has_z = !AGG && p.z != nullptr;
+  const bool has_z = !AGG && p.z != nullptr, has_d = !AGG && p.Dskip != nullptr;
   const void* zsrc = has_z ? p.z : p.x;  // without a gate z is read from x and never used
   const int64_t zstride = has_z ? p.sz : p.sx;
 
@@ -281,7 +281,7 @@ __global__ __launch_bounds__(64 * kPackedWaves, packed_states(N) <= 16 ? 4 : 2) 
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       bias[v] = p.delta_bias && v < pv ? p.delta_bias[col + v] : 0.0f;
-      dsk[v] = !AGG && p.Dskip && v < pv ? p.Dskip[col + v] : 0.0f;
+      dsk[v] = has_d && v < pv ? p.Dskip[col + v] : 0.0f;
       dsum[v] = 0.0f;
     }
     const int row1 = lrow < last_row ? lrow : last_row, k1 = k < last_row ? k : last_row;
@@ -317,7 +317,7 @@ __global__ __launch_bounds__(64 * kPackedWaves, packed_states(N) <= 16 ? 4 : 2) 
     };
     if (nchunks == 1) last_offsets();
     load();
-    for (int64_t c = 0; c < nchunks; ++c) {
+    for (int c = 0; c < nchunks; ++c) {
       // ---- the chunk's values, from the registers loaded a chunk ago
       const bool full = c + 1 < nchunks || last_row == CH - 1;
       float dt[V], xv[V];
@@ -345,13 +345,16 @@ __global__ __launch_bounds__(64 * kPackedWaves, packed_states(N) <= 16 ? 4 : 2) 
 #pragma unroll
         for (int j = 0; j < NPL; ++j) Bv[j] = k <= last_row ? Bv[j] : 0.0f;
       }
-      float gate[V];
+      float gate[V], skip[V];
       if constexpr (AGG) {
 #pragma unroll
         for (int v = 0; v < V; ++v) dsum[v] += dt[v];
       } else {
 #pragma unroll
-        for (int v = 0; v < V; ++v) gate[v] = has_z ? silu_f32(nz.get(v)) : 1.0f;
+        for (int v = 0; v < V; ++v) {
+          gate[v] = has_z ? silu_f32(nz.get(v)) : 1.0f;
+          skip[v] = has_d ? dsk[v] * xv[v] : 0.0f;  // (without D an infinite x adds nothing here)
+        }
       }
       if constexpr (kWhole) {
         float4* const qd = reinterpret_cast<float4*>(s_dw + lrow * 16 + lcol);
@@ -359,15 +362,15 @@ __global__ __launch_bounds__(64 * kPackedWaves, packed_states(N) <= 16 ? 4 : 2) 
         qd[1] = make_float4(dt[2], dt[2] * xv[2], dt[3], dt[3] * xv[3]);
         if constexpr (!AGG) {
           float4* const qx = reinterpret_cast<float4*>(s_xg + lrow * 16 + lcol);
-          qx[0] = make_float4(dsk[0] * xv[0], gate[0], dsk[1] * xv[1], gate[1]);
-          qx[1] = make_float4(dsk[2] * xv[2], gate[2], dsk[3] * xv[3], gate[3]);
+          qx[0] = make_float4(skip[0], gate[0], skip[1], gate[1]);
+          qx[1] = make_float4(skip[2], gate[2], skip[3], gate[3]);
         }
       } else {
 #pragma unroll
         for (int v = 0; v < V; ++v) {
           if (v >= pv || wcol + v < 0) continue;
           s_dw[lrow * 16 + wcol + v] = make_float2(dt[v], dt[v] * xv[v]);
-          if constexpr (!AGG) s_xg[lrow * 16 + wcol + v] = make_float2(dsk[v] * xv[v], gate[v]);
+          if constexpr (!AGG) s_xg[lrow * 16 + wcol + v] = make_float2(skip[v], gate[v]);
         }
       }
       if constexpr (kMatrix) {
@@ -387,6 +390,10 @@ __global__ __launch_bounds__(64 * kPackedWaves, packed_states(N) <= 16 ? 4 : 2) 
       // ---- 16 steps, four at a time
       [[maybe_unused]] float yp[4];
       auto finish = [&](int t) {  // read-outs of steps t .. t + 3
+        if constexpr (N < 4) {  // a padding state that an infinity made NaN counts for nothing
+#pragma unroll
+          for (int u = 0; u < 4; ++u) yp[u] = r < N ? yp[u] : 0.0f;
+        }
         const float y = sum_rows4(yp);
         const float2 xg = s_xg[(t + r) * 16 + k];
         s_y[(t + r) * 16 + k] = (y + xg.x) * xg.y;

@@ -32,6 +32,11 @@ from . import SSM_BF16, SSM_F32, Cache, Packed, RowStrides, _check, _dtype_code,
 # are compared by index, and what is wrong is worked out only once something is.
 
 
+# the current stream's handle; the public call makes a Stream object first, which takes a microsecond
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda device: torch.cuda.current_stream(device).cuda_stream)
+
+
 def _refuse(t, name: str, shape, dtype, device: int) -> None:
     if t is None:
         raise ValueError(f"{name} is required")
@@ -133,9 +138,9 @@ def _run(call, device: int, stream):
     if device < 0:
         raise ValueError("the tensors are on the host, expected a GPU")
     if stream is None and torch.cuda.current_device() == device:
-        return call(torch.cuda.current_stream(device).cuda_stream)
+        return call(_raw_stream(device))
     with _other(device, stream):
-        return call(torch.cuda.current_stream(device).cuda_stream)
+        return call(_raw_stream(device))
 
 
 def ssm_causal_conv1d_packed_fwd(x: torch.Tensor, weight: torch.Tensor, cu_seqlens: torch.Tensor,

@@ -677,3 +677,35 @@ def test_no_rows_no_sequences(ssm):
     y0 = torch.full((3, 8), SENTINEL, device="cuda")
     ssm.ssm_causal_conv1d_packed_fwd(x, z(8, 4, device="cuda"), i32([0]), y=y0)
     assert (y0 == SENTINEL).all()
+
+
+@pytest.mark.parametrize("nseq", [63, 64, 65, 300, 5000])
+def test_conv_packed_finds_every_sequence(ssm, nseq):
+    # the search for a tile's first sequence: 64 probes a round; empty sequences among them
+    lens = [(i * 7) % 5 for i in range(nseq)]
+    total, dim = sum(lens), 8
+    m = Maker(nseq)
+    x, w = m.normal((total, dim)), m.normal((dim, 4))
+    pool = m.normal((nseq, dim, 3))
+    before = pool.clone()
+    y = ssm.ssm_causal_conv1d_packed_fwd(x, w, cu_of(lens), None, False, cache=pool,
+                                         has_initial=torch.ones(nseq, dtype=torch.bool, device="cuda"))
+    lines, out = [], []
+    r0 = 0
+    for i, L in enumerate(lens):
+        line = torch.cat([R.f64(before[i]).T, R.f64(x[r0:r0 + L])])
+        out.append(R.conv_rows(line, R.f64(w), None, False))
+        lines.append(line[line.shape[0] - 3:].T.float())
+        r0 += L
+    R.check(y, torch.cat([o[0] for o in out]), torch.cat([o[1] for o in out]), torch.float32, f"{nseq} sequences")
+    assert torch.equal(pool.cpu(), torch.stack(lines))
+
+
+def test_scan_packed_infinite_input_and_padding_states(ssm):
+    # dstate 1 and 2 are computed as 4: an infinite input gives the infinities of the formula, not NaN
+    for n in (1, 2):
+        x = torch.zeros(6, 20, device="cuda")
+        x[2] = float("inf")
+        one = torch.ones(6, n, device="cuda")
+        y = ssm.ssm_scan_packed_fwd(x, torch.ones_like(x), -torch.ones(20, n, device="cuda"), one, one, cu_of([6]))
+        assert (y[:2] == 0).all() and torch.isinf(y[2:]).all()
