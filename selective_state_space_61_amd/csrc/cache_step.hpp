@@ -66,6 +66,9 @@ constexpr int kStepStates = CB16 ? (N < 8 ? N : 8) : (N < 4 ? N : 4);
 
 // A thread owns SPT consecutive states of a channel, N / SPT lanes a channel, in R entries of
 // the batch: A, D and the bias serve all of them, and their states' loads are in flight together.
+// Bound by the states' traffic: 250 entries of 5120 x 16 take 33.3 us with fp32 states (174 MB, 5.2 TB/s,
+// a copy's rate) and 21.5 us with bf16 ones (92 MB, 4.3 TB/s), with R 1 | 2 | 4 | 8 23.7 | 22.5 | 21.5 |
+// 25.8 us; with 32 bytes of state a lane 24.2 us.
 template <bool BF16, bool CB16, int N, int R>
 __global__ __launch_bounds__(kStepThreads) void state_update_cache_kernel(const StepArgs p) {
   constexpr int SPT = kStepStates<CB16, N>, TPC = N / SPT;
@@ -140,7 +143,8 @@ struct ConvStepArgs {
 constexpr int kConvStepVec = 4;  // channels per thread
 
 // A thread owns 4 channels of R entries: an entry's windows are 4 (K - 1) consecutive elements, and the
-// weights serve all R.
+// weights serve all R.  250 entries of 5120 channels, width 4, bf16: 7.4 us (20 MB; 13 us with R 1 and the
+// weights loaded one by one): the launch and one round trip to memory are half of it.
 template <bool BF16, int K, int R>
 __global__ __launch_bounds__(kStepThreads) void conv1d_update_cache_kernel(const ConvStepArgs p) {
   constexpr int V = kConvStepVec, W = K - 1, E = W > 0 ? V * W : 2;
@@ -231,7 +235,9 @@ template <bool CB16, int N>
 constexpr int kSsdStepChannels = kSsdStepUnroll * kStepThreads * (CB16 ? 8 : 4) / N;
 
 // One workgroup: a stretch of the channels of one head of one entry.  N / SPT lanes share a
-// channel; each lane's B and C values serve all of the channels that it takes.
+// channel; each lane's B and C values serve all of the channels that it takes, whose states' loads are in
+// flight together.  Bound by the states' traffic: 96 entries of 64 heads x 64 x 128 in fp32 take 75.5 us
+// (406 MB, 5.4 TB/s, a copy's rate).
 template <bool BF16, bool CB16, int N>
 __global__ __launch_bounds__(kStepThreads) void ssd_state_update_cache_kernel(const SsdStepArgs p) {
   constexpr int SPT = CB16 ? 8 : 4;

@@ -38,14 +38,16 @@ struct ConvPackedArgs {
 // Rows per tile: 32 (a sequence's 3 rows before a tile are a tenth of its reads), or 8 where that leaves
 // fewer than two workgroups a CU, or where sequences are shorter than a tile on average (a tile takes
 // its sequences one after another, about 2.5 us each).  bf16, us with 8 | 32: 171 rows of 1536 channels
-// 8.3 | 16.0, 1000 of 1536 9.3 | 14.9, 4288 of 1536 16.6 | 16.6, 12288 of 5120 80 | 55 (4.6 TB/s).
+// 8.0 | 15.5, 1000 of 1536 9.0 | 14.6, 4288 of 1536 13.2 | 16.0, 16384 of 1536 31 | 22.6 (4.4 TB/s; 25.8
+// with the tiles dealt round robin to the XCDs), 12288 of 5120 78 | 55 (4.6 TB/s).
 constexpr int kPackTile = 32, kPackTileSmall = 8;
 
 template <bool BF16, int K, int T>
 __global__ __launch_bounds__(kConvThreads) void conv1d_packed_kernel(const ConvPackedArgs p) {
   constexpr int V = kConvVec<BF16>, W = K - 1, WN = W > 0 ? W : 1;
-  const int64_t tile = blockIdx.x / p.ncb;
-  const int64_t d0 = (static_cast<int64_t>(blockIdx.x % p.ncb) * kConvThreads + threadIdx.x) * V;
+  const int64_t blk = xcd_local(blockIdx.x, gridDim.x);  // a tile's last rows are the next one's first reads: one L2
+  const int64_t tile = blk / p.ncb;
+  const int64_t d0 = (blk % p.ncb * kConvThreads + threadIdx.x) * V;
   const int64_t t0 = tile * T;
   const int64_t t1 = t0 + T < p.total ? t0 + T : p.total;
   // lanes without channels (nv 0) take part in the search for sequences

@@ -18,7 +18,13 @@
 //     group.  Rows of y go out as the rows of x came in.
 // There are no barriers.  A sequence's channels are many small independent waves, several per
 // SIMD, which cover each other's latencies and fill whatever CUs are free: with ragged prompts that
-// balances better than workgroups that own a CU.
+// balances better than workgroups that own a CU.  What bounds it is VALU issue: 449 VALU instructions
+// per chunk, of them 80 transcendental ones (about 11 cycles each) and 128 with DPP operands (about 5), are
+// nearly all of the 149 cycles that a row takes a SIMD with three waves.  bf16, dstate 16: 32 prompts
+// of 2048 x 1536 393 us (the dense scan's workgroups, one per CU: 490), 11 ragged ones of 11003 x 1536
+// 126 us (workgroups of scan_rows.hpp's kind, in pieces or not: 176), one of 8192 x 1536 97 us (123).  Eight
+// equal prompts of 2048 x 1536 fill the SIMDs with fewer than one wave each and take 179 us, where the
+// dense scan's wave specialisation takes 122: equal lengths are its case.
 //
 // Pieces.  Few long prompts have too few waves, so sequences are cut into pieces of `piece` rows: a
 // first launch (AGG) runs every piece but a sequence's last one without read-outs and leaves its end
