@@ -602,9 +602,10 @@ SSM_API ssm_status_t ssm_causal_conv1d_packed_fwd(const ssm_packed_t *seqs, int6
  * Tensors need their element's alignment only.  Row strides (and dim) are below
  * 2^24 elements (else SSM_ERR_UNSUPPORTED).  dstate is 1, 2, 4, ..., 64.  The
  * number of pieces, and so the last bits of a result, depends on total,
- * sequences, max_seqlen and dim, never on what other sequences hold.  The spans of y, the cache and the workspace must not overlap
- * an input's or each other's.  Values of one sequence, NaN and infinity
- * included, never reach another.
+ * sequences, max_seqlen and dim, never on what other sequences hold.  The
+ * spans of y, the cache and the workspace must not overlap an input's or each
+ * other's.  Values of one sequence, NaN and infinity included, never reach
+ * another.
  */
 SSM_API ssm_status_t ssm_scan_packed_fwd(const ssm_packed_t *seqs, int64_t dim, int64_t dstate, ssm_dtype_t dtype,
                                          const void *x, const void *delta, const float *A, const void *B,

@@ -201,9 +201,9 @@ ssm_status_t q8_call(bool store, int64_t count, int64_t rows, int64_t dstate, co
   const bool cb16 = cache->dtype == SSM_BF16;
   const Q8Kernel k = cb16 ? q8_kernel<true>(store, dstate) : q8_kernel<false>(store, dstate);
   if (!k) return fail(SSM_ERR_UNSUPPORTED, "dstate %lld is not a power of two up to 256", (long long)dstate);
-  int64_t entry, n_codes, n_scales, threads;
-  if (!mul_ok(rows, dstate, &entry) || !mul_ok(entry, stored, &n_codes) || !mul_ok(rows * 4, stored, &n_scales) ||
-      !mul_ok(entry, 4, &threads))
+  int64_t entry, entry_bytes, n_codes, n_scales;
+  if (!mul_ok(rows, dstate, &entry) || !mul_ok(entry, 4, &entry_bytes) || !mul_ok(entry, stored, &n_codes) ||
+      !mul_ok(rows * 4, stored, &n_scales))
     return fail(SSM_ERR_INVALID_ARG, "tensor size overflows int64");
   ssm::Q8Args a{};
   Range rc;

@@ -102,7 +102,7 @@ def _indices(t: Optional[torch.Tensor], name: str, count: int, device: int, slot
 
 
 def _packed(cu_seqlens, cache_slots, has_initial, total: int, ref: Optional[Cache], max_seqlen: int, device: int) -> Packed:
-    if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
+    if cu_seqlens is None or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
         raise ValueError("cu_seqlens must hold one more entry than there are sequences")
     nseq = cu_seqlens.numel() - 1
     cu = _dense(cu_seqlens, "cu_seqlens", (nseq + 1,), torch.int32, device)

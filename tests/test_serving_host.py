@@ -96,7 +96,8 @@ def test_packed_sizes(lib, call, kw):
 @pytest.mark.parametrize("call,kw", [(conv_packed, dict(dim=-1)), (scan_packed, dict(dim=-1)), (conv_step, dict(batch=-1)),
                                      (scan_step, dict(batch=-1)), (scan_step, dict(dim=-2)), (ssd_step, dict(heads=0)),
                                      (ssd_step, dict(batch=1 << 31)), (scan_packed, dict(dstate=-16)),
-                                     (store, dict(count=-1)), (load, dict(stored=-1))])
+                                     (store, dict(count=-1)), (load, dict(stored=-1)),
+                                     (store, dict(rows=1 << 62, dstate=1))])
 def test_bad_sizes(lib, call, kw):
     assert call(lib, **kw) == INVALID
 
@@ -214,7 +215,7 @@ def good_scan():
 @pytest.mark.parametrize("name,value,exc", [
     ("x", t(2, 6, 8), ValueError), ("delta", t(6, 7), ValueError), ("B", t(6, 8), ValueError),
     ("C", t(6, 16, dtype=torch.bfloat16), TypeError), ("A", t(8, 16, dtype=torch.bfloat16), TypeError),
-    ("cu_seqlens", t(3), TypeError), ("cu_seqlens", t(0, dtype=torch.int32), ValueError),
+    ("cu_seqlens", None, ValueError), ("cu_seqlens", t(3), TypeError), ("cu_seqlens", t(0, dtype=torch.int32), ValueError),
     ("cu_seqlens", t(1, 3, dtype=torch.int32), ValueError), ("x", t(8, 6).T, ValueError),
     ("z", t(6, 9), ValueError), ("z", t(1, 8).expand(6, 8), ValueError), ("D", t(9), ValueError),
     ("cache", t(4, 8, 15), ValueError), ("cache", t(4, 8, 16, dtype=torch.float16), TypeError),
