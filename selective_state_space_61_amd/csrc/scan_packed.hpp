@@ -10,21 +10,22 @@
 //   * the lanes load x, delta and z as (row lane / 4, four channels), one chunk ahead, and write
 //     (dt, dt x) and (D x, silu z) to a part of the LDS that is the wave's own;
 //   * lane k of row r loads step k's B and C of its NPL states: each step takes them through DPP
-//     row broadcasts, so they need no LDS;
-//   * 16 steps of step_readout (ssm_device.hpp);
+//     row broadcasts, so they need no LDS (but B goes there where the matrix cores take it, dstate 16);
+//   * 16 steps of step_readout (ssm_device.hpp), or of decay_readout4 with the input terms from the
+//     matrix cores;
 //   * the read-outs of four steps, each spread over the four rows of lanes, are added with two
 //     lane swaps and two adds a pair (v_permlane16_swap, v_permlane32_swap), which leaves step
 //     t + r's sum in row r: skip term, gate and rounding then run once per value, not per state
 //     group.  Rows of y go out as the rows of x came in.
 // There are no barriers.  A sequence's channels are many small independent waves, several per
 // SIMD, which cover each other's latencies and fill whatever CUs are free: with ragged prompts that
-// balances better than workgroups that own a CU.  What bounds it is VALU issue: 449 VALU instructions
-// per chunk, of them 80 transcendental ones (about 11 cycles each) and 128 with DPP operands (about 5), are
-// nearly all of the 149 cycles that a row takes a SIMD with three waves.  bf16, dstate 16: 32 prompts
-// of 2048 x 1536 393 us (the dense scan's workgroups, one per CU: 490), 11 ragged ones of 11003 x 1536
-// 126 us (workgroups of scan_rows.hpp's kind, in pieces or not: 176), one of 8192 x 1536 97 us (123).  Eight
-// equal prompts of 2048 x 1536 fill the SIMDs with fewer than one wave each and take 179 us, where the
-// dense scan's wave specialisation takes 122: equal lengths are its case.
+// balances better than workgroups that own a CU.  What bounds it is VALU issue: 395 VALU instructions
+// per chunk, of them 80 transcendental ones, keep a SIMD with three waves busy for 82% of its cycles, and
+// the matrix cores for 5%.  bf16, dstate 16: 32 prompts of 2048 x 1536 375 us (the dense scan's workgroups,
+// one per CU: 490), 11 ragged ones of 11003 x 1536 122 us (workgroups of scan_rows.hpp's kind, in pieces
+// or not: 176), one of 8192 x 1536 92 us (123).  Eight equal prompts of 2048 x 1536 fill the SIMDs with
+// fewer than one wave each and take 172 us, where the dense scan's wave specialisation takes 122: equal
+// lengths are its case.
 //
 // Pieces.  Few long prompts have too few waves, so sequences are cut into pieces of `piece` rows: a
 // first launch (AGG) runs every piece but a sequence's last one without read-outs and leaves its end
@@ -137,6 +138,31 @@ __device__ __forceinline__ void step_state(float dt, float w, const float* a2, c
   for (int j = 0; j < NPL; ++j) h[j] = fmaf(hw_exp2(dt * a2[j]), h[j], row_bcast<K>(b[j]) * w);
 }
 
+// What a step needs besides its input term: its decays e[j] = exp2(dt a2[j]) and, while h is still the
+// state before it, the read-out of the step before, sum_j C[j] h[j].  DPP operands and exponentials are at
+// least two instructions old where they are read or the block ends, as in step_readout.
+template <int KC>
+__device__ __forceinline__ float decay_readout4(float dt, const float* a2, const float* c, const float* h, float (&e)[4]) {
+  float yp;
+  asm("v_mul_f32 %[e0], %[dt], %[a0]\n\t"
+      "v_mul_f32 %[e1], %[dt], %[a1]\n\t"
+      "v_mul_f32 %[e2], %[dt], %[a2]\n\t"
+      "v_mul_f32 %[e3], %[dt], %[a3]\n\t"
+      "v_exp_f32 %[e0], %[e0]\n\t"
+      "v_exp_f32 %[e1], %[e1]\n\t"
+      "v_exp_f32 %[e2], %[e2]\n\t"
+      "v_exp_f32 %[e3], %[e3]\n\t"
+      "v_mul_f32_dpp %[yp], %[c0], %[h0] row_newbcast:%[kc] row_mask:0xf bank_mask:0xf\n\t"
+      "v_fmac_f32_dpp %[yp], %[c1], %[h1] row_newbcast:%[kc] row_mask:0xf bank_mask:0xf\n\t"
+      "v_fmac_f32_dpp %[yp], %[c2], %[h2] row_newbcast:%[kc] row_mask:0xf bank_mask:0xf\n\t"
+      "v_fmac_f32_dpp %[yp], %[c3], %[h3] row_newbcast:%[kc] row_mask:0xf bank_mask:0xf"
+      : [e0] "=&v"(e[0]), [e1] "=&v"(e[1]), [e2] "=&v"(e[2]), [e3] "=&v"(e[3]), [yp] "=&v"(yp)
+      : [dt] "v"(dt), [a0] "v"(a2[0]), [a1] "v"(a2[1]), [a2] "v"(a2[2]), [a3] "v"(a2[3]), [c0] "v"(c[0]),
+        [c1] "v"(c[1]), [c2] "v"(c[2]), [c3] "v"(c[3]), [h0] "v"(h[0]), [h1] "v"(h[1]), [h2] "v"(h[2]), [h3] "v"(h[3]),
+        [kc] "i"(KC));
+  return yp;
+}
+
 // Orders a wave's LDS writes before its other lanes' reads (LDS serves a wave in order: this only
 // keeps the compiler from moving them)
 __device__ __forceinline__ void wave_lds_fence() {
@@ -161,7 +187,7 @@ __device__ __forceinline__ float sum_rows4(const float (&v)[4]) {
   return pair(__builtin_amdgcn_permlane32_swap(bits(a), bits(b), false, false));
 }
 
-typedef float f32x4_t __attribute__((ext_vector_type(4)));
+typedef float f32x16_t __attribute__((ext_vector_type(16)));
 
 constexpr int kPackedWaves = 4;               // waves (of 16 channels) per workgroup
 constexpr int kPackedChunk = 16;              // rows per chunk: lanes of a DPP row
@@ -170,17 +196,19 @@ constexpr int packed_states(int N) { return N < 4 ? 4 : N; }
 template <bool BF16, int N, bool AGG>
 __global__ __launch_bounds__(64 * kPackedWaves, packed_states(N) <= 16 ? 4 : 2) void scan_packed_kernel(const ScanPackedArgs p) {
   constexpr int NPL = packed_states(N) / 4, CH = kPackedChunk, ES = BF16 ? 2 : 4, V = 4;
-  constexpr bool kMatrix = AGG && NPL % 4 == 0;  // B (dt x) on the matrix cores
-  constexpr int NP = packed_states(N), QN = kMatrix ? NPL / 4 : 1;
-  constexpr int BS = CH + 4;  // floats between states of s_b: 16-byte reads hit a bank at most twice
-  __shared__ float4 s_dw_[kPackedWaves][CH * 8];                         // (dt, dt x): [row][channel] float2
+  constexpr bool kOuter = N == 16;  // B (dt x) by the matrix cores
+  constexpr int BS = CH + 4;  // floats between states of s_b: 64 lanes read 16 states of 4 rows from 64 banks
+  // dt and dt x: [row][channel] float2, or (kOuter) all of dt before all of dt x
+  __shared__ float4 s_dw_[kPackedWaves][CH * 8];
   __shared__ float4 s_xg_[kPackedWaves][AGG ? 1 : CH * 8];               // (D x, silu z)
   __shared__ float4 s_y_[kPackedWaves][AGG ? 1 : CH * 4];                // y: [row][channel]
-  __shared__ float4 s_b_[kPackedWaves][kMatrix ? NP * BS / 4 : 1];       // B: [state][row]
+  __shared__ float4 s_b_[kPackedWaves][kOuter ? N * BS / 4 : 1];         // B: [state][row]
 
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   float2* const s_dw = reinterpret_cast<float2*>(s_dw_[wave]);
+  [[maybe_unused]] float* const s_dt = reinterpret_cast<float*>(s_dw_[wave]);
+  [[maybe_unused]] float* const s_w = s_dt + CH * 16;
   float2* const s_xg = reinterpret_cast<float2*>(s_xg_[wave]);
   float* const s_y = reinterpret_cast<float*>(s_y_[wave]);
   [[maybe_unused]] float* const s_b = reinterpret_cast<float*>(s_b_[wave]);
@@ -363,9 +391,15 @@ __global__ __launch_bounds__(64 * kPackedWaves, packed_states(N) <= 16 ? 4 : 2) 
         }
       }
       if constexpr (kWhole) {
-        float4* const qd = reinterpret_cast<float4*>(s_dw + lrow * 16 + lcol);
-        qd[0] = make_float4(dt[0], dt[0] * xv[0], dt[1], dt[1] * xv[1]);
-        qd[1] = make_float4(dt[2], dt[2] * xv[2], dt[3], dt[3] * xv[3]);
+        if constexpr (kOuter) {
+          *reinterpret_cast<float4*>(s_dt + lrow * 16 + lcol) = make_float4(dt[0], dt[1], dt[2], dt[3]);
+          *reinterpret_cast<float4*>(s_w + lrow * 16 + lcol) =
+              make_float4(dt[0] * xv[0], dt[1] * xv[1], dt[2] * xv[2], dt[3] * xv[3]);
+        } else {
+          float4* const qd = reinterpret_cast<float4*>(s_dw + lrow * 16 + lcol);
+          qd[0] = make_float4(dt[0], dt[0] * xv[0], dt[1], dt[1] * xv[1]);
+          qd[1] = make_float4(dt[2], dt[2] * xv[2], dt[3], dt[3] * xv[3]);
+        }
         if constexpr (!AGG) {
           float4* const qx = reinterpret_cast<float4*>(s_xg + lrow * 16 + lcol);
           qx[0] = make_float4(skip[0], gate[0], skip[1], gate[1]);
@@ -375,11 +409,16 @@ __global__ __launch_bounds__(64 * kPackedWaves, packed_states(N) <= 16 ? 4 : 2) 
 #pragma unroll
         for (int v = 0; v < V; ++v) {
           if (v >= pv || wcol + v < 0) continue;
-          s_dw[lrow * 16 + wcol + v] = make_float2(dt[v], dt[v] * xv[v]);
+          if constexpr (kOuter) {
+            s_dt[lrow * 16 + wcol + v] = dt[v];
+            s_w[lrow * 16 + wcol + v] = dt[v] * xv[v];
+          } else {
+            s_dw[lrow * 16 + wcol + v] = make_float2(dt[v], dt[v] * xv[v]);
+          }
           if constexpr (!AGG) s_xg[lrow * 16 + wcol + v] = make_float2(skip[v], gate[v]);
         }
       }
-      if constexpr (kMatrix) {
+      if constexpr (kOuter) {
 #pragma unroll
         for (int j = 0; j < NPL; ++j) s_b[(n0 + j) * BS + k] = Bv[j];
       }
@@ -404,48 +443,60 @@ __global__ __launch_bounds__(64 * kPackedWaves, packed_states(N) <= 16 ? 4 : 2) 
         const float2 xg = s_xg[(t + r) * 16 + k];
         s_y[(t + r) * 16 + k] = (y + xg.x) * xg.y;
       };
-      float2 dw[2][4];
-      auto read_dw = [&](int t, float2 (&w)[4]) {
+      if constexpr (kOuter) {
+        // The input terms B (x) dt x of four steps are one 16x16x1 matrix instruction of four blocks: in
+        // block b lane 16 b + m has B of step t + b, state m and dt x of channel m; of the result,
+        // register 4 b + j of lane 16 r + k is step t + b, state 4 r + j, channel k: the recurrence's
+        // own layout.  (A product of one term with a zero addend: rounded once, like a multiplication.)
+        // It does not wait for the state, so the next four steps' goes out in the middle of these
+        // four; the barrier keeps the compiler from moving it to where its result is used, at the
+        // price of its whole latency.  bf16, us against the terms by DPP operands in every step: 32
+        // prompts of 2048 x 1536 374 | 392, 8 of 2048 172 | 178, one of 8192 92 | 96.  dstate 32 and 64
+        // have no registers for the results of two groups (64: 536 | 480 us for 8 of 2048), and one
+        // 4x4x1 instruction a step with exp(dt A) h as its addend is no faster than DPP (187 | 178).
+        // The read-outs stay off the matrix cores: with them there too a full pass took 498 us for 397.
+        const float* const t_b = s_b + k * BS + r;
+        const float* const t_w = s_w + r * 16 + k;
+        float dq[2][4];
+        auto read_dt = [&](int t, float (&v)[4]) {
 #pragma unroll
-        for (int u = 0; u < 4; ++u) w[u] = s_dw[(t + u) * 16 + k];
-      };
-      read_dw(0, dw[0]);
-      if constexpr (kMatrix) {
-        // h <- exp(dt A) h + B (x) dt x: the outer product of a step's B with the 16 channels' dt x is
-        // one 4x4x1 matrix instruction of 16 blocks: block (r, k / 4) has states NPL r + 4 q .. + 3 and
-        // channels 4 (k / 4) .. + 3, and exp(dt A) h as its addend; lane l holds B of state
-        // NPL r + 4 q + l % 4.  40 us against 45 us with the DPP form for 7936 rows of 1536 channels.
-        // (The read-outs stay off the matrix cores: with them there too, at 8 cycles an instruction
-        // that no VALU work of other waves hid, a full pass took 498 us in place of 397.)
-        const float* const t_b = s_b + (n0 + (lane & 3)) * BS;
-        float4 bq[2][QN];  // B of four steps
-        auto read_b = [&](int t, float4 (&b)[QN]) {
-#pragma unroll
-          for (int q = 0; q < QN; ++q) b[q] = *reinterpret_cast<const float4*>(t_b + 4 * q * BS + t);
+          for (int u = 0; u < 4; ++u) v[u] = s_dt[(t + u) * 16 + k];
         };
-        read_b(0, bq[0]);
+        read_dt(0, dq[0]);
+        float ob = t_b[0], ow = t_w[0];
+        f32x16_t in[2];
+        in[0] = __builtin_amdgcn_mfma_f32_16x16x1f32(ob, ow, f32x16_t{}, 0, 0, 0);
+        ob = t_b[4], ow = t_w[4 * 16];
         static_for<CH / 4>([&](auto G) {
           constexpr int t = decltype(G)::value * 4, i = decltype(G)::value & 1;
-          if constexpr (t + 4 < CH) {
-            read_dw(t + 4, dw[i ^ 1]);
-            read_b(t + 4, bq[i ^ 1]);
-          }
+          if constexpr (t + 4 < CH) read_dt(t + 4, dq[i ^ 1]);
           static_for<4>([&](auto U) {
-            constexpr int u = decltype(U)::value;
-            const float2 w = dw[i][u];
-#pragma unroll
-            for (int q = 0; q < QN; ++q) {
-              f32x4_t s;
-#pragma unroll
-              for (int j = 0; j < 4; ++j) s[j] = hw_exp2(w.x * A2[4 * q + j]) * h[4 * q + j];
-              const float b = u == 0 ? bq[i][q].x : u == 1 ? bq[i][q].y : u == 2 ? bq[i][q].z : bq[i][q].w;
-              s = __builtin_amdgcn_mfma_f32_4x4x1f32(b, w.y, s, 0, 0, 0);
-#pragma unroll
-              for (int j = 0; j < 4; ++j) h[4 * q + j] = s[j];
+            constexpr int u = decltype(U)::value, s = t + u;
+            const float d = dq[i][u];
+            if constexpr (u == 1 && t + 4 < CH) {
+              in[i ^ 1] = __builtin_amdgcn_mfma_f32_16x16x1f32(ob, ow, f32x16_t{}, 0, 0, 0);
+              if constexpr (t + 8 < CH) ob = t_b[t + 8], ow = t_w[(t + 8) * 16];
+              __builtin_amdgcn_sched_barrier(0);
             }
+            float e[4];
+            if constexpr (AGG || s == 0) {
+#pragma unroll
+              for (int j = 0; j < 4; ++j) e[j] = hw_exp2(d * A2[j]);
+            } else {
+              yp[(s - 1) & 3] = decay_readout4<s - 1>(d, A2, Cv, h, e);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) h[j] = fmaf(e[j], h[j], in[i][4 * u + j]);
+            if constexpr (!AGG && s > 0 && s % 4 == 0) finish(s - 4);
           });
         });
       } else {
+        float2 dw[2][4];
+        auto read_dw = [&](int t, float2 (&w)[4]) {
+#pragma unroll
+          for (int u = 0; u < 4; ++u) w[u] = s_dw[(t + u) * 16 + k];
+        };
+        read_dw(0, dw[0]);
         static_for<CH / 4>([&](auto G) {
           constexpr int t = decltype(G)::value * 4, i = decltype(G)::value & 1;
           if constexpr (t + 4 < CH) read_dw(t + 4, dw[i ^ 1]);
@@ -460,15 +511,13 @@ __global__ __launch_bounds__(64 * kPackedWaves, packed_states(N) <= 16 ? 4 : 2) 
             }
           });
         });
-        if constexpr (!AGG) {
-          float last = row_bcast<15>(Cv[0]) * h[0];
-#pragma unroll
-          for (int j = 1; j < NPL; ++j) last = fmaf(row_bcast<15>(Cv[j]), h[j], last);
-          yp[3] = last;
-          finish(CH - 4);
-        }
       }
       if constexpr (!AGG) {
+        float last = row_bcast<15>(Cv[0]) * h[0];
+#pragma unroll
+        for (int j = 1; j < NPL; ++j) last = fmaf(row_bcast<15>(Cv[j]), h[j], last);
+        yp[3] = last;
+        finish(CH - 4);
         wave_lds_fence();
         const float4 y4 = *reinterpret_cast<const float4*>(s_y + lrow * 16 + lcol);
         const float out[V] = {y4.x, y4.y, y4.z, y4.w};
