@@ -246,34 +246,43 @@ struct ScanPackedShape {
 };
 
 // Rows per piece (0: whole sequences), by a model of the two launches from what was measured on MI355X
-// (dstate 16, bf16; other dstates by the factor `scale`): a wave alone on its SIMD takes 84 ns a row
-// and waves that share one 65 ns each (full pass), 60 and 50 ns without read-outs; the second launch
-// and the pieces' set-up take 9 us; composing the states of 8 pieces takes 2 us.  Both sides,
-// whole | in pieces of the chosen length, in us: one sequence of 8192 x 1536: 678 | 96; of 512: 47 | 19;
-// 11 ragged ones of 11003 x 1536: 224 | 120; 16 of 512 x 1536: 74 | 77 (whole is chosen); 32 of 2048 x
-// 1536: 395 | 606 (whole).
+// (dstate 16, bf16; other dstates by the factors below): a wave alone on its SIMD takes 85 ns a row and
+// m waves that share one 54 + 24 / m ns each (full pass), 62 and 34 + 32 / m ns without read-outs, where a
+// sequence's last piece is left out; the second launch and the pieces' set-up take 8 us; composing the
+// states of 8 pieces takes 2 us.  Pieces are no longer than an eighth of the longest sequence, or 32 rows:
+// of fewer, ragged ones the model knows too little (24 of 30000 x 1536: 402 us with 1024 rows, 295 with
+// 384).  Both sides, whole | in pieces of the chosen length, in us: one sequence of 8192 x 1536: 661 | 92;
+// of 512: 45 | 19; 11 ragged ones of 11003 x 1536: 218 | 116; 8 of 2048 x 1536: 173 | 158; 16 of 512 x 1536:
+// 70 | 79 (whole is chosen); 32 of 2048 x 1536: 375 | 575 (whole).  Over 55 shapes the choice is 2.8% off
+// the best of these lengths on average, 14% at worst.
 int64_t scan_packed_piece(int64_t total, int64_t sequences, int64_t longest, int64_t waves, int64_t dstate) {
-  const double simds = 4.0 * device_cus();
-  const double scale = 0.45 + 0.55 * static_cast<double>(dstate) / 16.0;
-  const double rows = static_cast<double>(total) * static_cast<double>(waves) / simds;  // per SIMD
-  // time of a pass over pieces of `length` rows, `n` of them in all
-  auto pass = [&](double length, double n, double alone, double shared) {
-    const double per_simd = n * static_cast<double>(waves) / simds;
-    // pieces of about one length that all run at once take as long as the SIMD with the most of them
-    const bool even = n * length < 1.2 * static_cast<double>(total) && per_simd <= 4.0;
-    const double queue = even ? length * std::ceil(per_simd) : rows + 0.5 * length;
-    const double busy = per_simd <= 1.0 ? 0.0 : shared * queue;
-    return scale * (busy > alone * length ? busy : alone * length);
+  const double per_simd = static_cast<double>(waves) / (4.0 * device_cus());  // waves of a sequence's channels
+  const double states = static_cast<double>(dstate < 4 ? 4 : dstate);
+  const double scale = 0.45 + 0.55 * states / 16.0;                            // of a wave alone
+  const double work = dstate == 16 ? 1.0 : (139.0 + 20.0 * states) / 395.0;  // VALU instructions, where waves share
+  const double rows = static_cast<double>(total), n = static_cast<double>(sequences);
+  // a pass over `count` pieces of up to `length` rows, `sum` rows in all; the fullest SIMD has one of
+  // `length` rows and others of `mean` where all run at once
+  auto pass = [&](double length, double mean, double count, double sum, double alone, double shared, double rest) {
+    const double m = std::ceil(count * per_simd);
+    const double queue = m <= 4.0 ? length + (m - 1.0) * mean : sum * per_simd + 0.3 * length;
+    const double busy = m <= 1.0 ? 0.0 : work * (shared + rest / (m < 4.0 ? m : 4.0)) * queue;
+    const double one = scale * alone * length;
+    return busy > one ? busy : one;
   };
-  double best = pass(static_cast<double>(longest), static_cast<double>(sequences), 0.084, 0.065);
+  const double most = static_cast<double>(longest);
+  double best = pass(most, rows / n, n, rows, 0.085, 0.054, 0.024);
   int64_t piece = 0;
   for (int64_t p : {32, 48, 64, 96, 128, 160, 192, 256, 384, 512, 768, 1024}) {
-    if (p >= longest) break;
-    const double n = sequences == 1 ? static_cast<double>((total + p - 1) / p)
-                                    : static_cast<double>(total) / p + 0.5 * sequences;
+    if (p >= longest || (p > 32 && 8 * p > longest)) break;
     const double length = static_cast<double>(p);
-    const double t = pass(length, n, 0.084, 0.065) + pass(length, n, 0.060, 0.050) + 9.0 +
-                     2.0 * static_cast<double>(longest) / (8.0 * length);
+    // of sequences of about one length every piece but the last is full; of others the last is half
+    // full on average
+    const double count = rows >= 0.9 * n * most ? n * std::ceil(most / length) : rows / length + 0.5 * n;
+    const double first = count > n ? count - n : 0.0;
+    const double t = pass(length, length, count, rows, 0.085, 0.054, 0.024) +
+                     pass(length, length, first, first * length < rows ? first * length : rows, 0.062, 0.034, 0.032) +
+                     8.0 + 2.0 * most / (8.0 * length);
     if (t < best) {
       best = t;
       piece = p;

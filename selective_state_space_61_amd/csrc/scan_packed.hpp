@@ -22,10 +22,10 @@
 // balances better than workgroups that own a CU.  What bounds it is VALU issue: 395 VALU instructions
 // per chunk, of them 80 transcendental ones, keep a SIMD with three waves busy for 82% of its cycles, and
 // the matrix cores for 5%.  bf16, dstate 16: 32 prompts of 2048 x 1536 375 us (the dense scan's workgroups,
-// one per CU: 490), 11 ragged ones of 11003 x 1536 122 us (workgroups of scan_rows.hpp's kind, in pieces
+// one per CU: 490), 11 ragged ones of 11003 x 1536 117 us (workgroups of scan_rows.hpp's kind, in pieces
 // or not: 176), one of 8192 x 1536 92 us (123).  Eight equal prompts of 2048 x 1536 fill the SIMDs with
-// fewer than one wave each and take 172 us, where the dense scan's wave specialisation takes 122: equal
-// lengths are its case.
+// fewer than one wave each and take 172 us (in pieces 160), where the dense scan's wave specialisation
+// takes 122: equal lengths are its case.
 //
 // Pieces.  Few long prompts have too few waves, so sequences are cut into pieces of `piece` rows: a
 // first launch (AGG) runs every piece but a sequence's last one without read-outs and leaves its end
@@ -451,7 +451,7 @@ __global__ __launch_bounds__(64 * kPackedWaves, packed_states(N) <= 16 ? 4 : 2) 
         // It does not wait for the state, so the next four steps' goes out in the middle of these
         // four; the barrier keeps the compiler from moving it to where its result is used, at the
         // price of its whole latency.  bf16, us against the terms by DPP operands in every step: 32
-        // prompts of 2048 x 1536 374 | 392, 8 of 2048 172 | 178, one of 8192 92 | 96.  dstate 32 and 64
+        // prompts of 2048 x 1536 374 | 392, 8 of 2048 (whole) 172 | 178, one of 8192 92 | 96.  dstate 32 and 64
         // have no registers for the results of two groups (64: 536 | 480 us for 8 of 2048), and one
         // 4x4x1 instruction a step with exp(dt A) h as its addend is no faster than DPP (187 | 178).
         // The read-outs stay off the matrix cores: with them there too a full pass took 498 us for 397.
