@@ -139,22 +139,23 @@ __device__ __forceinline__ void step_state(float dt, float w, const float* a2, c
 }
 
 // What a step needs besides its input term: its decays e[j] = exp2(dt a2[j]) and, while h is still the
-// state before it, the read-out of the step before, sum_j C[j] h[j].  DPP operands and exponentials are at
-// least two instructions old where they are read or the block ends, as in step_readout.
+// state before it, the read-out of the step before, sum_j C[j] h[j].  The order obeys step_readout's rules
+// (ssm_device.hpp): each multiply-accumulate reads its accumulator three instructions after the last one,
+// with decays in between.
 template <int KC>
 __device__ __forceinline__ float decay_readout4(float dt, const float* a2, const float* c, const float* h, float (&e)[4]) {
   float yp;
   asm("v_mul_f32 %[e0], %[dt], %[a0]\n\t"
       "v_mul_f32 %[e1], %[dt], %[a1]\n\t"
-      "v_mul_f32 %[e2], %[dt], %[a2]\n\t"
-      "v_mul_f32 %[e3], %[dt], %[a3]\n\t"
+      "v_mul_f32_dpp %[yp], %[c0], %[h0] row_newbcast:%[kc] row_mask:0xf bank_mask:0xf\n\t"
       "v_exp_f32 %[e0], %[e0]\n\t"
       "v_exp_f32 %[e1], %[e1]\n\t"
+      "v_fmac_f32_dpp %[yp], %[c1], %[h1] row_newbcast:%[kc] row_mask:0xf bank_mask:0xf\n\t"
+      "v_mul_f32 %[e2], %[dt], %[a2]\n\t"
+      "v_mul_f32 %[e3], %[dt], %[a3]\n\t"
+      "v_fmac_f32_dpp %[yp], %[c2], %[h2] row_newbcast:%[kc] row_mask:0xf bank_mask:0xf\n\t"
       "v_exp_f32 %[e2], %[e2]\n\t"
       "v_exp_f32 %[e3], %[e3]\n\t"
-      "v_mul_f32_dpp %[yp], %[c0], %[h0] row_newbcast:%[kc] row_mask:0xf bank_mask:0xf\n\t"
-      "v_fmac_f32_dpp %[yp], %[c1], %[h1] row_newbcast:%[kc] row_mask:0xf bank_mask:0xf\n\t"
-      "v_fmac_f32_dpp %[yp], %[c2], %[h2] row_newbcast:%[kc] row_mask:0xf bank_mask:0xf\n\t"
       "v_fmac_f32_dpp %[yp], %[c3], %[h3] row_newbcast:%[kc] row_mask:0xf bank_mask:0xf"
       : [e0] "=&v"(e[0]), [e1] "=&v"(e[1]), [e2] "=&v"(e[2]), [e3] "=&v"(e[3]), [yp] "=&v"(yp)
       : [dt] "v"(dt), [a0] "v"(a2[0]), [a1] "v"(a2[1]), [a2] "v"(a2[2]), [a3] "v"(a2[3]), [c0] "v"(c[0]),
