@@ -155,15 +155,15 @@ __device__ __forceinline__ void bwd_step4(float dt, float dy0, const float* a2, 
       "v_exp_f32 %[n2], %[t2]\n\t"
       "v_exp_f32 %[n3], %[t3]\n\t"
       "v_mul_f32_dpp %[gb], %[b0], %[u0] " SSM_BWD_DPP_KB "\n\t"
-      "v_fmac_f32_dpp %[gb], %[b1], %[u1] " SSM_BWD_DPP_KB "\n\t"
-      "v_fmac_f32_dpp %[gb], %[b2], %[u2] " SSM_BWD_DPP_KB "\n\t"
-      "v_fmac_f32_dpp %[gb], %[b3], %[u3] " SSM_BWD_DPP_KB "\n\t"
       "v_mul_f32 %[t0], %[n0], %[h0]\n\t"
       "v_mul_f32 %[t1], %[n1], %[h1]\n\t"
+      "v_fmac_f32_dpp %[gb], %[b1], %[u1] " SSM_BWD_DPP_KB "\n\t"
       "v_mul_f32 %[t2], %[n2], %[h2]\n\t"
       "v_mul_f32 %[t3], %[n3], %[h3]\n\t"
+      "v_fmac_f32_dpp %[gb], %[b2], %[u2] " SSM_BWD_DPP_KB "\n\t"
       "v_mul_f32 %[t0], %[t0], %[u0]\n\t"
       "v_mul_f32 %[t1], %[t1], %[u1]\n\t"
+      "v_fmac_f32_dpp %[gb], %[b3], %[u3] " SSM_BWD_DPP_KB "\n\t"
       "v_mul_f32 %[t2], %[t2], %[u2]\n\t"
       "v_mul_f32 %[t3], %[t3], %[u3]\n\t"
       "v_mul_f32 %[pd], %[t0], %[r0]\n\t"
@@ -193,25 +193,26 @@ __device__ __forceinline__ void bwd_step4(float dt, float dy0, const float* a2, 
 #undef SSM_BWD_DPP_KC
 
 // sum_k p_k w_k over the 16 lanes k of a row, w_k taken from lane k of the lane's own row; two
-// fma chains of eight.  (The leading wait covers a VALU write of w just before: a DPP source.)
+// fma chains of eight.  (The leading wait covers a VALU write of w just before, a DPP source; the one behind
+// each pair keeps an accumulator's two writes three instructions apart, as step_readout's rules ask.)
 __device__ __forceinline__ float dot16_row_bcast(const float4* p, float w) {
   float s0, s1;
 #define SSM_BC(k) "row_newbcast:" #k " row_mask:0xf bank_mask:0xf"
   asm("s_nop 1\n\t"
       "v_mul_f32_dpp %[s0], %[w], %[p0] " SSM_BC(0) "\n\t"
-      "v_mul_f32_dpp %[s1], %[w], %[p8] " SSM_BC(8) "\n\t"
+      "v_mul_f32_dpp %[s1], %[w], %[p8] " SSM_BC(8) "\n\ts_nop 0\n\t"
       "v_fmac_f32_dpp %[s0], %[w], %[p1] " SSM_BC(1) "\n\t"
-      "v_fmac_f32_dpp %[s1], %[w], %[p9] " SSM_BC(9) "\n\t"
+      "v_fmac_f32_dpp %[s1], %[w], %[p9] " SSM_BC(9) "\n\ts_nop 0\n\t"
       "v_fmac_f32_dpp %[s0], %[w], %[p2] " SSM_BC(2) "\n\t"
-      "v_fmac_f32_dpp %[s1], %[w], %[p10] " SSM_BC(10) "\n\t"
+      "v_fmac_f32_dpp %[s1], %[w], %[p10] " SSM_BC(10) "\n\ts_nop 0\n\t"
       "v_fmac_f32_dpp %[s0], %[w], %[p3] " SSM_BC(3) "\n\t"
-      "v_fmac_f32_dpp %[s1], %[w], %[p11] " SSM_BC(11) "\n\t"
+      "v_fmac_f32_dpp %[s1], %[w], %[p11] " SSM_BC(11) "\n\ts_nop 0\n\t"
       "v_fmac_f32_dpp %[s0], %[w], %[p4] " SSM_BC(4) "\n\t"
-      "v_fmac_f32_dpp %[s1], %[w], %[p12] " SSM_BC(12) "\n\t"
+      "v_fmac_f32_dpp %[s1], %[w], %[p12] " SSM_BC(12) "\n\ts_nop 0\n\t"
       "v_fmac_f32_dpp %[s0], %[w], %[p5] " SSM_BC(5) "\n\t"
-      "v_fmac_f32_dpp %[s1], %[w], %[p13] " SSM_BC(13) "\n\t"
+      "v_fmac_f32_dpp %[s1], %[w], %[p13] " SSM_BC(13) "\n\ts_nop 0\n\t"
       "v_fmac_f32_dpp %[s0], %[w], %[p6] " SSM_BC(6) "\n\t"
-      "v_fmac_f32_dpp %[s1], %[w], %[p14] " SSM_BC(14) "\n\t"
+      "v_fmac_f32_dpp %[s1], %[w], %[p14] " SSM_BC(14) "\n\ts_nop 0\n\t"
       "v_fmac_f32_dpp %[s0], %[w], %[p7] " SSM_BC(7) "\n\t"
       "v_fmac_f32_dpp %[s1], %[w], %[p15] " SSM_BC(15)
       : [s0] "=&v"(s0), [s1] "=&v"(s1)

@@ -7,7 +7,7 @@ import re
 import pytest
 
 CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "selective_state_space_61_amd", "csrc")
-FILES = ["ssm_device.hpp", "scan_packed.hpp"]
+FILES = ["ssm_device.hpp", "scan_packed.hpp", "scan_bwd_rows.hpp"]
 STRING = re.compile(r'"((?:[^"\\]|\\.)*)"')
 
 
