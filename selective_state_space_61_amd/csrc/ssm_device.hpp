@@ -48,14 +48,17 @@ __device__ __forceinline__ void store_stream(float* p, float4 v) {
 
 // softplus(v) = log(1 + e^v).  Above 20 the correction log1p(e^-v) < 2.1e-9 is below the fp32
 // resolution of v and v is returned.  Otherwise u = e^v, w = fl(1 + u) and
-//   log1p(u) = log(w) + log(1 + e / w),  e = u - (w - 1)  (the exact rounding error of 1 + u;
-// w - 1 is exact),  and log(1 + e/w) is replaced by e: |e| <= 2^-24 w, so the dropped terms are
-// below 2^-24 * u * |e| + e^2, far under one ulp of the result.  For u < 2^-24, w = 1 and the
-// result is u exactly.  Small steps (delta ~ 1e-4) stay accurate to about an ulp.
+//   log1p(u) = log(w) + log(1 + e / w),  e = u - (w - 1)  (the rounding error of 1 + u).
+// For u < 1, w - 1 and e are exact, |e| <= 2^-24, and e stands for log(1 + e / w): what that drops is
+// below 2^-24 u + 2^-48, under 1.5 * 2^-24 of the result.  For u < 2^-24, w = 1 and the result is u
+// exactly: small steps (delta ~ 1e-4) stay accurate to about an ulp.  From u = 1 on the term itself is at
+// most 2^-24, under 1.5 * 2^-24 of the result, and e is not it: where 1 + u passes a power of two
+// e grows with u, and from 2^24 on w - 1 is rounded too (e = 1 or 2 there).  Clamping e to +-2^-24 changes
+// no value below and makes it harmless above.
 __device__ __forceinline__ float softplus_f32(float v) {
   const float u = hw_exp2(v * kLog2e);
   const float w = 1.0f + u;
-  const float e = u - (w - 1.0f);
+  const float e = __builtin_amdgcn_fmed3f(u - (w - 1.0f), -0x1p-24f, 0x1p-24f);
   const float r = fmaf(hw_log2(w), kLn2, e);
   return v > 20.0f ? v : r;
 }
