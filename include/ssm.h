@@ -602,7 +602,9 @@ SSM_API ssm_status_t ssm_causal_conv1d_packed_fwd(const ssm_packed_t *seqs, int6
  * Tensors need their element's alignment only.  Row strides (and dim) are below
  * 2^24 elements (else SSM_ERR_UNSUPPORTED).  dstate is 1, 2, 4, ..., 64.  The
  * number of pieces, and so the last bits of a result, depends on total,
- * sequences, max_seqlen and dim, never on what other sequences hold.  The
+ * sequences, max_seqlen and dim, never on what other sequences hold.  (A state
+ * that has become infinite stays infinite in pieces or not, unless the decay of
+ * one step rounds to zero: a step then makes it NaN, a whole piece keeps it.)  The
  * spans of y, the cache and the workspace must not overlap an input's or each
  * other's.  Values of one sequence, NaN and infinity included, never reach
  * another.

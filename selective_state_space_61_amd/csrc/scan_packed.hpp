@@ -286,7 +286,11 @@ __global__ __launch_bounds__(64 * kPackedWaves, packed_states(N) <= 16 ? 4 : 2) 
         for (int u = 0; u < kAhead; ++u) {
           if (i + u >= kth) break;
 #pragma unroll
-          for (int j = 0; j < NPL; ++j) h[j] = fmaf(hw_exp2(ds[u] * A2[j]), h[j], e[u][j]);
+          for (int j = 0; j < NPL; ++j) {
+            // a whole piece's decay is often 0 in fp32, which no step's is: an infinite state stays one
+            const float a = hw_exp2(ds[u] * A2[j]), next = fmaf(a, h[j], e[u][j]);
+            h[j] = a == 0.0f && fabsf(h[j]) == INFINITY ? h[j] + e[u][j] : next;
+          }
         }
       }
     }
