@@ -628,7 +628,8 @@ SSM_API ssm_status_t ssm_scan_packed_workspace(const ssm_packed_t *seqs, int64_t
  * cache: one token of `batch` sequences, entry i on slot cache_slots[i] (int32
  * on the device; NULL: slot i), which is read and updated in place.  An entry
  * with no slot is skipped: its row of y is left as it was.
- *   conv   cache (slots, dim, width-1) dtype (may be NULL when width == 1);
+ *   conv   cache (slots, dim, width-1) dtype (may be NULL when width == 1:
+ *          then every slot that is not negative is one);
  *          x, y (batch, dim), rows strided
  *   scan   cache (slots, dim, dstate) fp32 or bf16; x, delta, z, y (batch,
  *          dim), B, C (batch, dstate), rows strided

@@ -465,14 +465,17 @@ ssm_status_t ssm_causal_conv1d_update_cache(int64_t batch, int64_t dim, int64_t 
   if (!cache && width > 1) return fail(SSM_ERR_INVALID_ARG, "NULL cache");
   ssm::ConvStepArgs a{};
   Range rc{nullptr, 0};
-  if (width > 1) {
+  if (cache) {
     if (cache->dtype != dtype) return fail(SSM_ERR_INVALID_ARG, "the cache's dtype differs from x's");
     SSM_TRY(check_cache(cache, entry, &a.cache, &rc));
+  } else {
+    a.cache.slots = kMaxIndex + 1;  // any slot that is not negative
   }
+  if (width == 1) a.cache.stride = 0;  // no windows: only which slots there are counts
   ssm_row_strides_t rs = strides_or_zero(strides);
   Rows t[] = {{x, dim, &rs.x, "x", 0}, {y, dim, &rs.y, "y", 0}};
   SSM_TRY(check_rows(t, 2, batch, es));
-  if (batch == 0 || dim == 0 || (width > 1 && cache->slots == 0)) return SSM_OK;
+  if (batch == 0 || dim == 0 || (cache && cache->slots == 0)) return SSM_OK;
   if (!x || !weight || !y) return fail(SSM_ERR_INVALID_ARG, "NULL required pointer (x, weight and y)");
   if (!aligned(weight, 4) || !aligned(bias, 4) || !aligned(cache_slots, 4))
     return fail(SSM_ERR_MISALIGNED, "weight, bias or cache_slots is not 4-byte aligned");

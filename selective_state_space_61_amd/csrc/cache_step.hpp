@@ -157,9 +157,9 @@ __global__ __launch_bounds__(kStepThreads) void conv1d_update_cache_kernel(const
     Run<BF16, E> win[R];
 #pragma unroll
     for (int i = 0; i < R; ++i) {
-      // without windows (K 1) there is no slot to look up: only padding is skipped
+      // (without windows, K 1, a slot only says whether the entry is padding)
       b[i] = b0 + i < p.batch ? b0 + i : b0;
-      at[i] = b0 + i >= p.batch ? -1 : W > 0 ? cache_offset(p.cache, p.slots, b0 + i) : (p.slots && p.slots[b0 + i] < 0 ? -1 : 0);
+      at[i] = b0 + i < p.batch ? cache_offset(p.cache, p.slots, b0 + i) : -1;
     }
 #pragma unroll
     for (int i = 0; i < R; ++i) {

@@ -1,10 +1,10 @@
 """The serving operators at the launch shapes that large batches take, against the same plain 64-bit forms
-and bounds as test_serving_gpu.py: prompts cut into pieces."""
+and bounds as test_serving_gpu.py: prompts cut into pieces, steps whose threads take four entries."""
 import pytest
 import torch
 
 import serving_ref as R
-from test_serving_gpu import Maker, cu_of, scan_inputs, scan_ref
+from test_serving_gpu import DT, SENTINEL, Maker, cu_of, i32, scan_inputs, scan_ref
 
 pytestmark = pytest.mark.gpu
 
@@ -47,3 +47,22 @@ def test_scan_packed_infinite_state_stays(ssm, n, hint):
     others = [c for c in range(dim) if not 3 <= c < 21]
     R.check(y[:, others], ref[:, others], err[:, others], torch.float32, "the other channels")
     R.check(pool[0, others], h[others], eh[others], torch.float32, "their states")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("cached", [True, False])
+@pytest.mark.parametrize("batch,dim", [(5, 70), (250, 5120)])
+def test_conv_step_of_width_one_skips_padding(ssm, batch, dim, cached, dtype):
+    """Without windows too an entry without a slot keeps its row of y; without a cache every slot that is not
+    negative counts."""
+    m, dt, nslots = Maker(dim), DT[dtype], batch + 1
+    x, w, b = m.normal((batch, dim), dt), m.normal((dim, 1)), m.normal((dim,))
+    slots = list(range(batch))
+    slots[1], slots[2], slots[batch - 1] = -1, nslots, 2_000_000_000
+    pool = torch.empty(nslots, dim, 0, dtype=dt, device="cuda") if cached else None
+    y = torch.full((batch, dim), SENTINEL, dtype=dt, device="cuda")
+    ssm.ssm_causal_conv1d_update_cache(pool, i32(slots), x, w, b, y=y)
+    ref, err = R.conv_rows(R.f64(x), R.f64(w), R.f64(b), True)
+    live = [i for i, s in enumerate(slots) if 0 <= s and (s < nslots or not cached)]
+    R.check(y[live], ref[live], err[live], dt, f"{len(live)} entries")
+    assert (y[[i for i in range(batch) if i not in live]] == SENTINEL).all()
