@@ -152,7 +152,7 @@ def ssm_causal_conv1d_packed_fwd(x: torch.Tensor, weight: torch.Tensor, cu_seqle
     x, y: (total, dim); weight: (dim, width) fp32; bias: (dim,) fp32; cache: (slots, dim, width - 1) in
     x's dtype or None.  Returns y; rows of no sequence are left as they were (as allocated)."""
     lib = load_library()
-    if x.dim() != 2 or weight.dim() != 2:
+    if x is None or weight is None or x.dim() != 2 or weight.dim() != 2:
         raise ValueError("x must be (total, dim) and weight (dim, width)")
     total, dim = x.shape
     width = weight.shape[1]
@@ -197,7 +197,7 @@ def ssm_scan_packed_fwd(x: torch.Tensor, delta: torch.Tensor, A: torch.Tensor, B
     launch shape.  workspace: a uint8 tensor of ssm_scan_packed_workspace bytes, allocated here when None.
     Returns y; rows of no sequence are left as they were (as allocated)."""
     lib = load_library()
-    if x.dim() != 2 or A.dim() != 2:
+    if x is None or A is None or x.dim() != 2 or A.dim() != 2:
         raise ValueError("x must be (total, dim) and A (dim, dstate)")
     total, dim = x.shape
     dstate = A.shape[1]
@@ -237,7 +237,7 @@ def ssm_causal_conv1d_update_cache(cache: Optional[torch.Tensor], cache_slots: O
     """One token of the convolution on a cache (include/ssm.h: ssm_causal_conv1d_update_cache).  cache:
     (slots, dim, width - 1) in x's dtype, updated in place; x, y: (batch, dim).  Returns y."""
     lib = load_library()
-    if x.dim() != 2 or weight.dim() != 2:
+    if x is None or weight is None or x.dim() != 2 or weight.dim() != 2:
         raise ValueError("x must be (batch, dim) and weight (dim, width)")
     batch, dim = x.shape
     width = weight.shape[1]
@@ -270,7 +270,7 @@ def ssm_state_update_cache(cache: torch.Tensor, cache_slots: Optional[torch.Tens
     dim, dstate) fp32 or bf16, updated in place; x, delta, z, y: (batch, dim); B, C: (batch, dstate).
     Returns y."""
     lib = load_library()
-    if x.dim() != 2 or A.dim() != 2:
+    if x is None or A is None or x.dim() != 2 or A.dim() != 2:
         raise ValueError("x must be (batch, dim) and A (dim, dstate)")
     batch, dim = x.shape
     dstate = A.shape[1]
@@ -305,7 +305,7 @@ def ssm_ssd_state_update_cache(cache: torch.Tensor, cache_slots: Optional[torch.
     (slots, nheads, headdim, dstate) fp32 or bf16, updated in place; x, z, y: (batch, nheads, headdim);
     dt: (batch, nheads); B, C: (batch, ngroups, dstate); A, D, dt_bias: (nheads,) fp32.  Returns y."""
     lib = load_library()
-    if x.dim() != 3 or B.dim() != 3:
+    if x is None or B is None or x.dim() != 3 or B.dim() != 3:
         raise ValueError("x must be (batch, nheads, headdim) and B (batch, ngroups, dstate)")
     batch, nheads, headdim = x.shape
     ngroups, dstate = B.shape[1], B.shape[2]
@@ -336,8 +336,10 @@ def ssm_ssd_state_update_cache(cache: torch.Tensor, cache_slots: Optional[torch.
 def _q8(cache, cache_slots, codes, scales, store_slots):
     """What a store or load needs, checked.  The cache's entries are (rows, dstate) or (nheads, headdim,
     dstate)."""
-    if cache.dim() not in (3, 4):
+    if cache is None or cache.dim() not in (3, 4):
         raise ValueError("cache must be (slots, dim, dstate) or (slots, nheads, headdim, dstate)")
+    if codes is None or codes.dim() != cache.dim():
+        raise ValueError("codes must be (stored,) + a slot's shape")
     dev = cache.get_device()
     entry = tuple(cache.shape[1:])
     ref = _cache(cache, "cache", entry, dev)
