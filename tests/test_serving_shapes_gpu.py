@@ -1,10 +1,12 @@
 """The serving operators at the launch shapes that large batches take, against the same plain 64-bit forms
-and bounds as test_serving_gpu.py: prompts cut into pieces, steps whose threads take four entries."""
+and bounds as test_serving_gpu.py: the convolution's tiles of 32 rows, steps whose threads take four entries,
+prompts cut into pieces at every dstate."""
+import numpy as np
 import pytest
 import torch
 
 import serving_ref as R
-from test_serving_gpu import DT, SENTINEL, Maker, cu_of, i32, scan_inputs, scan_ref
+from test_serving_gpu import DT, SENTINEL, Maker, conv_case, cu_of, i32, scan_case, scan_inputs, scan_ref
 
 pytestmark = pytest.mark.gpu
 
@@ -21,6 +23,141 @@ def gpu():
 def ssm():
     import selective_state_space_61_amd as m
     return m
+
+
+def cus():
+    return torch.cuda.get_device_properties(0).multi_processor_count
+
+
+# ---- the convolution's tiles of 32 rows ---------------------------------------------------------------
+
+# starts one to three rows before a tile's end (31, 62, 93), sequences shorter than the window before and at a
+# border, none, one of many tiles, a ragged last tile
+TILES = [31, 31, 31, 1, 1, 1, 2, 30, 0, 29, 3, 200, 1100, 0, 227]
+
+
+@pytest.mark.parametrize("width", [1, 2, 3, 4])
+@pytest.mark.parametrize("dtype,dim,gap", [("bf16", 5113, 0), ("bf16", 5120, 16), ("f32", 2570, 0)])
+def test_conv_packed_large_tiles(ssm, dtype, dim, gap, width):
+    total = sum(TILES)
+    tiles = -(-total // 32)
+    blocks = -(-(-(-dim // (2 if dtype == "bf16" else 1))) // 256)
+    assert tiles * blocks >= 2 * cus() and len(TILES) <= tiles and total % 32  # what makes the tiles large
+    conv_case(ssm, TILES, dim, width, dtype, gap=gap)
+
+
+def test_conv_packed_large_tiles_behind_rows_of_no_sequence(ssm):
+    conv_case(ssm, TILES, 5120, 4, "bf16", first=33, tail=70, slots=[-1, 3, 16, 0, 2_000_000_000] + list(range(4, 14)))
+
+
+# ---- steps whose threads take four entries --------------------------------------------------------------
+
+
+def padded_slots(batch, nslots):
+    """Each entry its own slot, entries without one inside, at the start and at the end of groups of four."""
+    s = [int(v) for v in np.random.default_rng(batch).permutation(nslots)[:batch]]
+    for i, bad in zip((0, 5, 6, 11, batch - 1), (-1, nslots, -7, 2_000_000_000, -1)):
+        s[i] = bad
+    return s
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("width", [2, 3, 4])
+@pytest.mark.parametrize("batch,dim,gap", [(250, 5120, 8), (251, 5113, 0)])
+def test_conv_step_four_entries_a_thread(ssm, batch, dim, gap, width, dtype):
+    assert -(-dim // 1024) * -(-batch // 4) >= cus()
+    m, dt, nslots = Maker(dim + width), DT[dtype], batch + 9
+    slots = padded_slots(batch, nslots)
+    x, w, b = m.rows(batch, dim, dt, gap), m.normal((dim, width)), m.normal((dim,))
+    pool = m.normal((nslots, dim, width - 1), dt)
+    before = pool.cpu().clone()
+    y = torch.full((batch, dim + gap), SENTINEL, dtype=dt, device="cuda")[:, gap // 2:gap // 2 + dim]
+    ssm.ssm_causal_conv1d_update_cache(pool, i32(slots), x, w, b, y=y)
+    torch.cuda.synchronize()
+    live = [i for i, s in enumerate(slots) if 0 <= s < nslots]
+    at = [slots[i] for i in live]
+    line = torch.cat([before[at].double().transpose(1, 2), R.f64(x)[live][:, None]], 1)  # (entries, width, dim)
+    ref, err = R.conv_rows(line.transpose(0, 1).reshape(width, -1), R.f64(w).repeat(len(live), 1),
+                           R.f64(b).repeat(len(live)), True)
+    R.check(y[live].reshape(1, -1), ref, err, dt, f"{len(live)} entries")
+    assert (y[[i for i in range(batch) if i not in live]] == SENTINEL).all()
+    before[at] = line[:, 1:].transpose(1, 2).to(dt)
+    assert torch.equal(pool.cpu(), before)
+
+
+@pytest.mark.parametrize("n,dtype,cdtype", [(n, *t) for n in (1, 2, 4, 8, 16, 32, 64) for t in (("bf16", "f32"), ("f32", "bf16"))]
+                         + [(16, "f32", "f32"), (16, "bf16", "bf16")])
+@pytest.mark.parametrize("dim,gap", [(5120, 16), (5113, 0)])
+def test_scan_step_four_entries_a_thread(ssm, dim, gap, n, dtype, cdtype):
+    dt, cdt = DT[dtype], DT[cdtype]
+    lanes = n // (min(n, 8) if cdtype == "bf16" else min(n, 4))
+    blocks = -(-dim * lanes // 256)
+    batch = max(4 * -(-cus() // blocks), 12) + 2
+    assert blocks * -(-batch // 4) >= cus() and batch % 4
+    m, nslots = Maker(dim + n), batch + 5
+    slots = padded_slots(batch, nslots)
+    d = scan_inputs(m, batch, dim, n, dt, gap, True, True, True)
+    pool = m.normal((nslots, dim, n), cdt)
+    before = pool.clone()
+    y = torch.full((batch, dim + gap), SENTINEL, dtype=dt, device="cuda")[:, gap // 2:gap // 2 + dim]
+    ssm.ssm_state_update_cache(pool, i32(slots), d["x"], d["delta"], d["A"], d["B"], d["C"], D=d["D"], z=d["z"],
+                               delta_bias=d["delta_bias"], delta_softplus=True, y=y)
+    torch.cuda.synchronize()
+    kept = torch.ones(nslots, dtype=torch.bool)
+    for i, s in enumerate(slots):
+        if not 0 <= s < nslots:
+            assert (y[i] == SENTINEL).all()
+            continue
+        ref, err, h, eh = scan_ref(d, i, i + 1, True, R.f64(before[s]))
+        R.check(y[i:i + 1], ref, err, dt, f"entry {i}")
+        R.check(pool[s], h, eh, cdt, f"state {i}")
+        kept[s] = False
+    assert torch.equal(pool[kept.cuda()], before[kept.cuda()])
+
+
+# ---- prompts cut into pieces ------------------------------------------------------------------------------
+
+
+def assert_cut(ssm, lens, extra, hint, dim, n, dtype):
+    """The launch has pieces: they are what the workspace is for."""
+    assert ssm.ssm_scan_packed_workspace(sum(lens) + extra, len(lens), hint, dim, n, DT[dtype]) > 0
+
+
+@pytest.mark.parametrize("n", [1, 2, 4, 8, 16, 32, 64])
+@pytest.mark.parametrize("lens,hint", [([1500], 0), ([700, 3, 801], 801), ([300, 0, 17, 400], 400)], ids=str)
+@pytest.mark.parametrize("dtype,cdtype", [("f32", "bf16"), ("bf16", "f32")])
+def test_scan_packed_pieces(ssm, lens, hint, n, dtype, cdtype):
+    # the first sequence, and every third after it, goes on from its slot
+    for dim, gap, first, tail in ((72, 0, 2, 3), (33, 5, 0, 0), (3, 0, 1, 0)):
+        assert_cut(ssm, lens, first + tail, hint, dim, n, dtype)
+        scan_case(ssm, lens, dim, n, dtype, cdtype, max_seqlen=hint, gap=gap, first=first, tail=tail)
+
+
+@pytest.mark.parametrize("n", [1, 16, 64])
+def test_scan_packed_pieces_variants(ssm, n):
+    lens = [700, 3, 801]
+    for kw in (dict(cache=False), dict(initial=False), dict(z=False, D=False), dict(slots=[1, -1, 2_000_000_000])):
+        assert_cut(ssm, lens, 0, 0, 40, n, "bf16")
+        scan_case(ssm, lens, 40, n, "bf16", **kw)
+
+
+@pytest.mark.parametrize("n", [2, 16, 32])
+def test_scan_packed_pieces_whatever_the_workspace_holds(ssm, n):
+    m, lens, dim = Maker(n), [500, 1, 620], 40
+    d = scan_inputs(m, sum(lens), dim, n, torch.bfloat16, 0, True, True, True)
+    size = ssm.ssm_scan_packed_workspace(sum(lens), len(lens), 620, dim, n, torch.bfloat16)
+    assert size > 0
+    pool = m.normal((3, dim, n))
+    got = []
+    for fill in (0, 255):  # 255: every float a NaN
+        cache = pool.clone()
+        y = ssm.ssm_scan_packed_fwd(d["x"], d["delta"], d["A"], d["B"], d["C"], cu_of(lens), D=d["D"], z=d["z"],
+                                    delta_bias=d["delta_bias"], delta_softplus=True, cache=cache, max_seqlen=620,
+                                    has_initial=torch.ones(3, dtype=torch.bool, device="cuda"),
+                                    workspace=torch.full((size,), fill, dtype=torch.uint8, device="cuda"))
+        got.append((y, cache))
+    assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+    assert torch.isfinite(got[0][0]).all() and torch.isfinite(got[0][1]).all()
 
 
 @pytest.mark.parametrize("n", [1, 8, 16, 64])
