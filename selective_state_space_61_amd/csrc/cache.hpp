@@ -96,12 +96,6 @@ struct Run {
     else return __builtin_bit_cast(float, w[v]);
   }
 
-  // an (empty) use of the words: the compiler waits for their load here, on every path through it
-  __device__ __forceinline__ void consume() const {
-#pragma unroll
-    for (int i = 0; i < kWords; ++i) asm volatile("" ::"v"(w[i]));
-  }
-
   __device__ __forceinline__ void set(const float (&val)[NV]) {
     if constexpr (BF16) {
 #pragma unroll

@@ -291,8 +291,7 @@ int64_t scan_packed_piece(int64_t total, int64_t sequences, int64_t longest, int
   return piece;
 }
 
-ssm_status_t scan_packed_shape(const ssm_packed_t* seqs, int64_t dim, int64_t dstate, ssm_dtype_t dtype,
-                               ScanPackedShape* out) {
+ssm_status_t scan_packed_shape(const ssm_packed_t* seqs, int64_t dim, int64_t dstate, ScanPackedShape* out) {
   const int64_t ncb = (dim + 16 * ssm::kPackedWaves - 1) / (16 * ssm::kPackedWaves);
   const int64_t longest =
       seqs->max_seqlen > 0 && seqs->max_seqlen < seqs->total ? seqs->max_seqlen : seqs->total;
@@ -374,7 +373,7 @@ ssm_status_t ssm_scan_packed_workspace(const ssm_packed_t* seqs, int64_t dim, in
   *bytes = 0;
   if (seqs->total == 0 || seqs->sequences == 0 || dim == 0) return SSM_OK;
   ScanPackedShape shape;
-  SSM_TRY(scan_packed_shape(seqs, dim, dstate, dtype, &shape));
+  SSM_TRY(scan_packed_shape(seqs, dim, dstate, &shape));
   *bytes = shape.floats * 4;
   return SSM_OK;
 }
@@ -409,7 +408,7 @@ ssm_status_t ssm_scan_packed_fwd(const ssm_packed_t* seqs, int64_t dim, int64_t 
     if (*r.stride >= ssm::kScanPackedMaxStride)
       return fail(SSM_ERR_UNSUPPORTED, "row stride %lld of %s is not below 2^24", (long long)*r.stride, r.name);
   ScanPackedShape shape;
-  SSM_TRY(scan_packed_shape(seqs, dim, dstate, dtype, &shape));
+  SSM_TRY(scan_packed_shape(seqs, dim, dstate, &shape));
   if (shape.floats > 0) {
     if (!workspace || workspace_bytes < shape.floats * 4)
       return fail(SSM_ERR_INVALID_ARG, "workspace of %lld bytes, %lld are needed",
