@@ -541,7 +541,7 @@ typedef struct {
 
 /* Packed sequences.  Sequence s is the rows cu_seqlens[s] .. cu_seqlens[s+1]-1
  * of every packed tensor (of `total` rows); rows of no sequence (before the
- * first, behind the last) are neither read nor written.
+ * first, behind the last) have no effect and are not written.
  *   cu_seqlens   (sequences + 1) int32 on the device, not falling
  *   cache_slots  (sequences) int32 on the device: each sequence's slot, or
  *                NULL: sequence s has slot s
@@ -666,7 +666,9 @@ SSM_API ssm_status_t ssm_ssd_state_update_cache(int64_t batch, int64_t nheads, i
  *   read back: code[n] * scale, rounded to fp32 (and to bf16 for such a cache)
  *
  * so a value is off by at most scale / 2 (and that rounding).  A row that
- * holds a NaN or an infinity gets the scale NaN and reads back as NaN.  It is
+ * holds a NaN or an infinity gets the scale NaN and reads back as NaN; one
+ * whose largest value is within 2^-24 of fp32's largest may read back as
+ * infinite (127 times a scale that was rounded up).  It is
  * a form to keep states in, not to step them in: rounding every step to 8
  * bits would stop slow decays.
  *

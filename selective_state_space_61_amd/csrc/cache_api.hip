@@ -249,12 +249,14 @@ struct ScanPackedShape {
 // (dstate 16, bf16; other dstates by the factors below): a wave alone on its SIMD takes 85 ns a row and
 // m waves that share one 54 + 24 / m ns each (full pass), 62 and 34 + 32 / m ns without read-outs, where a
 // sequence's last piece is left out; the second launch and the pieces' set-up take 8 us; composing the
-// states of 8 pieces takes 2 us.  Pieces are no longer than an eighth of the longest sequence, or 32 rows:
-// of fewer, ragged ones the model knows too little (24 of 30000 x 1536: 402 us with 1024 rows, 295 with
-// 384).  Both sides, whole | in pieces of the chosen length, in us: one sequence of 8192 x 1536: 661 | 92;
-// of 512: 45 | 19; 11 ragged ones of 11003 x 1536: 218 | 116; 8 of 2048 x 1536: 173 | 158; 16 of 512 x 1536:
-// 70 | 79 (whole is chosen); 32 of 2048 x 1536: 375 | 575 (whole).  Over 55 shapes the choice is 2.8% off
-// the best of these lengths on average, 14% at worst.
+// states of 8 pieces takes 2 us (linear in the pieces, where the reads of their states are not: too little
+// past some 100000 rows).  Pieces are no longer than an eighth of the longest sequence, or 32 rows: of
+// fewer, ragged ones the model knows too little (24 of 30000 x 1536: 402 us with 1024 rows, 300 with 384).
+// Both sides, whole | in pieces of the chosen length, in us: one sequence of 8192 x 1536: 661 | 93; of 512:
+// 45 | 19; 11 ragged ones of 11003 x 1536: 218 | 117; 8 of 2048 x 1536: 173 | 159; 16 of 512 x 1536: 71 | 79
+// (whole is chosen); 32 of 2048 x 1536: 377 | 575 (whole).  Over 55 bf16 shapes (35 of dstate 16, the others
+// of 1, 2, 4, 8, 32 and 64) the choice is 2.8% off the best of these lengths on average, 14% at worst; there
+// is no term for fp32 rows.
 int64_t scan_packed_piece(int64_t total, int64_t sequences, int64_t longest, int64_t waves, int64_t dstate) {
   const double per_simd = static_cast<double>(waves) / (4.0 * device_cus());  // waves of a sequence's channels
   const double states = static_cast<double>(dstate < 4 ? 4 : dstate);

@@ -19,11 +19,11 @@
 //     group.  Rows of y go out as the rows of x came in.
 // There are no barriers.  A sequence's channels are many small independent waves, several per
 // SIMD, which cover each other's latencies and fill whatever CUs are free: with ragged prompts that
-// balances better than workgroups that own a CU.  What bounds it is VALU issue: 395 VALU instructions
+// balances better than workgroups that own a CU.  What bounds it is VALU issue: 399 VALU instructions
 // per chunk, of them 80 transcendental ones, keep a SIMD with three waves busy for 82% of its cycles, and
-// the matrix cores for 5%.  bf16, dstate 16: 32 prompts of 2048 x 1536 375 us (the dense scan's workgroups,
-// one per CU: 490), 11 ragged ones of 11003 x 1536 117 us (workgroups of scan_rows.hpp's kind, in pieces
-// or not: 176), one of 8192 x 1536 92 us (123).  Eight equal prompts of 2048 x 1536 fill the SIMDs with
+// the matrix cores for 5%.  bf16, dstate 16: 32 prompts of 2048 x 1536 377 us (the dense scan's workgroups,
+// one per CU: 490), 11 ragged ones of 11003 x 1536 117 us launched back to back, 119 to 126 from Python
+// (workgroups of scan_rows.hpp's kind, in pieces or not: 176), one of 8192 x 1536 93 us (123).  Eight equal prompts of 2048 x 1536 fill the SIMDs with
 // fewer than one wave each and take 172 us (in pieces 160), where the dense scan's wave specialisation
 // takes 122: equal lengths are its case.
 //
