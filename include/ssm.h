@@ -687,6 +687,103 @@ SSM_API ssm_status_t ssm_cache_load_q8(int64_t count, int64_t rows, int64_t dsta
                                        const int8_t *codes, const float *scales, const int32_t *store_slots,
                                        const ssm_cache_t *cache, const int32_t *cache_slots, void *stream);
 
+/*
+ * ---- Gated recurrence ----------------------------------------------------
+ *
+ * A linear recurrence of one state per channel, whose decay and input are
+ * gated by projections of the input ("mamba->jamba" sec. 2.3: the scan of a
+ * linear recurrence by the associative operator; here without B, C and the
+ * state dimension).  Per channel d and step t:
+ *
+ *   r = sigmoid(a_gate + a_bias),  i = sigmoid(x_gate + x_bias)
+ *   l = -a_scale softplus(a_param) r,  a = exp(l)
+ *   h_t = a h_{t-1} + sqrt(1 - a^2) (i x_t)
+ *   y_t = h_t silu(z_t)                             (h_t if z is NULL)
+ *
+ *   x, a_gate, x_gate, z, y   rows of dim elements, dtype
+ *   a_param, a_bias, x_bias   (dim) fp32; the biases may be NULL (zeros)
+ *   a_scale                   finite, at least 0
+ *
+ * All arithmetic is fp32 (1 - a^2 without the cancellation of a difference),
+ * states are fp32 unless a cache is bf16.  The calls allocate nothing, keep
+ * nothing between calls, enqueue kernels only and may be captured into a HIP
+ * graph.  At most 2^31 - 1 rows (batch * seqlen, total or batch).
+ *
+ * The rows are cut into tiles that run in parallel and hand each other their
+ * states through the caller's workspace; the results do not depend on timing.
+ * workspace: at least ssm_gated_scan_workspace bytes, 16-byte aligned, the
+ * caller's until the call's work is done (each call that may run at the same
+ * time needs its own); may be NULL where that is 0.
+ */
+SSM_API ssm_status_t ssm_gated_scan_workspace(int64_t rows, int64_t dim, ssm_dtype_t dtype, int backward,
+                                              int64_t *bytes);
+
+/*
+ * Forward over a batch.
+ *   x, a_gate, x_gate, z, y      (batch, seqlen, dim) dtype
+ *   initial_state                (batch, dim) fp32, or NULL: zeros
+ *   last_state                   (batch, dim) fp32, or NULL: not written.  With
+ *                                seqlen 0 it is the initial state
+ *   checkpoints                  (batch * seqlen / 64, dim) fp32 (rounded down)
+ *                                for the backward, or NULL: the state after
+ *                                every 64th row of the batch's rows
+ * Outputs must not overlap inputs or each other.
+ */
+SSM_API ssm_status_t ssm_gated_scan_fwd(int64_t batch, int64_t seqlen, int64_t dim, ssm_dtype_t dtype, const void *x,
+                                        const void *a_gate, const void *x_gate, const float *a_param,
+                                        const float *a_bias, const float *x_bias, const void *z, float a_scale,
+                                        const float *initial_state, void *y, float *last_state, float *checkpoints,
+                                        void *workspace, int64_t workspace_bytes, void *stream);
+
+/*
+ * Gradients of sum(dy y) + sum(dlast_state last_state), from the forward's
+ * inputs and its checkpoints (NULL where the batch has at most 64 rows).
+ *   dy, dx, da_gate, dx_gate, dz  (batch, seqlen, dim) dtype; dz is needed with
+ *                                 z and not written without
+ *   dlast_state                   (batch, dim) fp32, or NULL: zeros
+ *   da_param, da_bias, dx_bias    (dim) fp32, summed over all rows in an order
+ *                                 that the sizes alone decide; the last two may
+ *                                 be NULL
+ *   dinitial_state                (batch, dim) fp32, or NULL: not written
+ * Where a step's decay is 1 (an a_gate of -inf), the gradients through its input
+ * weight are their limit 0.  a_gate and a_param get no gradient from the
+ * derivative of sqrt there, which has none.
+ */
+SSM_API ssm_status_t ssm_gated_scan_bwd(int64_t batch, int64_t seqlen, int64_t dim, ssm_dtype_t dtype, const void *x,
+                                        const void *a_gate, const void *x_gate, const float *a_param,
+                                        const float *a_bias, const float *x_bias, const void *z, float a_scale,
+                                        const float *initial_state, const float *checkpoints, const void *dy,
+                                        const float *dlast_state, void *dx, void *da_gate, void *dx_gate,
+                                        float *da_param, float *da_bias, float *dx_bias, void *dz,
+                                        float *dinitial_state, void *workspace, int64_t workspace_bytes, void *stream);
+
+/* Elements between the rows of each tensor, 0 for contiguous rows, as in
+ * ssm_row_strides_t. */
+typedef struct {
+  int64_t x, a_gate, x_gate, z, y;
+} ssm_gated_strides_t;
+
+/*
+ * Forward over packed prompts (see "Serving": sequences, slots, statuses).
+ *   x, a_gate, x_gate, z, y  (total, dim) dtype, rows strided
+ *   cache                    (slots, dim) fp32 or bf16, or NULL: every sequence
+ *                            starts from zeros and no state is stored
+ * max_seqlen is not used.  Values of one sequence, NaN and infinity included,
+ * never reach another.
+ */
+SSM_API ssm_status_t ssm_gated_scan_packed_fwd(const ssm_packed_t *seqs, int64_t dim, ssm_dtype_t dtype, const void *x,
+                                               const void *a_gate, const void *x_gate, const float *a_param,
+                                               const float *a_bias, const float *x_bias, const void *z, float a_scale,
+                                               void *y, const ssm_cache_t *cache, const ssm_gated_strides_t *strides,
+                                               void *workspace, int64_t workspace_bytes, void *stream);
+
+/* One token of `batch` sequences on a cache (slots, dim), as the steps above. */
+SSM_API ssm_status_t ssm_gated_update_cache(int64_t batch, int64_t dim, ssm_dtype_t dtype, const ssm_cache_t *cache,
+                                            const int32_t *cache_slots, const void *x, const void *a_gate,
+                                            const void *x_gate, const float *a_param, const float *a_bias,
+                                            const float *x_bias, const void *z, float a_scale, void *y,
+                                            const ssm_gated_strides_t *strides, void *stream);
+
 /* Static string naming a status code ("SSM_OK", ...); never NULL. */
 SSM_API const char *ssm_status_string(ssm_status_t status);
 

@@ -15,7 +15,7 @@ D, delta_bias (dim,) fp32; y like x; last_state / state (batch, dim, dstate) fp3
 z and y share one dtype: torch.float32 or torch.bfloat16.
 
 For serving (packed prompts, single tokens on a cache of slots, states set aside in 8 bits) see
-``serving.py``, whose functions this module exports too.
+``serving.py``, for the gated recurrence ``gated.py``; this module exports their functions too.
 """
 from __future__ import annotations
 
@@ -37,7 +37,9 @@ EXPORTED = ("ssm_scan_fwd", "ssm_scan_fwd_ex", "ssm_scan_fwd_noalloc", "ssm_scan
             "ssm_causal_conv1d_update", "ssm_ssd_fwd", "ssm_ssd_state_update", "ssm_status_string", "ssm_last_error", "ssm_abi_version",
             "ssm_causal_conv1d_packed_fwd", "ssm_scan_packed_fwd", "ssm_scan_packed_workspace",
             "ssm_causal_conv1d_update_cache", "ssm_state_update_cache", "ssm_ssd_state_update_cache",
-            "ssm_cache_store_q8", "ssm_cache_load_q8")
+            "ssm_cache_store_q8", "ssm_cache_load_q8",
+            "ssm_gated_scan_workspace", "ssm_gated_scan_fwd", "ssm_gated_scan_bwd", "ssm_gated_scan_packed_fwd",
+            "ssm_gated_update_cache")
 
 
 class SsmError(RuntimeError):
@@ -77,6 +79,10 @@ class Packed(ctypes.Structure):
 
 class RowStrides(ctypes.Structure):
     _fields_ = [(k, ctypes.c_int64) for k in ("x", "delta", "B", "C", "z", "y")]
+
+
+class GatedStrides(ctypes.Structure):
+    _fields_ = [(k, ctypes.c_int64) for k in ("x", "a_gate", "x_gate", "z", "y")]
 
 
 SSM_BBAR_DELTA_B, SSM_BBAR_ZOH = 0, 1
@@ -138,7 +144,13 @@ def load_library(path: str = LIBRARY) -> ctypes.CDLL:
                                                i32, vp, strides, vp]
     lib.ssm_cache_store_q8.argtypes = [i64, i64, i64, cache, vp, i64, vp, vp, vp, vp]
     lib.ssm_cache_load_q8.argtypes = [i64, i64, i64, i64, vp, vp, vp, cache, vp, vp]
-    for name in EXPORTED[-8:]:
+    gstrides, f32 = ctypes.POINTER(GatedStrides), ctypes.c_float
+    lib.ssm_gated_scan_workspace.argtypes = [i64, i64, i32, i32, ctypes.POINTER(i64)]
+    lib.ssm_gated_scan_fwd.argtypes = [i64, i64, i64, i32] + [vp] * 7 + [f32] + [vp] * 5 + [i64, vp]
+    lib.ssm_gated_scan_bwd.argtypes = [i64, i64, i64, i32] + [vp] * 7 + [f32] + [vp] * 13 + [i64, vp]
+    lib.ssm_gated_scan_packed_fwd.argtypes = [packed, i64, i32] + [vp] * 7 + [f32, vp, cache, gstrides, vp, i64, vp]
+    lib.ssm_gated_update_cache.argtypes = [i64, i64, i32, cache, vp] + [vp] * 7 + [f32, vp, gstrides, vp]
+    for name in EXPORTED[EXPORTED.index("ssm_causal_conv1d_packed_fwd"):]:
         getattr(lib, name).restype = i32
     lib.ssm_status_string.argtypes = [i32]
     lib.ssm_status_string.restype = ctypes.c_char_p
@@ -526,6 +538,8 @@ def abi_version() -> int:
 from .serving import (ssm_cache_load_q8, ssm_cache_store_q8, ssm_causal_conv1d_packed_fwd,  # noqa: E402
                       ssm_causal_conv1d_update_cache, ssm_scan_packed_fwd, ssm_scan_packed_workspace,
                       ssm_ssd_state_update_cache, ssm_state_update_cache)
+from .gated import (gated_checkpoint_shape, ssm_gated_scan_bwd_ckpt, ssm_gated_scan_fwd, ssm_gated_scan_fwd_ckpt,  # noqa: E402
+                    ssm_gated_scan_packed_fwd, ssm_gated_scan_workspace, ssm_gated_update_cache)
 
 __all__ = ["ssm_scan_fwd", "ssm_scan_bwd", "ssm_state_update", "ssm_causal_conv1d_fwd", "ssm_causal_conv1d_update",
            "ssm_ssd_fwd", "ssm_ssd_state_update", "SsdOpts", "BwdOpts", "abi_version", "load_library", "SsmError", "ScanOpts", "UpdateOpts",
@@ -533,4 +547,6 @@ __all__ = ["ssm_scan_fwd", "ssm_scan_bwd", "ssm_state_update", "ssm_causal_conv1
            "ssm_causal_conv1d_packed_fwd", "ssm_scan_packed_fwd", "ssm_scan_packed_workspace",
            "ssm_causal_conv1d_update_cache", "ssm_state_update_cache", "ssm_ssd_state_update_cache",
            "ssm_cache_store_q8", "ssm_cache_load_q8",
+           "ssm_gated_scan_fwd", "ssm_gated_scan_fwd_ckpt", "ssm_gated_scan_bwd_ckpt", "gated_checkpoint_shape",
+           "ssm_gated_scan_packed_fwd", "ssm_gated_scan_workspace", "ssm_gated_update_cache",
            "LIBRARY", "EXPORTED"]

@@ -1,0 +1,344 @@
+// gated_api.hip -- the entry points of the gated recurrence (include/ssm.h): host-side validation, launch
+// shapes and launches.
+#include <hip/hip_runtime.h>
+
+#include <cmath>
+
+#include "../../include/ssm.h"
+#include "cache_host.hpp"
+#include "gated_scan.hpp"
+
+using namespace ssm_host;
+
+namespace {
+
+// A kernel and the rows of its tiles.
+struct Tiled {
+  void (*kernel)(const ssm::GatedArgs);
+  int64_t rows;
+};
+template <bool BF16, int V, int R>
+Tiled forward_of() {
+  return {ssm::gated_scan_kernel<BF16, V, R>, ssm::GatedShape<V, R>::kRows};
+}
+template <bool BF16, int V, int R>
+Tiled backward_of() {
+  return {ssm::gated_scan_bwd_kernel<BF16, V, R>, ssm::GatedShape<V, R>::kRows};
+}
+
+// The forward's shape: 8 bytes of a bf16 row or of an fp32 row a lane.  Single channels where dim has fewer.
+Tiled forward_kernel(bool bf16, int64_t dim) {
+  if (dim < 4) return bf16 ? forward_of<true, 1, 8>() : forward_of<false, 1, 8>();
+  return bf16 ? forward_of<true, 4, 8>() : forward_of<false, 2, 8>();
+}
+Tiled backward_kernel(bool bf16, int64_t dim) {
+  if (dim < 2) return bf16 ? backward_of<true, 1, 16>() : backward_of<false, 1, 16>();
+  return bf16 ? backward_of<true, 2, 8>() : backward_of<false, 2, 8>();
+}
+
+constexpr int64_t kTicketBytes = 16;
+
+// Tiles of `rows` rows and the bytes that they publish through (0 where one tile has no other to tell)
+ssm_status_t tiles_of(const Tiled& t, int64_t rows, int64_t dim, int64_t* tiles, int64_t* published) {
+  *tiles = (rows + t.rows - 1) / t.rows;
+  *published = 0;
+  int64_t n;
+  if (*tiles <= 1) return SSM_OK;
+  if (!mul_ok(*tiles, dim, &n) || !mul_ok(n, 12, &n) || __builtin_add_overflow(n, kTicketBytes + 15, &n))
+    return fail(SSM_ERR_INVALID_ARG, "workspace size overflows int64");
+  *published = n / 16 * 16;
+  return SSM_OK;
+}
+
+ssm_status_t check_sizes(int64_t rows, int64_t dim, ssm_dtype_t dtype) {
+  if (dim < 0) return fail(SSM_ERR_INVALID_ARG, "negative size (dim=%lld)", (long long)dim);
+  if (rows > kMaxIndex) return fail(SSM_ERR_UNSUPPORTED, "more than 2^31-1 rows");
+  if (dtype != SSM_F32 && dtype != SSM_BF16) return fail(SSM_ERR_UNSUPPORTED, "unknown dtype %d", (int)dtype);
+  return SSM_OK;
+}
+
+ssm_status_t workspace_of(int64_t rows, int64_t dim, bool bf16, bool backward, int64_t* bytes) {
+  int64_t tiles;
+  *bytes = 0;
+  if (rows == 0 || dim == 0) return SSM_OK;
+  SSM_TRY(tiles_of(backward ? backward_kernel(bf16, dim) : forward_kernel(bf16, dim), rows, dim, &tiles, bytes));
+  if (backward) {
+    int64_t n;
+    if (!mul_ok(tiles, dim, &n) || !mul_ok(n, 12, &n) || __builtin_add_overflow(*bytes, n, bytes))
+      return fail(SSM_ERR_INVALID_ARG, "workspace size overflows int64");
+  }
+  return SSM_OK;
+}
+
+ssm_status_t check_params(const float* param, const float* ab, const float* xb, float scale) {
+  if (!aligned(param, 4) || !aligned(ab, 4) || !aligned(xb, 4))
+    return fail(SSM_ERR_MISALIGNED, "a_param, a_bias or x_bias is not 4-byte aligned");
+  if (!(scale >= 0.0f) || std::isinf(scale))
+    return fail(SSM_ERR_INVALID_ARG, "a_scale %g is not a finite number of at least 0", (double)scale);
+  return SSM_OK;
+}
+
+ssm_status_t check_workspace(const void* workspace, int64_t bytes, int64_t need) {
+  if (need == 0) return SSM_OK;
+  if (!workspace || bytes < need)
+    return fail(SSM_ERR_INVALID_ARG, "workspace of %lld bytes, need %lld", workspace ? (long long)bytes : 0ll,
+                (long long)need);
+  if (!aligned(workspace, 16)) return fail(SSM_ERR_MISALIGNED, "workspace (%p) is not 16-byte aligned", workspace);
+  return SSM_OK;
+}
+
+// Clears the words that tiles publish and launches the kernel over all tiles.
+ssm_status_t launch_tiles(const Tiled& t, ssm::GatedArgs& a, int64_t tiles, int64_t published, void* workspace,
+                          hipStream_t st, const char* what) {
+  int64_t grid;
+  const int64_t chains = (a.dim + ssm::kGatedChannels - 1) / ssm::kGatedChannels;
+  if (!mul_ok(chains, tiles, &grid) || grid > kMaxBlocks) return fail(SSM_ERR_UNSUPPORTED, "grid too large");
+  const int64_t words = published / 16, blocks = (words + 255) / 256;
+  if (blocks > kMaxBlocks) return fail(SSM_ERR_UNSUPPORTED, "grid too large");
+  a.tiles = tiles;
+  a.chains = static_cast<int32_t>(chains);
+  if (published) {
+    char* w = static_cast<char*>(workspace);
+    a.ticket = reinterpret_cast<uint32_t*>(w);
+    a.maps = reinterpret_cast<uint64_t*>(w + kTicketBytes);
+    a.ends = reinterpret_cast<uint32_t*>(w + kTicketBytes + tiles * a.dim * 8);
+    hipLaunchKernelGGL(ssm::gated_clear_kernel, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, st,
+                       reinterpret_cast<ssm::U32x4*>(w), words);
+    SSM_TRY(check_launch("gated scan (clear)"));
+  }
+  hipLaunchKernelGGL(t.kernel, dim3(static_cast<unsigned>(grid)), dim3(ssm::kGatedThreads), 0, st, a);
+  return check_launch(what);
+}
+
+ssm_status_t keep_states(const float* in, float* out, int64_t n, hipStream_t st) {
+  const int64_t blocks = (n + 255) / 256;
+  if (blocks > kMaxBlocks) return fail(SSM_ERR_UNSUPPORTED, "grid too large");
+  hipLaunchKernelGGL(ssm::gated_keep_kernel, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, st, in, out, n);
+  return check_launch("gated scan (states of no rows)");
+}
+
+struct Batch {
+  int64_t rows, elems, bytes, states;  // bytes of a (batch, seqlen, dim) tensor and of a (batch, dim) fp32 one
+};
+ssm_status_t check_batch(int64_t batch, int64_t seqlen, int64_t dim, ssm_dtype_t dtype, Batch* b) {
+  if (batch < 0 || seqlen < 0 || dim < 0)
+    return fail(SSM_ERR_INVALID_ARG, "negative size (batch=%lld seqlen=%lld dim=%lld)", (long long)batch,
+                (long long)seqlen, (long long)dim);
+  const int64_t es = dtype == SSM_BF16 ? 2 : 4;
+  if (!mul_ok(batch, seqlen, &b->rows) || !mul_ok(b->rows, dim, &b->elems) || !mul_ok(b->elems, es, &b->bytes) ||
+      !mul_ok(batch, dim, &b->states) || !mul_ok(b->states, 4, &b->states))
+    return fail(SSM_ERR_INVALID_ARG, "tensor size overflows int64");
+  if (batch > kMaxIndex) return fail(SSM_ERR_UNSUPPORTED, "batch exceeds int32");
+  return check_sizes(b->rows, dim, dtype);
+}
+
+ssm_status_t first_misaligned(const Arg* args, size_t n) {
+  if (const Arg* m = misaligned(args, n))
+    return fail(SSM_ERR_MISALIGNED, "%s (%p) is not aligned to its element size", m->name, m->p);
+  return SSM_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+ssm_status_t ssm_gated_scan_workspace(int64_t rows, int64_t dim, ssm_dtype_t dtype, int backward, int64_t* bytes) {
+  g_err[0] = '\0';
+  if (!bytes) return fail(SSM_ERR_INVALID_ARG, "NULL bytes");
+  if (rows < 0) return fail(SSM_ERR_INVALID_ARG, "negative size (rows=%lld)", (long long)rows);
+  SSM_TRY(check_sizes(rows, dim, dtype));
+  return workspace_of(rows, dim, dtype == SSM_BF16, backward != 0, bytes);
+}
+
+ssm_status_t ssm_gated_scan_fwd(int64_t batch, int64_t seqlen, int64_t dim, ssm_dtype_t dtype, const void* x,
+                                const void* a_gate, const void* x_gate, const float* a_param, const float* a_bias,
+                                const float* x_bias, const void* z, float a_scale, const float* initial_state, void* y,
+                                float* last_state, float* checkpoints, void* workspace, int64_t workspace_bytes,
+                                void* stream) {
+  g_err[0] = '\0';
+  Batch n;
+  SSM_TRY(check_batch(batch, seqlen, dim, dtype, &n));
+  SSM_TRY(check_params(a_param, a_bias, x_bias, a_scale));
+  const int64_t es = dtype == SSM_BF16 ? 2 : 4;
+  const Arg args[] = {{x, es, "x"}, {a_gate, es, "a_gate"}, {x_gate, es, "x_gate"}, {z, es, "z"}, {y, es, "y"},
+                      {initial_state, 4, "initial_state"}, {last_state, 4, "last_state"}, {checkpoints, 4, "checkpoints"}};
+  SSM_TRY(first_misaligned(args, sizeof args / sizeof *args));
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  const Range r0{initial_state, n.states}, r1{last_state, n.states};
+  if (n.elems == 0) {
+    if (overlap(r0, r1)) return fail(SSM_ERR_INVALID_ARG, "an output overlaps an input");
+    if (!last_state || n.states == 0) return SSM_OK;
+    return keep_states(initial_state, last_state, n.states / 4, st);
+  }
+  if (!x || !a_gate || !x_gate || !a_param || !y)
+    return fail(SSM_ERR_INVALID_ARG, "NULL required pointer (x, a_gate, x_gate, a_param and y)");
+  const Tiled t = forward_kernel(dtype == SSM_BF16, dim);
+  int64_t tiles, published;
+  SSM_TRY(tiles_of(t, n.rows, dim, &tiles, &published));
+  SSM_TRY(check_workspace(workspace, workspace_bytes, published));
+  const Range outs[] = {{y, n.bytes}, r1, {checkpoints, n.rows / ssm::kGatedSave * dim * 4}, {workspace, published}};
+  const Range ins[] = {{x, n.bytes}, {a_gate, n.bytes}, {x_gate, n.bytes}, {z, n.bytes}, r0,
+                       {a_param, dim * 4}, {a_bias, dim * 4}, {x_bias, dim * 4}};
+  SSM_TRY(check_overlap(outs, count_of(outs), ins, count_of(ins)));
+  ssm::GatedArgs a{};
+  a.x = x; a.ag = a_gate; a.xg = x_gate; a.z = z; a.y = y;
+  a.param = a_param; a.ab = a_bias; a.xb = x_bias; a.scale = a_scale;
+  a.sx = a.sag = a.sxg = a.sz = a.sy = dim;
+  a.total = n.rows; a.dim = dim; a.seqlen = seqlen; a.nseq = batch;
+  a.in = {const_cast<float*>(initial_state), batch, dim};
+  a.out = {last_state, batch, dim};
+  a.ckpt = checkpoints;
+  return launch_tiles(t, a, tiles, published, workspace, st, "gated scan");
+}
+
+ssm_status_t ssm_gated_scan_bwd(int64_t batch, int64_t seqlen, int64_t dim, ssm_dtype_t dtype, const void* x,
+                                const void* a_gate, const void* x_gate, const float* a_param, const float* a_bias,
+                                const float* x_bias, const void* z, float a_scale, const float* initial_state,
+                                const float* checkpoints, const void* dy, const float* dlast_state, void* dx,
+                                void* da_gate, void* dx_gate, float* da_param, float* da_bias, float* dx_bias, void* dz,
+                                float* dinitial_state, void* workspace, int64_t workspace_bytes, void* stream) {
+  g_err[0] = '\0';
+  Batch n;
+  SSM_TRY(check_batch(batch, seqlen, dim, dtype, &n));
+  SSM_TRY(check_params(a_param, a_bias, x_bias, a_scale));
+  const int64_t es = dtype == SSM_BF16 ? 2 : 4;
+  const Arg args[] = {{x, es, "x"}, {a_gate, es, "a_gate"}, {x_gate, es, "x_gate"}, {z, es, "z"}, {dy, es, "dy"},
+                      {dx, es, "dx"}, {da_gate, es, "da_gate"}, {dx_gate, es, "dx_gate"}, {dz, es, "dz"},
+                      {initial_state, 4, "initial_state"}, {checkpoints, 4, "checkpoints"},
+                      {dlast_state, 4, "dlast_state"}, {da_param, 4, "da_param"}, {da_bias, 4, "da_bias"},
+                      {dx_bias, 4, "dx_bias"}, {dinitial_state, 4, "dinitial_state"}};
+  SSM_TRY(first_misaligned(args, sizeof args / sizeof *args));
+  if (dim == 0) return SSM_OK;
+  if (!a_param || !da_param) return fail(SSM_ERR_INVALID_ARG, "NULL required pointer (a_param and da_param)");
+  if (n.elems > 0 && (!x || !a_gate || !x_gate || !dy || !dx || !da_gate || !dx_gate))
+    return fail(SSM_ERR_INVALID_ARG, "NULL required pointer (x, a_gate, x_gate, dy, dx, da_gate and dx_gate)");
+  if (n.elems > 0 && z && !dz) return fail(SSM_ERR_INVALID_ARG, "z needs dz");
+  const Tiled t = backward_kernel(dtype == SSM_BF16, dim);
+  int64_t tiles, published, need;
+  SSM_TRY(tiles_of(t, n.rows, dim, &tiles, &published));
+  SSM_TRY(workspace_of(n.rows, dim, dtype == SSM_BF16, true, &need));
+  SSM_TRY(check_workspace(workspace, workspace_bytes, need));
+  const int64_t saved = n.rows / ssm::kGatedSave * dim * 4;
+  if (tiles > 1 && !checkpoints) return fail(SSM_ERR_INVALID_ARG, "NULL checkpoints");
+  const Range outs[] = {{dx, n.bytes}, {da_gate, n.bytes}, {dx_gate, n.bytes}, {z ? dz : nullptr, n.bytes},
+                        {da_param, dim * 4}, {da_bias, dim * 4}, {dx_bias, dim * 4}, {dinitial_state, n.states},
+                        {workspace, need}};
+  const Range ins[] = {{x, n.bytes}, {a_gate, n.bytes}, {x_gate, n.bytes}, {z, n.bytes}, {dy, n.bytes},
+                       {initial_state, n.states}, {checkpoints, saved}, {dlast_state, n.states},
+                       {a_param, dim * 4}, {a_bias, dim * 4}, {x_bias, dim * 4}};
+  SSM_TRY(check_overlap(outs, count_of(outs), ins, count_of(ins)));
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  ssm::GatedSumArgs sum{};
+  sum.param = a_param; sum.dparam = da_param; sum.dab = da_bias; sum.dxb = dx_bias; sum.dim = dim;
+  if (n.elems > 0) {
+    ssm::GatedArgs a{};
+    a.x = x; a.ag = a_gate; a.xg = x_gate; a.z = z; a.dy = dy;
+    a.param = a_param; a.ab = a_bias; a.xb = x_bias; a.scale = a_scale;
+    a.total = n.rows; a.dim = dim; a.seqlen = seqlen; a.nseq = batch;
+    a.in = {const_cast<float*>(initial_state), batch, dim};
+    a.ckpt = const_cast<float*>(checkpoints);
+    a.dlast = dlast_state; a.dx = dx; a.dag = da_gate; a.dxg = dx_gate; a.dz = dz; a.dh0 = dinitial_state;
+    a.partial = reinterpret_cast<float*>(static_cast<char*>(workspace) + published);
+    sum.partial = a.partial;
+    sum.tiles = tiles;
+    SSM_TRY(launch_tiles(t, a, tiles, published, workspace, st, "gated scan backward"));
+  } else if (dinitial_state && n.states > 0) {
+    SSM_TRY(keep_states(dlast_state, dinitial_state, n.states / 4, st));
+  }
+  const int64_t blocks = (dim + 63) / 64;
+  if (blocks > kMaxBlocks / 4) return fail(SSM_ERR_UNSUPPORTED, "grid too large");
+  hipLaunchKernelGGL(ssm::gated_sum_kernel, dim3(static_cast<unsigned>(blocks), 3), dim3(ssm::kGatedSumThreads), 0, st,
+                     sum);
+  return check_launch("gated scan backward (sums)");
+}
+
+ssm_status_t ssm_gated_scan_packed_fwd(const ssm_packed_t* seqs, int64_t dim, ssm_dtype_t dtype, const void* x,
+                                       const void* a_gate, const void* x_gate, const float* a_param,
+                                       const float* a_bias, const float* x_bias, const void* z, float a_scale, void* y,
+                                       const ssm_cache_t* cache, const ssm_gated_strides_t* strides, void* workspace,
+                                       int64_t workspace_bytes, void* stream) {
+  g_err[0] = '\0';
+  SSM_TRY(check_packed(seqs));
+  SSM_TRY(check_sizes(seqs->total, dim, dtype));
+  SSM_TRY(check_params(a_param, a_bias, x_bias, a_scale));
+  const int64_t es = dtype == SSM_BF16 ? 2 : 4;
+  ssm::GatedArgs a{};
+  Range rc{nullptr, 0};
+  if (cache) SSM_TRY(check_cache(cache, dim, &a.in, &rc));
+  ssm_gated_strides_t rs = strides ? *strides : ssm_gated_strides_t{};
+  Rows t[] = {{x, dim, &rs.x, "x", 0}, {a_gate, dim, &rs.a_gate, "a_gate", 0}, {x_gate, dim, &rs.x_gate, "x_gate", 0},
+              {z, dim, &rs.z, "z", 0}, {y, dim, &rs.y, "y", 0}};
+  SSM_TRY(check_rows(t, 5, seqs->total, es));
+  if (seqs->total == 0 || seqs->sequences == 0 || dim == 0) return SSM_OK;
+  if (!x || !a_gate || !x_gate || !a_param || !y)
+    return fail(SSM_ERR_INVALID_ARG, "NULL required pointer (x, a_gate, x_gate, a_param and y)");
+  Range idx[3];
+  SSM_TRY(check_packed_pointers(seqs, idx));
+  const Tiled k = forward_kernel(dtype == SSM_BF16, dim);
+  int64_t tiles, published;
+  SSM_TRY(tiles_of(k, seqs->total, dim, &tiles, &published));
+  SSM_TRY(check_workspace(workspace, workspace_bytes, published));
+  const Range outs[] = {{y, t[4].bytes}, rc, {workspace, published}};
+  const Range ins[] = {{x, t[0].bytes}, {a_gate, t[1].bytes}, {x_gate, t[2].bytes}, {z, t[3].bytes}, {a_param, dim * 4},
+                       {a_bias, dim * 4}, {x_bias, dim * 4}, idx[0], idx[1], idx[2]};
+  SSM_TRY(check_overlap(outs, count_of(outs), ins, count_of(ins)));
+  a.x = x; a.ag = a_gate; a.xg = x_gate; a.z = z; a.y = y;
+  a.param = a_param; a.ab = a_bias; a.xb = x_bias; a.scale = a_scale;
+  a.sx = rs.x; a.sag = rs.a_gate; a.sxg = rs.x_gate; a.sz = rs.z; a.sy = rs.y;
+  a.total = seqs->total; a.dim = dim; a.nseq = seqs->sequences;
+  a.cu = seqs->cu_seqlens; a.slots = seqs->cache_slots; a.has_initial = seqs->has_initial;
+  a.out = a.in;
+  a.cb16 = cache && cache->dtype == SSM_BF16;
+  return launch_tiles(k, a, tiles, published, workspace, static_cast<hipStream_t>(stream), "gated scan (packed)");
+}
+
+ssm_status_t ssm_gated_update_cache(int64_t batch, int64_t dim, ssm_dtype_t dtype, const ssm_cache_t* cache,
+                                    const int32_t* cache_slots, const void* x, const void* a_gate, const void* x_gate,
+                                    const float* a_param, const float* a_bias, const float* x_bias, const void* z,
+                                    float a_scale, void* y, const ssm_gated_strides_t* strides, void* stream) {
+  g_err[0] = '\0';
+  if (batch < 0) return fail(SSM_ERR_INVALID_ARG, "bad size (batch=%lld)", (long long)batch);
+  SSM_TRY(check_sizes(batch, dim, dtype));
+  SSM_TRY(check_params(a_param, a_bias, x_bias, a_scale));
+  if (!cache) return fail(SSM_ERR_INVALID_ARG, "NULL cache");
+  const int64_t es = dtype == SSM_BF16 ? 2 : 4;
+  ssm::GatedStepArgs q{};
+  ssm::GatedArgs& a = q.g;
+  Range rc;
+  SSM_TRY(check_cache(cache, dim, &a.in, &rc));
+  ssm_gated_strides_t rs = strides ? *strides : ssm_gated_strides_t{};
+  Rows t[] = {{x, dim, &rs.x, "x", 0}, {a_gate, dim, &rs.a_gate, "a_gate", 0}, {x_gate, dim, &rs.x_gate, "x_gate", 0},
+              {z, dim, &rs.z, "z", 0}, {y, dim, &rs.y, "y", 0}};
+  SSM_TRY(check_rows(t, 5, batch, es));
+  if (batch == 0 || dim == 0 || cache->slots == 0) return SSM_OK;
+  if (!x || !a_gate || !x_gate || !a_param || !y)
+    return fail(SSM_ERR_INVALID_ARG, "NULL required pointer (x, a_gate, x_gate, a_param and y)");
+  if (!aligned(cache_slots, 4)) return fail(SSM_ERR_MISALIGNED, "cache_slots is not 4-byte aligned");
+  const Range outs[] = {{y, t[4].bytes}, rc};
+  const Range ins[] = {{x, t[0].bytes}, {a_gate, t[1].bytes}, {x_gate, t[2].bytes}, {z, t[3].bytes}, {a_param, dim * 4},
+                       {a_bias, dim * 4}, {x_bias, dim * 4}, {cache_slots, batch * 4}};
+  SSM_TRY(check_overlap(outs, count_of(outs), ins, count_of(ins)));
+  a.x = x; a.ag = a_gate; a.xg = x_gate; a.z = z; a.y = y;
+  a.param = a_param; a.ab = a_bias; a.xb = x_bias; a.scale = a_scale;
+  a.sx = rs.x; a.sag = rs.a_gate; a.sxg = rs.x_gate; a.sz = rs.z; a.sy = rs.y;
+  a.dim = dim; a.slots = cache_slots; q.batch = batch;
+  const bool bf16 = dtype == SSM_BF16, cb16 = cache->dtype == SSM_BF16;
+  using Kernel = void (*)(const ssm::GatedStepArgs);
+  const int64_t v = dim < 4 ? 1 : 4;
+  const int64_t blocks = ((dim + v - 1) / v + ssm::kGatedThreads - 1) / ssm::kGatedThreads;
+  if (blocks > kMaxBlocks) return fail(SSM_ERR_UNSUPPORTED, "grid too large");
+  const int R = v == 4 ? step_entries(blocks, batch) : 1;
+  const auto pick = [&](auto B, auto C) -> Kernel {
+    constexpr bool b = decltype(B)::value, c = decltype(C)::value;
+    return v == 1 ? ssm::gated_step_kernel<b, c, 1, 1>
+                  : R > 1 ? ssm::gated_step_kernel<b, c, 4, kStepEntries> : ssm::gated_step_kernel<b, c, 4, 1>;
+  };
+  using T = std::true_type;
+  using F = std::false_type;
+  const Kernel k = bf16 ? (cb16 ? pick(T{}, T{}) : pick(T{}, F{})) : (cb16 ? pick(F{}, T{}) : pick(F{}, F{}));
+  hipLaunchKernelGGL(k, dim3(static_cast<unsigned>(blocks), grid_y((batch + R - 1) / R)), dim3(ssm::kGatedThreads), 0,
+                     static_cast<hipStream_t>(stream), q);
+  return check_launch("gated step (cache)");
+}
+
+}  // extern "C"
