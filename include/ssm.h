@@ -784,6 +784,79 @@ SSM_API ssm_status_t ssm_gated_update_cache(int64_t batch, int64_t dim, ssm_dtyp
                                             const float *x_bias, const void *z, float a_scale, void *y,
                                             const ssm_gated_strides_t *strides, void *stream);
 
+/*
+ * ---- Beam search ---------------------------------------------------------
+ *
+ * Between two single-token steps a server that searches with beams chooses the
+ * best continuations of all of a sequence's hypotheses and makes each kept one
+ * go on from its parent's state ("Mamba 论文精读" sec. 6: the fixed-size state
+ * is all that a sequence carries, so a hypothesis forks by copying it).
+ *
+ * Candidate (j, v), token v after hypothesis j, has the value
+ *
+ *   scores[j] + (logits[j, v] - lse_j),  lse_j = log sum_v exp(logits[j, v])
+ *
+ *   logits       (batch, rows, vocab) dtype: rows of contiguous elements,
+ *                stride_row and stride_batch elements apart (0: contiguous);
+ *                at any alignment of their elements
+ *   scores       (batch, rows) fp32
+ *   finished     (batch, rows) bytes, or NULL: a finished row (not 0) has the
+ *                one candidate eos, whose value is its score; its logits are
+ *                not read
+ *   parents, tokens, out_scores  (batch, beams) int32, int32 and fp32: the
+ *                candidates of the largest values, largest first.  Of each row
+ *                the largest logits are taken, equal ones by the lower token;
+ *                what is taken of all rows goes by its value in 64 bits, equal
+ *                ones by the lower j * vocab + v
+ *   out_finished (batch, beams) bytes, or NULL: 1 if the parent was finished
+ *                or the token is eos; needs finished
+ *   workspace    ssm_beam_select_workspace bytes, 16-byte aligned, the caller's
+ *                until the call's work is done
+ *
+ * rows and beams are 1..64, beams at most rows * vocab.  A row whose score is
+ * not finite, or whose lse is not (a NaN or +inf logit, or all -inf), is dead:
+ * its candidates are its lowest tokens, at -inf.  Candidates at -inf (masked
+ * logits, dead rows, other tokens of a finished row) are taken when there are
+ * too few others.  exp and the sums of a row's pieces are fp32, the rest of
+ * the value is 64 bits, rounded once to out_scores.
+ */
+SSM_API ssm_status_t ssm_beam_select(int64_t batch, int64_t rows, int64_t vocab, int64_t beams, ssm_dtype_t dtype,
+                                     const void *logits, int64_t stride_batch, int64_t stride_row, const float *scores,
+                                     const uint8_t *finished, int64_t eos, int32_t *parents, int32_t *tokens,
+                                     float *out_scores, uint8_t *out_finished, void *workspace,
+                                     int64_t workspace_bytes, void *stream);
+SSM_API ssm_status_t ssm_beam_select_workspace(int64_t batch, int64_t rows, int64_t vocab, int64_t beams,
+                                               ssm_dtype_t dtype, int64_t *bytes);
+
+/* Entries of a cache as bytes, whatever they hold: `bytes` of each slot,
+ * slot_stride bytes from one to the next (0: bytes), at any alignment. */
+typedef struct {
+  void *data;
+  int64_t slots;
+  int64_t slot_stride;
+  int64_t bytes;
+} ssm_entries_t;
+
+/*
+ * Beam i of sequence b takes the entry of beam parents[b, i], in place and in
+ * each of `count` caches:
+ *
+ *   data[cache_slots[b, i]] <- data[cache_slots[b, parents[b, i]]]  (old values)
+ *
+ *   cache_slots  (batch, beams) int32 on the device, or NULL: slot b * beams + i.
+ *                Slots must differ from one another
+ *   parents      (batch, beams) int32 on the device, as ssm_beam_select gives
+ *                them; several beams may have one parent
+ *   caches       descriptors, in host memory, of caches that do not overlap
+ *
+ * beams is 1..64.  A beam without a slot (negative, or past the cache's slots),
+ * of a parent out of range or without a slot, or that is its own parent keeps
+ * its entry.  Each entry that is some other beam's parent is read once and each
+ * one that changes written once.
+ */
+SSM_API ssm_status_t ssm_cache_reorder(int64_t batch, int64_t beams, const ssm_entries_t *caches, int64_t count,
+                                       const int32_t *cache_slots, const int32_t *parents, void *stream);
+
 /* Static string naming a status code ("SSM_OK", ...); never NULL. */
 SSM_API const char *ssm_status_string(ssm_status_t status);
 

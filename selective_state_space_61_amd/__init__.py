@@ -15,7 +15,8 @@ D, delta_bias (dim,) fp32; y like x; last_state / state (batch, dim, dstate) fp3
 z and y share one dtype: torch.float32 or torch.bfloat16.
 
 For serving (packed prompts, single tokens on a cache of slots, states set aside in 8 bits) see
-``serving.py``, for the gated recurrence ``gated.py``; this module exports their functions too.
+``serving.py``, for the gated recurrence ``gated.py``, for beam search on cached states ``beams.py``;
+this module exports their functions too.
 """
 from __future__ import annotations
 
@@ -39,7 +40,7 @@ EXPORTED = ("ssm_scan_fwd", "ssm_scan_fwd_ex", "ssm_scan_fwd_noalloc", "ssm_scan
             "ssm_causal_conv1d_update_cache", "ssm_state_update_cache", "ssm_ssd_state_update_cache",
             "ssm_cache_store_q8", "ssm_cache_load_q8",
             "ssm_gated_scan_workspace", "ssm_gated_scan_fwd", "ssm_gated_scan_bwd", "ssm_gated_scan_packed_fwd",
-            "ssm_gated_update_cache")
+            "ssm_gated_update_cache", "ssm_beam_select", "ssm_beam_select_workspace", "ssm_cache_reorder")
 
 
 class SsmError(RuntimeError):
@@ -83,6 +84,11 @@ class RowStrides(ctypes.Structure):
 
 class GatedStrides(ctypes.Structure):
     _fields_ = [(k, ctypes.c_int64) for k in ("x", "a_gate", "x_gate", "z", "y")]
+
+
+class Entries(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("slots", ctypes.c_int64), ("slot_stride", ctypes.c_int64),
+                ("bytes", ctypes.c_int64)]
 
 
 SSM_BBAR_DELTA_B, SSM_BBAR_ZOH = 0, 1
@@ -150,6 +156,9 @@ def load_library(path: str = LIBRARY) -> ctypes.CDLL:
     lib.ssm_gated_scan_bwd.argtypes = [i64, i64, i64, i32] + [vp] * 7 + [f32] + [vp] * 13 + [i64, vp]
     lib.ssm_gated_scan_packed_fwd.argtypes = [packed, i64, i32] + [vp] * 7 + [f32, vp, cache, gstrides, vp, i64, vp]
     lib.ssm_gated_update_cache.argtypes = [i64, i64, i32, cache, vp] + [vp] * 7 + [f32, vp, gstrides, vp]
+    lib.ssm_beam_select.argtypes = [i64, i64, i64, i64, i32, vp, i64, i64, vp, vp, i64, vp, vp, vp, vp, vp, i64, vp]
+    lib.ssm_beam_select_workspace.argtypes = [i64, i64, i64, i64, i32, ctypes.POINTER(i64)]
+    lib.ssm_cache_reorder.argtypes = [i64, i64, ctypes.POINTER(Entries), i64, vp, vp, vp]
     for name in EXPORTED[EXPORTED.index("ssm_causal_conv1d_packed_fwd"):]:
         getattr(lib, name).restype = i32
     lib.ssm_status_string.argtypes = [i32]
@@ -540,6 +549,7 @@ from .serving import (ssm_cache_load_q8, ssm_cache_store_q8, ssm_causal_conv1d_p
                       ssm_ssd_state_update_cache, ssm_state_update_cache)
 from .gated import (gated_checkpoint_shape, ssm_gated_scan_bwd_ckpt, ssm_gated_scan_fwd, ssm_gated_scan_fwd_ckpt,  # noqa: E402
                     ssm_gated_scan_packed_fwd, ssm_gated_scan_workspace, ssm_gated_update_cache)
+from .beams import ssm_beam_select, ssm_beam_select_workspace, ssm_cache_reorder  # noqa: E402
 
 __all__ = ["ssm_scan_fwd", "ssm_scan_bwd", "ssm_state_update", "ssm_causal_conv1d_fwd", "ssm_causal_conv1d_update",
            "ssm_ssd_fwd", "ssm_ssd_state_update", "SsdOpts", "BwdOpts", "abi_version", "load_library", "SsmError", "ScanOpts", "UpdateOpts",
@@ -549,4 +559,5 @@ __all__ = ["ssm_scan_fwd", "ssm_scan_bwd", "ssm_state_update", "ssm_causal_conv1
            "ssm_cache_store_q8", "ssm_cache_load_q8",
            "ssm_gated_scan_fwd", "ssm_gated_scan_fwd_ckpt", "ssm_gated_scan_bwd_ckpt", "gated_checkpoint_shape",
            "ssm_gated_scan_packed_fwd", "ssm_gated_scan_workspace", "ssm_gated_update_cache",
+           "ssm_beam_select", "ssm_beam_select_workspace", "ssm_cache_reorder",
            "LIBRARY", "EXPORTED"]

@@ -11,11 +11,11 @@ CSRC = os.path.join(HERE, "csrc")
 LIBRARY = os.path.join(HERE, "libssm61.so")
 SOURCES = [os.path.join(CSRC, f) for f in ("ssm_api.hip", "scan_f32.hip", "scan_bf16.hip", "scan_zoh_f32.hip",
                                             "scan_zoh_bf16.hip", "ssd_bf16.hip", "scan_rows.hip", "scan_time.hip",
-                                            "scan_bwd_rows.hip", "cache_api.hip", "scan_packed.hip", "gated_api.hip")]
+                                            "scan_bwd_rows.hip", "cache_api.hip", "scan_packed.hip", "gated_api.hip", "beam_api.hip")]
 HEADERS = [os.path.join(CSRC, f) for f in ("ssm_device.hpp", "scan_fwd.hpp", "scan_table.hpp", "scan_rows.hpp", "scan_rows_table.hpp", "scan_time.hpp", "scan_time_table.hpp", "state_update.hpp",
                                                   "conv1d.hpp", "scan_bwd.hpp", "scan_bwd_rows.hpp", "ssd_fwd.hpp",
                                                   "host_util.hpp", "cache.hpp", "cache_step.hpp", "cache_q8.hpp", "conv1d_packed.hpp",
-                                                  "scan_packed.hpp", "cache_host.hpp", "gated_scan.hpp")] + [
+                                                  "scan_packed.hpp", "cache_host.hpp", "gated_scan.hpp", "beam.hpp")] + [
     os.path.join(os.path.dirname(HERE), "include", "ssm.h")]
 OBJDIR = os.path.join(HERE, "_build")
 ARCH = "gfx950"

@@ -1,0 +1,382 @@
+// beam.hpp -- beam search on cached states for gfx950: the selection over beams and vocabulary, and the
+// reordering of the states that follows it.
+//
+// Selection.  A candidate (j, v) of a sequence has the value score_j + (logit[j, v] - lse_j) with lse_j =
+// log sum_v exp(logit[j, v]); the `beams` largest are taken.  Two launches: every wave takes a stretch
+// of one row into registers, sums exp(logit - its largest) and keeps its largest `beams` logits; then a
+// workgroup a sequence joins its rows' stretches, adds lse and score in 64 bits (they rank candidates of
+// different rows) and ranks what is left.  Logits are read once.
+//
+// The largest k of a wave's values: the k-th largest of the 64 lanes' largest ones is a bound that at
+// least k values reach and few others do.  It is found bit by bit with a ballot each, what reaches it is
+// gathered (by ballots again) and ranked by comparing all with all.  Where more than 64 values reach
+// it (rows of few different values) the k are found one after another.
+#pragma once
+
+#include "cache.hpp"
+
+namespace ssm {
+
+constexpr int kBeamThreads = 256;
+constexpr int kBeamMost = 64;   // beams, and rows of a sequence
+constexpr int kBeamValues = 32;  // values of a lane
+
+struct BeamArgs {
+  const void* logits;
+  int64_t sb, sr;           // elements between sequences and rows
+  const float* scores;      // (batch, rows)
+  const uint8_t* finished;  // (batch, rows) or NULL
+  int32_t rows, beams, eos;
+  int64_t batch, vocab;
+  int32_t chunks, blocks;   // stretches of a row, 16-byte blocks of a stretch
+  uint64_t* best;           // (batch * rows, chunks, beams): key and token, largest first
+  float* stats;             // (batch * rows, chunks, 2): largest logit, sum of exp(logit - it)
+  int32_t *parents, *tokens;
+  float* out_scores;
+  uint8_t* out_finished;
+};
+
+// A value's key rises with it (-0 is 0); every key of a value is above 0.
+__device__ __forceinline__ uint32_t beam_key(float v) {
+  const uint32_t b = __builtin_bit_cast(uint32_t, v + 0.0f);
+  return b ^ (static_cast<uint32_t>(static_cast<int32_t>(b) >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float beam_logit(uint32_t key) {
+  const uint32_t b = key ^ (static_cast<uint32_t>(static_cast<int32_t>(~key) >> 31) | 0x80000000u);
+  return __builtin_bit_cast(float, b);
+}
+// Key and token in one word whose order is the candidates': equal keys by the lower token
+__device__ __forceinline__ uint64_t beam_word(uint32_t key, uint32_t token) {
+  return (static_cast<uint64_t>(key) << 32) | (0xffffffffu - token);
+}
+
+__device__ __forceinline__ uint64_t wave_max(uint64_t v) {
+  const uint32_t hi = static_cast<uint32_t>(v >> 32);
+  const uint32_t top = group_reduce<64>(hi, [](uint32_t a, uint32_t b) { return a > b ? a : b; });
+  const uint32_t lo = hi == top ? static_cast<uint32_t>(v) : 0u;
+  return (static_cast<uint64_t>(top) << 32) | group_reduce<64>(lo, [](uint32_t a, uint32_t b) { return a > b ? a : b; });
+}
+
+// A bound that the keys of at least k lanes reach (k at most 64), near the k-th largest
+__device__ __forceinline__ uint32_t kth_key(uint32_t key, int k) {
+  const uint32_t hi = __builtin_amdgcn_readfirstlane(group_reduce<64>(key, [](uint32_t a, uint32_t b) { return a > b ? a : b; }));
+  const uint32_t lo = __builtin_amdgcn_readfirstlane(group_reduce<64>(key, [](uint32_t a, uint32_t b) { return a < b ? a : b; }));
+  if (hi == lo) return hi;
+  int bit = 31 - __builtin_clz(hi ^ lo);
+  uint32_t t = bit == 31 ? 0u : hi >> (bit + 1) << (bit + 1);
+  for (; bit >= 12; --bit) {  // (11 bits of the mantissa: the few values more do not matter)
+    const uint32_t c = t | (1u << bit);
+    if (__popcll(__ballot(key >= c)) >= k) t = c;
+  }
+  return t;
+}
+
+// Rank of a lane's word among those of the first n lanes (no two of which are equal)
+__device__ __forceinline__ int rank_of(uint64_t w, int n) {
+  int rank = 0;
+  for (int i = 0; i < n; ++i) {
+    const uint64_t o = (static_cast<uint64_t>(__builtin_amdgcn_readlane(static_cast<uint32_t>(w >> 32), i)) << 32) |
+                       static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<uint32_t>(w), i));
+    rank += o > w;
+  }
+  return rank;
+}
+
+__device__ __forceinline__ bool is_finite(float v) { return __builtin_isfinite(v); }
+
+template <bool BF16>
+__global__ __launch_bounds__(kBeamThreads) void beam_rows_kernel(const BeamArgs p) {
+  constexpr int EPB = BF16 ? 8 : 4, IT = kBeamValues / EPB, ES = BF16 ? 2 : 4;
+  __shared__ uint64_t lists[kBeamThreads / 64][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t n = static_cast<int64_t>(blockIdx.x) * (kBeamThreads / 64) + wave;
+  const int64_t row = n / p.chunks;
+  const int chunk = static_cast<int>(n - row * p.chunks);
+  if (row >= p.batch * p.rows) return;
+  // what a finished or dead row holds does not matter
+  if (!is_finite(p.scores[row]) || (p.finished && p.finished[row])) return;
+  const int64_t seq = row / p.rows;
+  const char* base = static_cast<const char*>(p.logits) + (seq * p.sb + (row - seq * p.rows) * p.sr) * ES;
+  // Blocks of 16 bytes by token, at whatever alignment the row has (gfx950 takes wide loads at any), so that
+  // rows of the same values have the same sums, and tie.
+  const int64_t block0 = static_cast<int64_t>(chunk) * p.blocks;
+  uint32_t raw[IT][4];
+  uint32_t live = 0;  // blocks that hold values of the row
+#pragma unroll
+  for (int i = 0; i < IT; ++i) {
+    const int at = i * 64 + lane;
+    const int64_t first = (block0 + at) * EPB;  // the block's first token
+    raw[i][0] = raw[i][1] = raw[i][2] = raw[i][3] = BF16 ? 0xff80ff80u : 0xff800000u;  // -inf
+    if (at < p.blocks && first < p.vocab) {
+      live |= 1u << i;
+      if (first + EPB <= p.vocab) {
+        const U32x4 v = *reinterpret_cast<const typename Words<ES>::U4*>(base + first * ES);
+        raw[i][0] = v.x; raw[i][1] = v.y; raw[i][2] = v.z; raw[i][3] = v.w;
+      } else {
+#pragma unroll
+        for (int e = 0; e < EPB; ++e) {
+          if (first + e >= p.vocab) continue;
+          if constexpr (BF16) {
+            const uint32_t h = reinterpret_cast<const uint16_t*>(base)[first + e];
+            raw[i][e >> 1] = e & 1 ? (raw[i][e >> 1] & 0xffffu) | h << 16 : (raw[i][e >> 1] & 0xffff0000u) | h;
+          } else {
+            raw[i][e] = reinterpret_cast<const uint32_t*>(base)[first + e];
+          }
+        }
+      }
+    }
+  }
+  auto value = [&](int i, int e) {
+    if constexpr (BF16) return e & 1 ? bf16_hi(raw[i][e >> 1]) : bf16_lo(raw[i][e >> 1]);
+    else return __builtin_bit_cast(float, raw[i][e]);
+  };
+  float top = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < IT; ++i)
+#pragma unroll
+    for (int e = 0; e < EPB; ++e) top = fmaxf(top, value(i, e));
+  const uint32_t key = live ? beam_key(top) : 0u;
+  const float m = group_reduce<64>(top, [](float a, float b) { return fmaxf(a, b); });
+  const float shift = m == -INFINITY ? 0.0f : m;  // (NaN and +inf leave a NaN in the sum)
+  float s = 0.0f;
+#pragma unroll
+  for (int i = 0; i < IT; ++i)
+#pragma unroll
+    for (int e = 0; e < EPB; ++e) s += hw_exp2((value(i, e) - shift) * kLog2e);
+  s = group_sum<64>(s);
+  if (lane == 0) {
+    p.stats[2 * n] = m;
+    p.stats[2 * n + 1] = s;
+  }
+
+  const int k = p.beams;
+  const uint32_t bound = kth_key(key, k);
+  uint64_t* list = lists[wave];
+  int count = 0;
+#pragma unroll
+  for (int i = 0; i < IT; ++i) {
+    const int64_t first = (block0 + i * 64 + lane) * EPB;
+#pragma unroll
+    for (int e = 0; e < EPB; ++e) {
+      const uint32_t ke = beam_key(value(i, e));
+      const uint64_t on = __ballot((live >> i & 1) && ke >= bound && first + e < p.vocab);
+      if (on) {
+        const int at = count + __builtin_amdgcn_mbcnt_hi(static_cast<uint32_t>(on >> 32),
+                                                         __builtin_amdgcn_mbcnt_lo(static_cast<uint32_t>(on), 0));
+        if ((on >> lane & 1) && at < 64) list[at] = beam_word(ke, static_cast<uint32_t>(first + e));
+        count += __popcll(on);
+      }
+    }
+  }
+  uint64_t* out = p.best + n * k;
+  if (count <= 64) {
+    // the wave's own LDS: its writes are done before its reads
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    const uint64_t w = lane < count ? list[lane] : 0u;
+    const int rank = rank_of(w, count);
+    if (lane < count && rank < k) out[rank] = w;
+    if (lane >= count && lane < k) out[lane] = 0u;  // fewer values than beams
+    return;
+  }
+  uint64_t last = ~0ull;
+  for (int r = 0; r < k; ++r) {
+    uint64_t best = 0u;
+#pragma unroll
+    for (int i = 0; i < IT; ++i) {
+      const int64_t first = (block0 + i * 64 + lane) * EPB;
+#pragma unroll
+      for (int e = 0; e < EPB; ++e) {
+        const uint64_t w = beam_word(beam_key(value(i, e)), static_cast<uint32_t>(first + e));
+        if ((live >> i & 1) && first + e < p.vocab && w < last && w > best) best = w;
+      }
+    }
+    last = wave_max(best);
+    if (lane == 0) out[r] = last;
+    if (last == 0u) last = 1u;  // none left: the rest is 0 too
+  }
+}
+
+// One sequence a workgroup.
+__global__ __launch_bounds__(1024) static void beam_join_kernel(const BeamArgs p) {
+  __shared__ double values[kBeamMost * kBeamMost];
+  __shared__ int32_t tokens[kBeamMost * kBeamMost];
+  __shared__ uint64_t lists[16][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
+  const int k = static_cast<int>(p.vocab < p.beams ? p.vocab : p.beams);  // candidates of a row
+  const int64_t seq = blockIdx.x;
+  for (int j = wave; j < p.rows; j += waves) {
+    const int64_t row = seq * p.rows + j;
+    const float score = p.scores[row];
+    const bool done = p.finished && p.finished[row];
+    double lse = 0.0;
+    bool dead = !is_finite(score);
+    uint64_t* list = lists[wave];
+    if (!dead && !done) {
+      const float* st = p.stats + 2 * row * p.chunks;
+      float m = -INFINITY;
+      for (int c = lane; c < p.chunks; c += 64) m = fmaxf(m, st[2 * c]);
+      m = group_reduce<64>(m, [](float a, float b) { return fmaxf(a, b); });
+      double s = 0.0;
+      for (int c = lane; c < p.chunks; c += 64)
+        s += st[2 * c + 1] * static_cast<double>(st[2 * c] == m ? 1.0f : hw_exp2((st[2 * c] - m) * kLog2e));
+      for (int o = 32; o; o >>= 1) s += __shfl_xor(s, o);
+      lse = m + log(s);
+      dead = !is_finite(m) || !(s > 0.0) || !__builtin_isfinite(lse);
+    }
+    if (dead || done) {
+      // tokens in their order, all of no value but the end of a finished beam
+      if (lane < k) {
+        int t = lane;
+        double v = -INFINITY;
+        if (!dead) {
+          t = lane == 0 ? p.eos : (lane <= p.eos ? lane - 1 : lane);
+          if (lane == 0) v = score;
+        }
+        values[j * k + lane] = v;
+        tokens[j * k + lane] = t;
+      }
+      continue;
+    }
+    const uint64_t* best = p.best + row * p.chunks * p.beams;
+    const int n = p.chunks * p.beams;
+    uint64_t top = 0u;
+    for (int i = lane; i < n; i += 64) top = best[i] > top ? best[i] : top;
+    const uint32_t bound = kth_key(static_cast<uint32_t>(top >> 32), k);
+    int count = 0;
+    for (int i = lane; i - lane < n; i += 64) {
+      const uint64_t w = i < n ? best[i] : 0u;
+      const uint64_t on = __ballot(w != 0u && static_cast<uint32_t>(w >> 32) >= bound);
+      const int at = count + __builtin_amdgcn_mbcnt_hi(static_cast<uint32_t>(on >> 32),
+                                                       __builtin_amdgcn_mbcnt_lo(static_cast<uint32_t>(on), 0));
+      if ((on >> lane & 1) && at < 64) list[at] = w;
+      count += __popcll(on);
+    }
+    uint64_t mine = 0u;  // the lane-th largest
+    if (count <= 64) {
+      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+      const uint64_t w = lane < count ? list[lane] : 0u;
+      const int rank = rank_of(w, count);
+      __builtin_amdgcn_wave_barrier();
+      if (lane < count) list[rank] = w;
+      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+      mine = lane < k ? list[lane] : 0u;
+    } else {
+      uint64_t last = ~0ull;
+      for (int r = 0; r < k; ++r) {
+        uint64_t b = 0u;
+        for (int i = lane; i < n; i += 64) {
+          const uint64_t w = best[i];
+          if (w < last && w > b) b = w;
+        }
+        last = wave_max(b);
+        if (lane == r) mine = last;
+      }
+    }
+    // by value now: logits that differ may give one value, which then goes by the token
+    const double v = score + (static_cast<double>(beam_logit(static_cast<uint32_t>(mine >> 32))) - lse);
+    const int32_t t = static_cast<int32_t>(0xffffffffu - static_cast<uint32_t>(mine));
+    int rank = 0;
+    for (int i = 0; i < k; ++i) {
+      const double o = __shfl(v, i);
+      const int32_t u = __shfl(t, i);
+      rank += o > v || (o == v && u < t);
+    }
+    if (lane < k) {
+      values[j * k + rank] = v;
+      tokens[j * k + rank] = t;
+    }
+  }
+  __syncthreads();
+  // each candidate's rank: its place in its own row, and how many of every other row come before it
+  for (int i = threadIdx.x; i < p.rows * k; i += blockDim.x) {
+    const int j = i / k;
+    const double v = values[i];
+    int rank = i - j * k;
+    for (int o = 0; o < p.rows && rank < p.beams; ++o) {
+      if (o == j) continue;
+      int lo = 0, hi = k;  // the first that does not come before (rows above win ties)
+      while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        const double w = values[o * k + mid];
+        if (w > v || (w == v && o < j)) lo = mid + 1;
+        else hi = mid;
+      }
+      rank += lo;
+    }
+    if (rank < p.beams) {
+      const int64_t at = seq * p.beams + rank;
+      p.parents[at] = j;
+      p.tokens[at] = tokens[i];
+      p.out_scores[at] = static_cast<float>(v);
+      if (p.out_finished) p.out_finished[at] = p.finished[seq * p.rows + j] || tokens[i] == p.eos;
+    }
+  }
+}
+
+// Reordering.  Beam i of a sequence takes the entry of beam parents[i].  A thread owns 16 bytes of the
+// entry in every beam's slot: it reads what moves, then writes it, so that the order of beams does not
+// matter and no copy of the cache is needed.
+constexpr int kReorderCaches = 32;
+struct ReorderCache {
+  char* data;
+  int64_t slots, stride, bytes;  // bytes between slots, bytes of an entry
+  int64_t block0;                // the cache's first workgroup
+};
+struct ReorderArgs {
+  ReorderCache c[kReorderCaches];
+  const int32_t *slots, *parents;
+  int64_t batch;
+  int32_t beams, caches;
+};
+
+template <int BEAMS>
+__global__ __launch_bounds__(kBeamThreads) void reorder_kernel(const ReorderArgs p) {
+  int k = 0;
+  while (k + 1 < p.caches && static_cast<int64_t>(blockIdx.x) >= p.c[k + 1].block0) ++k;
+  const ReorderCache& c = p.c[k];
+  const int64_t at = ((static_cast<int64_t>(blockIdx.x) - c.block0) * kBeamThreads + threadIdx.x) * 16;
+  const int64_t left = c.bytes - at;
+  if (left <= 0) return;
+  for (int64_t b = blockIdx.y; b < p.batch; b += gridDim.y) {
+    const int32_t* parents = p.parents + b * p.beams;
+    auto slot_of = [&](int i) -> int64_t { return p.slots ? p.slots[b * p.beams + i] : b * p.beams + i; };
+    U32x4 v[BEAMS];
+    uint64_t moves = 0;
+#pragma unroll
+    for (int i = 0; i < BEAMS; ++i) {
+      if (i >= p.beams) continue;
+      const int from = parents[i];
+      if (from < 0 || from >= p.beams || from == i) continue;
+      const int64_t dst = slot_of(i), src = slot_of(from);
+      if (dst < 0 || dst >= c.slots || src < 0 || src >= c.slots || dst == src) continue;
+      moves |= 1ull << i;
+      const char* q = c.data + src * c.stride + at;
+      if (left >= 16) {
+        v[i] = *reinterpret_cast<const Words<1>::U4*>(q);
+      } else {
+        uint32_t w[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          if (e < left) w[e >> 2] |= static_cast<uint32_t>(static_cast<uint8_t>(q[e])) << (8 * (e & 3));
+        v[i] = U32x4{w[0], w[1], w[2], w[3]};
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < BEAMS; ++i) {
+      if (!(moves >> i & 1)) continue;
+      char* q = c.data + slot_of(i) * c.stride + at;
+      if (left >= 16) {
+        *reinterpret_cast<Words<1>::U4*>(q) = v[i];
+      } else {
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          if (e < left) q[e] = static_cast<char>(v[i][e >> 2] >> (8 * (e & 3)));
+      }
+    }
+  }
+}
+
+}  // namespace ssm

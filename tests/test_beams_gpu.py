@@ -1,0 +1,323 @@
+"""Beam search on the GPU: the selection against a 64-bit sort of every candidate, the reordering of
+caches against indexing, and a run of them together with the framework's steps."""
+import pytest
+import torch
+
+import selective_state_space_61_amd as ssm
+from gpu_util import say
+
+pytestmark = pytest.mark.gpu
+BF, F = torch.bfloat16, torch.float32
+INF = float("inf")
+
+
+@pytest.fixture(scope="module", autouse=True)
+def gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    ssm.load_library()
+
+
+def select(logits, scores, beams, finished=None, eos=-1):
+    """(parents, tokens, scores in 64 bits, finished) by the definition, on the CPU."""
+    logits, scores = logits.cpu().double(), scores.cpu().double()
+    batch, rows, vocab = logits.shape
+    out = []
+    for b in range(batch):
+        cand = []  # (value, flat index)
+        for j in range(rows):
+            l, s = logits[b, j], scores[b, j].item()
+            lse = torch.logsumexp(l, 0).item() if torch.isfinite(scores[b, j]) else 0.0
+            fin = finished is not None and bool(finished[b, j])
+            dead = not torch.isfinite(scores[b, j]) or (not fin and not torch.isfinite(torch.tensor(lse)))
+            if dead:
+                row = [(-INF, v) for v in range(min(beams, vocab))]
+            elif fin:
+                row = [(s, eos)] + [(-INF, v) for v in range(min(beams + 1, vocab)) if v != eos]
+            else:
+                top, at = torch.sort(l, descending=True, stable=True)
+                row = [(s + (x - lse), v) for x, v in zip(top[:beams].tolist(), at[:beams].tolist())]
+            cand += [(v, j * vocab + t) for v, t in row[:min(beams, vocab)]]
+        cand.sort(key=lambda c: (-c[0], c[1]))
+        out.append(cand[:beams])
+    value = torch.tensor([[v for v, _ in c] for c in out], dtype=torch.float64)
+    flat = torch.tensor([[f for _, f in c] for c in out])
+    parents, tokens = flat // vocab, flat % vocab
+    fin = None if finished is None else finished.cpu().bool().gather(1, parents) | (tokens == eos)
+    return parents, tokens, value, fin
+
+
+def check(got, ref, scores):
+    parents, tokens, value, fin = ref
+    assert torch.equal(got[0].cpu().long(), parents) and torch.equal(got[1].cpu().long(), tokens)
+    dead = value == -INF
+    assert torch.equal(got[2].cpu() == -INF, dead)
+    # A stretch's sum of exp: exponents off by 2^-23 of at most 104 (less would be 0), one unit of exp2, sums of
+    # 32 values a lane and 64 lanes: under 160 roundings of 2^-24, the log's absolute error; then one rounding
+    # of the score
+    off = (got[2].cpu().double() - value).abs()
+    assert (off[~dead] <= (160 * 2.0 ** -24 + value.abs() * 2.0 ** -23)[~dead]).all()
+    assert fin is None or torch.equal(got[3].cpu(), fin)
+
+
+def rand(shape, dtype, seed, scale=2.5):
+    g = torch.Generator().manual_seed(seed)
+    logits = (torch.randn(shape, generator=g) * scale).to(dtype).cuda()
+    return logits, (-torch.rand(shape[:2], generator=g) * 3 - 20).cuda()
+
+
+CASES = [((1, 4, 32000), 4), ((3, 1, 1000), 5), ((2, 8, 50257), 8), ((5, 3, 17), 3), ((1, 1, 1), 1), ((4, 2, 1), 2),
+         ((2, 5, 3), 7), ((1, 64, 700), 64), ((3, 16, 4099), 16), ((2, 64, 2), 64), ((1, 1, 64), 64), ((7, 33, 2049), 33),
+         ((1, 2, 300001), 6), ((70, 2, 513), 2)]
+
+
+@pytest.mark.parametrize("shape,beams,dtype", [(s, k, d) for s, k in CASES for d in (BF, F)])
+def test_selection(shape, beams, dtype):
+    say(f"[case] beams {shape} {beams} {dtype}")
+    logits, scores = rand(shape, dtype, sum(shape))
+    check(ssm.ssm_beam_select(logits, scores, beams), select(logits, scores, beams), scores)
+
+
+@pytest.mark.parametrize("dtype", [BF, F])
+@pytest.mark.parametrize("k", [1, 4, 64])
+def test_ties_go_to_the_lowest(dtype, k):
+    """Few different values: equal logits by the token, equal rows by the row, far more of them than beams."""
+    vocab = 9001
+    logits, scores = rand((2, 3, vocab), dtype, 1)
+    logits = torch.round(logits.float()).clamp(-2, 2).to(dtype)  # a tenth of a row is equal to its largest
+    logits[1] = logits[1, 1:2]
+    scores[1] = -4.0
+    check(ssm.ssm_beam_select(logits, scores, k), select(logits, scores, k), scores)
+    flat = torch.zeros((2, 2, vocab), dtype=dtype).cuda()
+    check(ssm.ssm_beam_select(flat, scores[:, :2].contiguous(), k), select(flat, scores[:, :2], k), scores)
+    signed = flat.clone()
+    signed[:, :, ::2] = -0.0  # equal to 0
+    got = ssm.ssm_beam_select(signed, scores[:, :2].contiguous(), k)
+    assert torch.equal(got[1], ssm.ssm_beam_select(flat, scores[:, :2].contiguous(), k)[1])
+
+
+@pytest.mark.parametrize("dtype", [BF, F])
+def test_rows_of_equal_values_tie_at_any_alignment(dtype):
+    """An odd vocabulary puts each row at another alignment; equal rows have equal values all the same."""
+    row = rand((1, 1, 20011), dtype, 3)[0][0, 0]
+    logits = row.expand(4, 8, -1).contiguous()
+    got = ssm.ssm_beam_select(logits, torch.zeros(4, 8).cuda(), 5)
+    # the best token of every row comes first, by the row
+    assert torch.equal(got[0].cpu(), torch.arange(5, dtype=torch.int32).expand(4, -1))
+    assert (got[1] == got[1][0, 0]).all() and (got[2] == got[2][0, 0]).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, F])
+def test_masked_and_bad_logits(dtype):
+    """-inf logits, rows that are all -inf, NaN, +inf, the type's lowest value, scores that are not finite."""
+    vocab = 5000
+    logits, scores = rand((10, 4, vocab), dtype, 7)
+    keep = torch.rand(4, vocab, generator=torch.Generator().manual_seed(1)).cuda() < 0.0008
+    logits[0] = torch.where(keep, logits[0], -INF)         # a handful of tokens left
+    logits[1, :, 3:] = -INF                                 # fewer tokens than beams
+    logits[2, 1] = -INF                                     # a row that leaves nothing
+    logits[3, 2, 4000] = float("nan")
+    logits[4, 0, 17] = INF
+    logits[5, :, 100:] = torch.finfo(dtype).min
+    scores[6, :3] = -INF                                    # the first step: one live beam
+    scores[7, 1], scores[7, 2] = float("nan"), INF
+    logits[8] = -INF                                        # nothing at all
+    logits[9] = logits[9] * 1e30 if dtype is F else logits[9] * 1e20
+    for k in (1, 6, 64):
+        check(ssm.ssm_beam_select(logits, scores, k), select(logits, scores, k), scores)
+
+
+@pytest.mark.parametrize("eos", [0, 2, 4998, 4999])
+def test_finished_beams(eos):
+    logits, scores = rand((6, 5, 5000), BF, 8)
+    finished = torch.rand(6, 5, generator=torch.Generator().manual_seed(2)) < 0.5
+    finished[0], finished[1] = True, False
+    scores[2, 1], finished[2, 1] = -INF, True
+    logits[:, 0, eos] = 30.0  # a row that ends now
+    logits[3, finished[3].cuda()] = float("nan")  # not read
+    finished = finished.cuda()
+    for k in (1, 5, 9):
+        for f in (finished, finished.to(torch.uint8)):
+            check(ssm.ssm_beam_select(logits, scores, k, finished=f, eos=eos), select(logits, scores, k, finished, eos), scores)
+
+
+def test_strided_logits():
+    """Rows of a longer tensor: the last position of each sequence, an odd offset, rows beside what is not read."""
+    whole, scores = rand((3, 4 * 5, 2003), BF, 9)
+    view = whole.view(3, 4, 5, 2003)[:, :, 4, 1:1998]
+    check(ssm.ssm_beam_select(view, scores[:, :4].contiguous(), 6), select(view, scores[:, :4], 6), scores)
+    view = whole[:, ::7, 3:900]
+    check(ssm.ssm_beam_select(view, scores[:, :3].contiguous(), 6), select(view, scores[:, :3], 6), scores)
+    with pytest.raises(ValueError, match="contiguous"):
+        ssm.ssm_beam_select(whole[:, :, ::2], scores, 4)
+
+
+def test_logits_past_32_bits():
+    logits = torch.zeros((2, 3, 2 ** 29 + 11), dtype=BF, device="cuda")  # 3.2e9 elements
+    logits[0, 2, 2 ** 29 + 10], logits[1, 0, 5], logits[1, 1, 2 ** 29] = 30.0, 31.0, 30.0
+    parents, tokens, value, _ = ssm.ssm_beam_select(logits, torch.zeros(2, 3).cuda(), 2)
+    assert parents.tolist() == [[2, 0], [0, 1]] and tokens.tolist() == [[2 ** 29 + 10, 0], [5, 2 ** 29]]
+
+
+def test_selection_in_graphs_and_on_streams():
+    a, sa = rand((4, 6, 9000), BF, 1)
+    ref = ssm.ssm_beam_select(a, sa, 6)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    state = torch.randn(24, 50).cuda()
+    start = state.clone()
+    with torch.cuda.stream(side), torch.cuda.graph(graph, stream=side):
+        out = ssm.ssm_beam_select(a, sa, 6)
+        ssm.ssm_cache_reorder(state, None, out[0])
+    want = start.view(4, 6, 50).gather(1, ref[0].long()[:, :, None].expand(-1, -1, 50)).view(24, 50)
+    b, sb = rand((2, 3, 800), F, 2)
+    for rep in range(4):
+        state.copy_(start)
+        for o in out[:3]:
+            o.fill_(9)
+        graph.replay()
+        ssm.ssm_beam_select(b, sb, 3)
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(out[:3], ref[:3])) and torch.equal(state, want), rep
+    n = ssm.ssm_beam_select_workspace(4, 6, 9000, 6, BF)
+    other = torch.cuda.Stream()
+    got = ssm.ssm_beam_select(a, sa, 6, workspace=torch.empty(n, dtype=torch.uint8, device="cuda"), stream=other)
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(got[:3], ref[:3]))
+    with pytest.raises(ssm.SsmError, match="workspace"):
+        ssm.ssm_beam_select(a, sa, 6, workspace=torch.empty(n - 16, dtype=torch.uint8, device="cuda"))
+
+
+# ---- reordering ------------------------------------------------------------------------------------------
+
+
+def reordered(cache, slots, parents):
+    out = cache.clone()
+    n, beams = cache.shape[0], parents.shape[1]
+    for b in range(parents.shape[0]):
+        for i in range(beams):
+            p = int(parents[b, i])
+            dst, src = int(slots[b, i]), int(slots[b, p]) if 0 <= p < beams else -1
+            if 0 <= dst < n and 0 <= src < n:
+                out[dst] = cache[src]
+    return out
+
+
+def same(a, b):
+    return torch.equal(a.contiguous().view(torch.uint8), b.contiguous().view(torch.uint8))
+
+
+@pytest.mark.parametrize("batch,beams", [(1, 1), (1, 2), (3, 4), (2, 5), (4, 8), (1, 16), (2, 31), (1, 64), (70000, 2)])
+def test_reordering(batch, beams):
+    g = torch.Generator().manual_seed(batch + beams)
+    n = batch * beams + 3
+    slots = torch.randperm(n, generator=g)[:batch * beams].view(batch, beams).int()
+    parents = torch.randint(0, beams, (batch, beams), generator=g).int()
+    caches = [torch.randn(n, *s, generator=g).to(d) for s, d in (((3, 5), F), ((7,), BF), ((1,), torch.int8), ((), F))]
+    if batch < 100:
+        caches += [torch.randn(n, 2, 41, 16, generator=g), torch.randint(-99, 99, (n, 4099), generator=g).to(torch.int8),
+                   torch.randn(n, 3, 100, generator=g).to(BF)[:, 1]]
+    if beams > 2:
+        parents[0, 1], parents[0, 0] = -1, beams  # out of range
+        slots[-1, 2] = -1                          # padding, and a parent that is padding
+        parents[-1, 1] = 2
+        if batch > 1:
+            slots[1, 0] = n
+    dev = [c.cuda() if c.is_contiguous() else torch.empty(n, 3, 100, dtype=BF, device="cuda")[:, 1].copy_(c) for c in caches]
+    ssm.ssm_cache_reorder(dev, slots.cuda(), parents.cuda())
+    torch.cuda.synchronize()
+    if batch < 100:
+        for got, c in zip(dev, caches):
+            assert same(got.cpu(), reordered(c, slots, parents)), c.shape
+    else:
+        source = slots.long().gather(1, parents.long()).view(-1)
+        for got, c in zip(dev, caches):
+            want = c.clone()
+            want[slots.long().view(-1)] = c[source]
+            assert same(got.cpu(), want)
+
+
+def test_reordering_many_caches_without_slots():
+    """More caches than one launch takes, NaN and infinities as they are, and beside a layer of an allocation
+    nothing."""
+    g = torch.Generator().manual_seed(4)
+    parents = torch.tensor([[1, 0, 3, 2], [0, 0, 0, 0], [3, 2, 1, 0], [2, 2, 1, 1]], dtype=torch.int32)
+    slots = torch.arange(16).view(4, 4)
+    whole = torch.randn(18, 70, 33, generator=g)
+    whole[2, 5] = float("nan")
+    whole[3, 6] = INF
+    dev = whole.cuda()
+    layers = [dev[:, k] for k in range(0, 70, 2)] + [torch.empty(0, 8).cuda()]
+    with pytest.raises(ValueError, match="slots"):
+        ssm.ssm_cache_reorder(layers, None, parents.cuda())
+    ssm.ssm_cache_reorder(layers[:-1], None, parents.cuda())
+    want = whole.clone()
+    want[:, ::2] = reordered(whole[:, ::2].contiguous(), slots, parents)
+    assert same(dev.cpu(), want)
+
+
+def test_reordering_past_32_bits():
+    """Slots past 2^32 bytes of a cache."""
+    cache = torch.zeros((5, 2 ** 30 + 64), dtype=torch.int8, device="cuda")
+    for s in range(5):
+        cache[s, :5], cache[s, -5:] = s + 1, 11 * s + 1
+    parents, slots = torch.tensor([[2, 0, 1]], dtype=torch.int32).cuda(), torch.tensor([[4, 3, 0]], dtype=torch.int32).cuda()
+    ssm.ssm_cache_reorder(cache, slots, parents)
+    assert cache[:, 0].tolist() == [4, 2, 3, 5, 1] and cache[:, -1].tolist() == [34, 12, 23, 45, 1]
+    assert int(cache[:, 5:-5].abs().max()) == 0
+
+
+def test_a_search_with_states():
+    """Prompts through packed convolution, scan and gated recurrence, then beams stepping on the caches, reordered
+    after each selection: every hypothesis' states are those of its own tokens run alone."""
+    dim, vocab, beams, steps = 48, 60, 3, 6
+    g = torch.Generator().manual_seed(12)
+    n = lambda *s: torch.randn(s, generator=g).cuda()  # noqa: E731
+    embed, head, weight, A = n(vocab, dim), n(dim, vocab) * 0.3, n(dim, 4) * 0.5, -torch.rand(dim, 16, generator=g).cuda() - 0.5
+    wb, wc, wa, wx, param = n(dim, 16) * 0.2, n(dim, 16) * 0.2, n(dim, dim) * 0.2, n(dim, dim) * 0.2, torch.full((dim,), -4.0).cuda()
+    prompts = [[5, 9, 11], [7], [3, 3, 8, 1, 20]]
+    slots = torch.randperm(12, generator=g)[:9].view(3, 3).int().cuda()
+
+    def caches():
+        return torch.zeros(12, dim, 3).cuda(), torch.zeros(12, dim, 16).cuda(), torch.zeros(12, dim).cuda()
+
+    def prompt(tokens, cs, at):
+        x = embed[torch.tensor(sum(tokens, [])).cuda()]
+        cu = torch.tensor([0] + [sum(map(len, tokens[:k + 1])) for k in range(len(tokens))], dtype=torch.int32).cuda()
+        u = ssm.ssm_causal_conv1d_packed_fwd(x, weight, cu, cache=cs[0], cache_slots=at)
+        y = ssm.ssm_scan_packed_fwd(u, u * 0.1, A, u @ wb, u @ wc, cu, delta_softplus=True, cache=cs[1], cache_slots=at)
+        y = ssm.ssm_gated_scan_packed_fwd(y, u @ wa, u @ wx, param, cu, cache=cs[2], cache_slots=at)
+        return y[cu[1:].long() - 1] @ head
+
+    def step(tokens, cs, at):
+        x = embed[tokens]
+        u = ssm.ssm_causal_conv1d_update_cache(cs[0], at, x, weight)
+        y = ssm.ssm_state_update_cache(cs[1], at, u, u * 0.1, A, u @ wb, u @ wc, delta_softplus=True)
+        return ssm.ssm_gated_update_cache(cs[2], at, y, u @ wa, u @ wx, param) @ head
+
+    cs = caches()
+    logits = prompt(prompts, cs, slots[:, 0].contiguous())
+    scores = torch.zeros(3, 1).cuda()
+    hyps = [[list(p)] for p in prompts]
+    for k in range(steps):
+        parents, tokens, scores, _ = ssm.ssm_beam_select(logits.view(3, -1, vocab), scores, beams)
+        if k == 0:
+            parents_full = parents  # every beam goes on from the prompt's slot, the first
+            assert (parents == 0).all()
+        else:
+            parents_full = parents
+        ssm.ssm_cache_reorder(list(cs), slots, parents_full)
+        hyps = [[hyps[b][p] + [t] for p, t in zip(parents[b].tolist(), tokens[b].tolist())] for b in range(3)]
+        logits = step(tokens.view(-1).long(), cs, slots.view(-1))
+    assert len({tuple(h) for b in hyps for h in b}) == 9
+    for b in range(3):
+        for i in range(beams):
+            alone = caches()
+            one = torch.tensor([0], dtype=torch.int32).cuda()
+            prompt([hyps[b][i]], alone, one)
+            for c, d in zip(cs, alone):
+                # fp32 steps of the same tokens, in one call or one by one: the states differ by roundings of a
+                # dozen steps whose maps do not grow (decays below 1), a few hundred of 2^-24 relative to the largest
+                top = d[0].abs().max()
+                assert (c[slots[b, i].long()] - d[0]).abs().max() <= 1024 * 2.0 ** -24 * top, (b, i)
