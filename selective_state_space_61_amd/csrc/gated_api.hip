@@ -18,22 +18,24 @@ struct Tiled {
   int64_t rows;
 };
 template <bool BF16, int V, int R>
-Tiled forward_of() {
-  return {ssm::gated_scan_kernel<BF16, V, R>, ssm::GatedShape<V, R>::kRows};
+Tiled forward_of(bool z) {
+  return {z ? ssm::gated_scan_kernel<BF16, true, V, R> : ssm::gated_scan_kernel<BF16, false, V, R>,
+          ssm::GatedShape<V, R>::kRows};
 }
 template <bool BF16, int V, int R>
-Tiled backward_of() {
-  return {ssm::gated_scan_bwd_kernel<BF16, V, R>, ssm::GatedShape<V, R>::kRows};
+Tiled backward_of(bool z) {
+  return {z ? ssm::gated_scan_bwd_kernel<BF16, true, V, R> : ssm::gated_scan_bwd_kernel<BF16, false, V, R>,
+          ssm::GatedShape<V, R>::kRows};
 }
 
 // The forward's shape: 8 bytes of a bf16 row or of an fp32 row a lane.  Single channels where dim has fewer.
-Tiled forward_kernel(bool bf16, int64_t dim) {
-  if (dim < 4) return bf16 ? forward_of<true, 1, 8>() : forward_of<false, 1, 8>();
-  return bf16 ? forward_of<true, 4, 8>() : forward_of<false, 2, 8>();
+Tiled forward_kernel(bool bf16, int64_t dim, bool z) {
+  if (dim < 4) return bf16 ? forward_of<true, 1, 8>(z) : forward_of<false, 1, 8>(z);
+  return bf16 ? forward_of<true, 4, 8>(z) : forward_of<false, 2, 8>(z);
 }
-Tiled backward_kernel(bool bf16, int64_t dim) {
-  if (dim < 2) return bf16 ? backward_of<true, 1, 16>() : backward_of<false, 1, 16>();
-  return bf16 ? backward_of<true, 2, 8>() : backward_of<false, 2, 8>();
+Tiled backward_kernel(bool bf16, int64_t dim, bool z) {
+  if (dim < 2) return bf16 ? backward_of<true, 1, 16>(z) : backward_of<false, 1, 16>(z);
+  return bf16 ? backward_of<true, 2, 8>(z) : backward_of<false, 2, 8>(z);
 }
 
 constexpr int64_t kTicketBytes = 16;
@@ -50,8 +52,13 @@ ssm_status_t tiles_of(const Tiled& t, int64_t rows, int64_t dim, int64_t* tiles,
   return SSM_OK;
 }
 
+// a tile's rows are reached by 32-bit byte offsets
+constexpr int64_t kMaxRowStride = int64_t{1} << 23;
+static_assert(128 * kMaxRowStride * 4 <= int64_t{1} << 32, "128 rows of fp32");
+
 ssm_status_t check_sizes(int64_t rows, int64_t dim, ssm_dtype_t dtype) {
   if (dim < 0) return fail(SSM_ERR_INVALID_ARG, "negative size (dim=%lld)", (long long)dim);
+  if (dim >= kMaxRowStride) return fail(SSM_ERR_UNSUPPORTED, "dim %lld is not below 2^23", (long long)dim);
   if (rows > kMaxIndex) return fail(SSM_ERR_UNSUPPORTED, "more than 2^31-1 rows");
   if (dtype != SSM_F32 && dtype != SSM_BF16) return fail(SSM_ERR_UNSUPPORTED, "unknown dtype %d", (int)dtype);
   return SSM_OK;
@@ -61,7 +68,7 @@ ssm_status_t workspace_of(int64_t rows, int64_t dim, bool bf16, bool backward, i
   int64_t tiles;
   *bytes = 0;
   if (rows == 0 || dim == 0) return SSM_OK;
-  SSM_TRY(tiles_of(backward ? backward_kernel(bf16, dim) : forward_kernel(bf16, dim), rows, dim, &tiles, bytes));
+  SSM_TRY(tiles_of(backward ? backward_kernel(bf16, dim, true) : forward_kernel(bf16, dim, true), rows, dim, &tiles, bytes));
   if (backward) {
     int64_t n;
     if (!mul_ok(tiles, dim, &n) || !mul_ok(n, 12, &n) || __builtin_add_overflow(*bytes, n, bytes))
@@ -172,7 +179,7 @@ ssm_status_t ssm_gated_scan_fwd(int64_t batch, int64_t seqlen, int64_t dim, ssm_
   }
   if (!x || !a_gate || !x_gate || !a_param || !y)
     return fail(SSM_ERR_INVALID_ARG, "NULL required pointer (x, a_gate, x_gate, a_param and y)");
-  const Tiled t = forward_kernel(dtype == SSM_BF16, dim);
+  const Tiled t = forward_kernel(dtype == SSM_BF16, dim, z != nullptr);
   int64_t tiles, published;
   SSM_TRY(tiles_of(t, n.rows, dim, &tiles, &published));
   SSM_TRY(check_workspace(workspace, workspace_bytes, published));
@@ -213,7 +220,7 @@ ssm_status_t ssm_gated_scan_bwd(int64_t batch, int64_t seqlen, int64_t dim, ssm_
   if (n.elems > 0 && (!x || !a_gate || !x_gate || !dy || !dx || !da_gate || !dx_gate))
     return fail(SSM_ERR_INVALID_ARG, "NULL required pointer (x, a_gate, x_gate, dy, dx, da_gate and dx_gate)");
   if (n.elems > 0 && z && !dz) return fail(SSM_ERR_INVALID_ARG, "z needs dz");
-  const Tiled t = backward_kernel(dtype == SSM_BF16, dim);
+  const Tiled t = backward_kernel(dtype == SSM_BF16, dim, z != nullptr);
   int64_t tiles, published, need;
   SSM_TRY(tiles_of(t, n.rows, dim, &tiles, &published));
   SSM_TRY(workspace_of(n.rows, dim, dtype == SSM_BF16, true, &need));
@@ -269,12 +276,15 @@ ssm_status_t ssm_gated_scan_packed_fwd(const ssm_packed_t* seqs, int64_t dim, ss
   Rows t[] = {{x, dim, &rs.x, "x", 0}, {a_gate, dim, &rs.a_gate, "a_gate", 0}, {x_gate, dim, &rs.x_gate, "x_gate", 0},
               {z, dim, &rs.z, "z", 0}, {y, dim, &rs.y, "y", 0}};
   SSM_TRY(check_rows(t, 5, seqs->total, es));
+  for (const Rows& r : t)
+    if (*r.stride >= kMaxRowStride)
+      return fail(SSM_ERR_UNSUPPORTED, "row stride %lld of %s is not below 2^23", (long long)*r.stride, r.name);
   if (seqs->total == 0 || seqs->sequences == 0 || dim == 0) return SSM_OK;
   if (!x || !a_gate || !x_gate || !a_param || !y)
     return fail(SSM_ERR_INVALID_ARG, "NULL required pointer (x, a_gate, x_gate, a_param and y)");
   Range idx[3];
   SSM_TRY(check_packed_pointers(seqs, idx));
-  const Tiled k = forward_kernel(dtype == SSM_BF16, dim);
+  const Tiled k = forward_kernel(dtype == SSM_BF16, dim, z != nullptr);
   int64_t tiles, published;
   SSM_TRY(tiles_of(k, seqs->total, dim, &tiles, &published));
   SSM_TRY(check_workspace(workspace, workspace_bytes, published));

@@ -28,7 +28,7 @@ namespace ssm {
 constexpr int kGatedThreads = 256;
 constexpr int kGatedChannels = 64;   // channels of a workgroup: one 128-byte line of a bf16 row
 constexpr uint32_t kEmpty = 0xffffffffu;
-constexpr int kGatedWindow = 8;      // tiles that one look back covers
+constexpr int kGatedWindow = 2;      // tiles that one look back covers
 constexpr int kGatedSave = 64;       // rows between checkpoints
 
 struct GatedArgs {
@@ -126,45 +126,95 @@ template <int ROWS>
 struct TileRows {
   int32_t seq[ROWS];
   uint64_t first[(ROWS + 63) / 64], last[(ROWS + 63) / 64], live[(ROWS + 63) / 64];
+  // all of one sequence, neither its first nor its last
+  __device__ __forceinline__ bool inside() const {
+    uint64_t other = 0;
+#pragma unroll
+    for (int i = 0; i < (ROWS + 63) / 64; ++i)
+      other |= first[i] | last[i] | (live[i] ^ (ROWS < 64 ? (1ull << (ROWS & 63)) - 1 : ~0ull));
+    return __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(other) | static_cast<uint32_t>(other >> 32)) == 0;
+  }
 };
 
+// The last sequence whose first row is not above `row`, as an index into cu (-1: none).  By one lane.
+__device__ inline int64_t last_not_above(const int32_t* cu, int64_t nseq, int64_t row) {
+  int64_t lo = -1, hi = nseq + 1;
+  while (hi - lo > 1) {
+    const int64_t mid = (lo + hi) >> 1;
+    if (cu[mid] <= row) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
+// By the first threads, a row each.  Packed rows: a wave reads 64 entries of cu, from the last one that is
+// not above its first row on (64 probes at a time: one round trip up to 63 sequences, two up to 4095), and
+// its lanes search them in its registers.
 template <int ROWS>
-__device__ __forceinline__ void find_rows(TileRows<ROWS>& t, const GatedArgs& p, int64_t row0) {
-  for (int at = threadIdx.x; at < ROWS; at += kGatedThreads) {
-    const int64_t row = row0 + at;
-    bool first = false, last = false, live = row < p.total;
-    int64_t s = -1;
+__device__ __forceinline__ void find_rows(TileRows<ROWS>& t, const GatedArgs& p, uint32_t row0) {
+  const uint32_t at = threadIdx.x;
+  if (at >= (ROWS < 64 ? 64 : ROWS)) return;  // whole waves
+  const int32_t row = static_cast<int32_t>(row0 + at);  // (total is at most 2^31 - 1; rows behind it are not live)
+  bool first = false, last = false, live = at < ROWS && row0 + at < p.total;
+  int32_t s = -1;
+  if (!p.cu) {
     if (live) {
-      if (!p.cu) {
-        s = static_cast<uint32_t>(row) / static_cast<uint32_t>(p.seqlen);
-        const int64_t in = row - s * p.seqlen;
-        first = in == 0;
-        last = in == p.seqlen - 1;
-      } else {
-        // the last entry not above the row
-        int64_t lo = -1, hi = p.nseq + 1;
-        while (hi - lo > 1) {
-          const int64_t mid = (lo + hi) >> 1;
-          if (p.cu[mid] <= row) lo = mid;
-          else hi = mid;
-        }
-        live = lo >= 0 && lo < p.nseq;
-        if (live) {
-          s = lo;
-          first = p.cu[s] == row;
-          last = p.cu[s + 1] == row + 1;
-        }
-      }
+      const uint32_t len = static_cast<uint32_t>(p.seqlen), n = (row0 + at) / len, in = row0 + at - n * len;
+      s = static_cast<int32_t>(n);
+      first = in == 0;
+      last = in == len - 1;
     }
-    t.seq[at] = static_cast<int32_t>(s);
-    const uint64_t f = __ballot(first), l = __ballot(last), v = __ballot(live);
-    if ((threadIdx.x & 63) == 0) {
-      t.first[at >> 6] = f;
-      t.last[at >> 6] = l;
-      t.live[at >> 6] = v;
+  } else {
+    const int lane = threadIdx.x & 63;
+    const int64_t from = static_cast<int64_t>(row0) + (at - lane);  // the wave's first row
+    int64_t s0 = 0;
+    for (int64_t left = p.nseq + 1; left > 64;) {
+      const int64_t step = (left + 63) / 64, i = lane * step;
+      const int c = __popcll(__ballot(i < left && p.cu[s0 + (i < left ? i : 0)] <= from));
+      const int64_t skip = c > 0 ? (c - 1) * step : 0;
+      s0 += skip;
+      left = left - skip < step ? left - skip : step;
+    }
+    const int32_t entry = s0 + lane <= p.nseq ? p.cu[s0 + lane] : INT32_MAX;
+    int c = 0;  // entries not above the row
+#pragma unroll
+    for (int k = 32; k; k >>= 1) c += __shfl(entry, c + k - 1) <= row ? k : 0;
+    c += __shfl(entry, c < 64 ? c : 63) <= row && c < 64 ? 1 : 0;
+    int32_t begin = __shfl(entry, c > 0 ? c - 1 : 0), end = __shfl(entry, c < 64 ? c : 63);
+    int64_t n = s0 + c - 1;
+    if (live && c == 64) {  // more sequences than that begin here
+      n = last_not_above(p.cu, p.nseq, row);
+      begin = n >= 0 ? p.cu[n] : 0;
+      end = n >= 0 && n < p.nseq ? p.cu[n + 1] : 0;
+    }
+    live = live && c > 0 && n >= 0 && n < p.nseq;
+    if (live) {
+      s = static_cast<int32_t>(n);
+      first = begin == row;
+      last = end == row + 1;
     }
   }
+  if (at < ROWS) t.seq[at] = s;
+  const uint64_t f = __ballot(first), l = __ballot(last), v = __ballot(live);
+  if ((at & 63) == 0) {
+    t.first[at >> 6] = f;
+    t.last[at >> 6] = l;
+    t.live[at >> 6] = v;
+  }
 }
+
+// A part's rows of a tile as bits
+template <int R>
+struct PartRows {
+  uint32_t first, last, live;
+  template <int ROWS>
+  __device__ __forceinline__ PartRows(const TileRows<ROWS>& t, int at) {
+    constexpr uint32_t kAll = (1u << R) - 1u;
+    first = static_cast<uint32_t>(t.first[at >> 6] >> (at & 63)) & kAll;
+    last = static_cast<uint32_t>(t.last[at >> 6] >> (at & 63)) & kAll;
+    live = static_cast<uint32_t>(t.live[at >> 6] >> (at & 63)) & kAll;
+  }
+};
 
 // V consecutive channels of a state: of sequence s's slot, zeros where it has none.  Fills h and says
 // whether there is one to read.
@@ -183,19 +233,20 @@ __device__ __forceinline__ void initial_state(const GatedArgs& p, int64_t s, int
 }
 
 template <int V>
-__device__ __forceinline__ void final_state(const GatedArgs& p, int64_t s, int64_t d, int own, const float (&h)[V]) {
+__device__ __forceinline__ void final_state(const GatedArgs& p, int64_t s, int64_t d, const float (&h)[V]) {
   if (!p.out.data) return;
   const int64_t at = cache_offset(p.out, p.slots, s);
   if (at < 0) return;
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    if (v < own) continue;
     if (p.cb16) static_cast<uint16_t*>(p.out.data)[at + d + v] = to_bf16(h[v]);
     else static_cast<float*>(p.out.data)[at + d + v] = h[v];
   }
 }
 
-__device__ __forceinline__ float sigmoid_f32(float v) { return hw_rcp(1.0f + hw_exp2(-v * kLog2e)); }
+// sigmoid(v + bias) with c = -bias log2(e): one fused multiply-add, exp2, sum, reciprocal
+__device__ __forceinline__ float sigmoid_f32(float v, float c) { return hw_rcp(1.0f + hw_exp2(fmaf(v, -kLog2e, c))); }
+__device__ __forceinline__ float sigmoid_f32(float v) { return hw_rcp(1.0f + hw_exp2(v * -kLog2e)); }
 
 // w = sqrt(1 - a^2) with a = e^l.  1 - a^2 = -expm1(2 l): from p = -2 l = 0.35 on the difference itself (its
 // rounding errors are below 2^-24 / 0.29 of it), below it p times the series of (1 - e^-p) / p up to p^6,
@@ -212,50 +263,75 @@ __device__ __forceinline__ float input_weight(float l, float a) {
   return __builtin_amdgcn_sqrtf(p < 0.35f ? s * p : fmaf(-a, a, 1.0f));
 }
 
-// The channels of a lane: V neighbouring ones.  Where dim is no multiple of V the last lane's begin
-// further left, so that every load is a whole vector; what it shares with its neighbour it computes
-// but does not store (channels below d + own are another lane's).
+// The channels of a workgroup, a block of up to kGatedChannels, and of its lanes, V neighbouring ones each.
+// Where the last lane's would pass dim they begin further left, so that every access is a whole vector: what
+// it shares with its neighbour both compute and store alike.  A last block of fewer than V channels takes V
+// more from the block before it, so that no two workgroups share a channel (a cached state is read and
+// written by one alone).
 template <int V>
-struct LaneChannels {
-  int64_t d;
-  int own;
-  __device__ __forceinline__ LaneChannels(int64_t natural, int64_t dim) {
-    d = natural < dim - V ? natural : dim - V;
-    own = natural - d < V ? static_cast<int>(natural - d) : V;
+struct Channels {
+  int64_t first, dim;
+  int32_t count;
+  __device__ __forceinline__ Channels(uint32_t block, int64_t width) : first(int64_t{block} * kGatedChannels), dim(width) {
+    const int64_t left = dim - first, next = left - kGatedChannels;
+    count = static_cast<int32_t>(left < kGatedChannels ? left : kGatedChannels);
+    if (block > 0 && left < V) {
+      first -= V;
+      count += V;
+    } else if (next > 0 && next < V) {
+      count -= V;
+    }
   }
+  // the first channel of lane l, and whether it has any
+  __device__ __forceinline__ int64_t of(int l) const {
+    const int64_t d = first + l * V;
+    return d < dim - V ? d : dim - V;
+  }
+  __device__ __forceinline__ bool has(int l) const { return l * V < count; }
 };
 
-template <bool BF16, int V>
-__device__ __forceinline__ void store_own(void* base, int64_t idx, int own, const float (&val)[V]) {
-  Run<BF16, V> r;
-  r.set(val);
-  if (own == 0) {
-    r.store(base, idx);
-  } else {
+// l = k r of a channel: k = -a_scale softplus(a_param), by the library's exp and log1p (once a workgroup and
+// channel, not once a lane).  Finite, so that l a is 0 and not NaN where a is 0.
+__device__ __forceinline__ float decay_rate(float scale, float q) {
+  return -fminf(scale * (fmaxf(q, 0.0f) + log1pf(expf(-fabsf(q)))), 1e30f);
+}
+
+// -bias log2(e) of a lane's channels (sigmoid_f32)
+template <int V>
+__device__ __forceinline__ void load_bias(const float* bias, int64_t d, float (&c)[V]) {
+  Run<false, V> r;
+  if (bias) r.load(bias, d);
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      if (v < own) continue;
-      if constexpr (BF16) static_cast<uint16_t*>(base)[idx + v] = static_cast<uint16_t>(r.w[v >> 1] >> (16 * (v & 1)));
-      else static_cast<uint32_t*>(base)[idx + v] = r.w[v];
+  for (int v = 0; v < V; ++v) c[v] = bias ? r.get(v) * -kLog2e : 0.0f;
+}
+
+// A lane's rows of a tensor, `stride` elements apart (not FULL: past the last row that row again).  The
+// addresses are a base that the workgroup shares and a lane's 32-bit offset (row strides are below 2^23).
+template <bool FULL, bool BF16, int V, int R>
+__device__ __forceinline__ void load_rows(Run<BF16, V> (&out)[R], const void* base, int64_t stride, int64_t tile0,
+                                          int at, int64_t d, int64_t total) {
+  constexpr int ES = BF16 ? 2 : 4;
+  const char* q = static_cast<const char*>(base) + tile0 * stride * ES;
+  if constexpr (FULL) {
+    const uint32_t off = (static_cast<uint32_t>(at) * static_cast<uint32_t>(stride) + static_cast<uint32_t>(d)) * ES;
+#pragma unroll
+    for (int j = 0; j < R; ++j) out[j].load_bytes(q + j * stride * ES + off);
+  } else {
+    const uint32_t left = static_cast<uint32_t>(total - tile0) - 1u;
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+      const uint32_t row = static_cast<uint32_t>(at + j) < left ? static_cast<uint32_t>(at + j) : left;
+      out[j].load_bytes(q + (row * static_cast<uint32_t>(stride) + static_cast<uint32_t>(d)) * ES);
     }
   }
 }
 
-// Parameters of a lane's channels: biases, and l = k r
-template <int V>
-struct LaneParams {
-  float ab[V], xb[V], k[V];
-  __device__ __forceinline__ LaneParams(const GatedArgs& p, int64_t d) {
+// A row of no sequence leaves a state as it is: a decay of 1 (an a_gate of -inf) and no input
+template <bool BF16, int V>
+__device__ __forceinline__ void no_row(Run<BF16, V>& r, bool off, bool closed) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      ab[v] = p.ab ? p.ab[d + v] : 0.0f;
-      xb[v] = p.xb ? p.xb[d + v] : 0.0f;
-      const float q = p.param[d + v];
-      // finite, so that l a is 0 and not NaN where a is 0
-      k[v] = -fminf(p.scale * (fmaxf(q, 0.0f) + log1pf(expf(-fabsf(q)))), 1e30f);
-    }
-  }
-};
+  for (int i = 0; i < Run<BF16, V>::kWords; ++i) r.w[i] = off ? (closed ? (BF16 ? 0xff80ff80u : 0xff800000u) : 0u) : r.w[i];
+}
 
 // The maps of a channel's lanes in the LDS, then what enters each of them.
 template <int PARTS>
@@ -266,139 +342,170 @@ struct PartMaps {
 };
 
 // A tile's number, in the order in which tiles are taken
-__device__ __forceinline__ int64_t take_ticket(const GatedArgs& p, uint32_t* shared) {
+__device__ __forceinline__ uint32_t take_ticket(const GatedArgs& p, uint32_t* shared) {
   if (!p.ticket) return blockIdx.x;
   if (threadIdx.x == 0)
     *shared = __hip_atomic_fetch_add(p.ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) + 1u;  // (cleared to ~0)
   __syncthreads();
-  return *shared;
+  return __builtin_amdgcn_readfirstlane(*shared);
 }
 
-template <bool BF16, int V, int R>
+template <bool BF16, bool Z, int V, int R>
 __global__ __launch_bounds__(kGatedThreads) void gated_scan_kernel(const GatedArgs p) {
   using S = GatedShape<V, R>;
   __shared__ TileRows<S::kRows> rows;
   __shared__ PartMaps<S::kParts> maps;
-  __shared__ float entering[kGatedChannels];
+  __shared__ float entering[kGatedChannels], rate[kGatedChannels];
   __shared__ uint32_t ticket;
-  const int64_t n = take_ticket(p, &ticket);
-  const int64_t tile = n / p.chains;
-  const int64_t c0 = (n - tile * p.chains) * kGatedChannels;
-  const int lane = threadIdx.x % S::kLanes, part = threadIdx.x / S::kLanes;
-  const int64_t row0 = tile * S::kRows + part * R;
-  const LaneChannels<V> ch(c0 + lane * V, p.dim);
+  const uint32_t n = take_ticket(p, &ticket);
+  const uint32_t tile = n / static_cast<uint32_t>(p.chains);
+  const Channels<V> ch(n - tile * static_cast<uint32_t>(p.chains), p.dim);
+  const int lane = threadIdx.x % S::kLanes, part = threadIdx.x / S::kLanes, at0 = part * R;
+  const int64_t tile0 = static_cast<int64_t>(tile) * S::kRows, d = ch.of(lane);
 
-  Run<BF16, V> x[R], ag[R], xg[R], z[R];
-  const bool has_z = p.z != nullptr;
-  const void* zsrc = has_z ? p.z : p.x;
-  const int64_t zstride = has_z ? p.sz : p.sx;
-#pragma unroll
-  for (int j = 0; j < R; ++j) {
-    const int64_t row = row0 + j < p.total ? row0 + j : p.total - 1;
-    x[j].load(p.x, row * p.sx + ch.d);
-    ag[j].load(p.ag, row * p.sag + ch.d);
-    xg[j].load(p.xg, row * p.sxg + ch.d);
-    z[j].load(zsrc, row * zstride + ch.d);
-  }
-  const LaneParams<V> par(p, ch.d);
-  find_rows(rows, p, tile * S::kRows);
-  __syncthreads();
-  const int at0 = part * R;
-  const uint32_t bits = (1u << R) - 1u;
-  const uint32_t first = static_cast<uint32_t>(rows.first[at0 >> 6] >> (at0 & 63)) & bits;
-  const uint32_t last = static_cast<uint32_t>(rows.last[at0 >> 6] >> (at0 & 63)) & bits;
-  const uint32_t live = static_cast<uint32_t>(rows.live[at0 >> 6] >> (at0 & 63)) & bits;
-
-  float a[R][V], b[R][V], A[V], B[V];
-#pragma unroll
-  for (int v = 0; v < V; ++v) A[v] = 1.0f, B[v] = 0.0f;
-#pragma unroll
-  for (int j = 0; j < R; ++j) {
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const float l = par.k[v] * sigmoid_f32(ag[j].get(v) + par.ab[v]);
-      const float i = sigmoid_f32(xg[j].get(v) + par.xb[v]);
-      const float e = hw_exp2(l * kLog2e);
-      const bool on = live >> j & 1;
-      a[j][v] = on ? e : 1.0f;
-      b[j][v] = on ? input_weight(l, e) * (i * x[j].get(v)) : 0.0f;
-    }
-    if (first >> j & 1) {
-      float h[V];
-      initial_state<V>(p, rows.seq[at0 + j], ch.d, h);
-#pragma unroll
-      for (int v = 0; v < V; ++v) b[j][v] = fmaf(a[j][v], h[v], b[j][v]);
-    }
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      A[v] *= a[j][v];
-      B[v] = first >> j & 1 ? b[j][v] : fmaf(a[j][v], B[v], b[j][v]);
-    }
-  }
-#pragma unroll
-  for (int v = 0; v < V; ++v) {
-    maps.a[part][lane * V + v] = A[v];
-    maps.b[part][lane * V + v] = B[v];
-  }
-  if (lane == 0) maps.own[part] = first != 0;
+  const float param = p.param[ch.of(threadIdx.x % kGatedChannels / V) + threadIdx.x % V];
+  find_rows(rows, p, static_cast<uint32_t>(tile0));
   __syncthreads();
 
-  if (threadIdx.x < kGatedChannels) {
-    const int c = threadIdx.x, l = c / V, v = c - l * V;
-    const LaneChannels<V> my(c0 + l * V, p.dim);
-    const bool on = v >= my.own;
-    const int64_t d = my.d + v;
-    // what comes before each part, as a map of what enters the tile
-    float ta = 1.0f, tb = 0.0f;
-    bool own = false;
+  auto body = [&](auto edges) {
+    constexpr bool EDGES = decltype(edges)::value;
+    // (each variant loads for itself: rows loaded before the branch would stay in registers beside the other's)
+    Run<BF16, V> x[R], ag[R], xg[R], z[R];
+    load_rows<!EDGES>(ag, p.ag, p.sag, tile0, at0, d, p.total);
+    load_rows<!EDGES>(xg, p.xg, p.sxg, tile0, at0, d, p.total);
+    load_rows<!EDGES>(x, p.x, p.sx, tile0, at0, d, p.total);
+    if constexpr (Z) load_rows<!EDGES>(z, p.z, p.sz, tile0, at0, d, p.total);
+    float ab[V], xb[V];
+    load_bias<V>(p.ab, d, ab);
+    load_bias<V>(p.xb, d, xb);
+    if (threadIdx.x < kGatedChannels) rate[threadIdx.x] = decay_rate(p.scale, param);
+    __syncthreads();
+    const PartRows<R> in(rows, at0);
+    if constexpr (EDGES) {
 #pragma unroll
-    for (int k = 0; k < S::kParts; ++k) {
-      const float pa = maps.a[k][c], pb = maps.b[k][c];
-      maps.a[k][c] = own ? 0.0f : ta;
-      maps.b[k][c] = tb;
-      if (maps.own[k]) {
-        own = true;
-        tb = pb;
-      } else {
-        ta *= pa;
-        tb = fmaf(pa, tb, pb);
+      for (int j = 0; j < R; ++j) {
+        const bool off = !(in.live >> j & 1);
+        no_row<BF16, V>(ag[j], off, true);
+        no_row<BF16, V>(xg[j], off, false);
+        no_row<BF16, V>(x[j], off, false);
       }
     }
-    float h = 0.0f;
-    if (p.ticket) {
-      const int64_t at = tile * p.dim + d;
-      if (on && !own) publish(p.maps + at, ta, tb);
-      if (on && own) publish(p.ends + at, tb);
-      h = look_back(p.maps + at - p.dim, p.ends + at - p.dim, -p.dim, tile, on && !(rows.first[0] & 1));
-      if (on && !own) publish(p.ends + at, fmaf(ta, h, tb));
+    float a[R][V], b[R][V], A[V], B[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) A[v] = 1.0f, B[v] = 0.0f;
+#pragma unroll
+    for (int j = 0; j < R; ++j)
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const float l = rate[lane * V + v] * sigmoid_f32(ag[j].get(v), ab[v]);
+        a[j][v] = hw_exp2(l * kLog2e);
+        b[j][v] = input_weight(l, a[j][v]) * (sigmoid_f32(xg[j].get(v), xb[v]) * x[j].get(v));
+      }
+    if constexpr (EDGES) {
+      for (uint32_t bits = in.first; bits; bits &= bits - 1) {
+        const int at = __builtin_ctz(bits);
+        float h[V];
+        initial_state<V>(p, rows.seq[at0 + at], d, h);
+#pragma unroll
+        for (int j = 0; j < R; ++j)
+#pragma unroll
+          for (int v = 0; v < V; ++v) b[j][v] = j == at ? fmaf(a[j][v], h[v], b[j][v]) : b[j][v];
+      }
     }
-    entering[c] = h;
-  }
-  __syncthreads();
-
-  float h[V];
-  bool before = false;  // a part before this one has a state of its own
 #pragma unroll
-  for (int k = 0; k < S::kParts; ++k) before |= k < part && maps.own[k];
+    for (int j = 0; j < R; ++j)
 #pragma unroll
-  for (int v = 0; v < V; ++v) {
-    const int c = lane * V + v;
-    h[v] = before ? maps.b[part][c] : fmaf(maps.a[part][c], entering[c], maps.b[part][c]);
-  }
-#pragma unroll
-  for (int j = 0; j < R; ++j) {
-    float o[V];
+      for (int v = 0; v < V; ++v) {
+        A[v] *= a[j][v];
+        B[v] = EDGES && (in.first >> j & 1) ? b[j][v] : fmaf(a[j][v], B[v], b[j][v]);
+      }
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      h[v] = first >> j & 1 ? b[j][v] : fmaf(a[j][v], h[v], b[j][v]);
-      o[v] = has_z ? h[v] * silu_f32(z[j].get(v)) : h[v];
+      maps.a[part][lane * V + v] = A[v];
+      maps.b[part][lane * V + v] = B[v];
     }
-    if (live >> j & 1) store_own<BF16, V>(p.y, (row0 + j) * p.sy + ch.d, ch.own, o);
-    if (last >> j & 1) final_state<V>(p, rows.seq[at0 + j], ch.d, ch.own, h);
-  }
-  static_assert(kGatedSave % R == 0, "a checkpoint is the state after a part");
-  if (p.ckpt && (row0 + R) % kGatedSave == 0 && row0 + R <= p.total)
-    store_own<false, V>(p.ckpt, (row0 / kGatedSave) * p.dim + ch.d, ch.own, h);
+    if (EDGES && lane == 0) maps.own[part] = in.first != 0;
+    __syncthreads();
+
+    if (threadIdx.x < kGatedChannels) {
+      const int c = threadIdx.x;
+      const bool on = ch.has(c / V);
+      // what comes before each part, as a map of what enters the tile
+      float ta = 1.0f, tb = 0.0f;
+      bool own = false;
+#pragma unroll
+      for (int i = 0; i < S::kParts; ++i) {
+        const float pa = maps.a[i][c], pb = maps.b[i][c];
+        maps.a[i][c] = ta;
+        maps.b[i][c] = tb;
+        const bool starts = EDGES && maps.own[i];
+        own |= starts;
+        ta *= pa;
+        tb = starts ? pb : fmaf(pa, tb, pb);
+      }
+      float h = 0.0f;
+      if (p.ticket) {
+        const int64_t at = tile * p.dim + ch.of(c / V) + c % V;
+        if (on && !own) publish(p.maps + at, ta, tb);
+        if (on && own) publish(p.ends + at, tb);
+        h = look_back(p.maps + at - p.dim, p.ends + at - p.dim, -p.dim, tile, on && !(EDGES && (rows.first[0] & 1)));
+        if (on && !own) publish(p.ends + at, fmaf(ta, h, tb));
+      }
+      entering[c] = h;
+    }
+    __syncthreads();
+
+    float h[V];
+    bool before = false;  // a part before this one has a state of its own
+    if constexpr (EDGES) {
+#pragma unroll
+      for (int i = 0; i < S::kParts; ++i) before |= i < part && maps.own[i];
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int c = lane * V + v;
+      h[v] = before ? maps.b[part][c] : fmaf(maps.a[part][c], entering[c], maps.b[part][c]);
+    }
+    if (!EDGES || ch.has(lane)) {
+      constexpr int ES = BF16 ? 2 : 4;
+      char* y = static_cast<char*>(p.y) + tile0 * p.sy * ES;
+      const uint32_t off = (static_cast<uint32_t>(at0) * static_cast<uint32_t>(p.sy) + static_cast<uint32_t>(d)) * ES;
+#pragma unroll
+      for (int j = 0; j < R; ++j) {
+        float o[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          h[v] = EDGES && (in.first >> j & 1) ? b[j][v] : fmaf(a[j][v], h[v], b[j][v]);
+          if constexpr (EDGES) b[j][v] = h[v];
+          if constexpr (Z) o[v] = h[v] * silu_f32(z[j].get(v));
+          else o[v] = h[v];
+        }
+        Run<BF16, V> out;
+        out.set(o);
+        if (!EDGES || (in.live >> j & 1)) out.store_bytes(y + j * p.sy * ES + off);
+      }
+      if constexpr (EDGES) {
+        for (uint32_t bits = in.last; bits; bits &= bits - 1) {
+          const int at = __builtin_ctz(bits);
+          float e[V];
+#pragma unroll
+          for (int j = 0; j < R; ++j)
+#pragma unroll
+            for (int v = 0; v < V; ++v) e[v] = j == at || j == 0 ? b[j][v] : e[v];
+          final_state<V>(p, rows.seq[at0 + at], d, e);
+        }
+      }
+      static_assert(kGatedSave % R == 0, "a checkpoint is the state after a part");
+      if (p.ckpt && (at0 + R + tile0) % kGatedSave == 0 && tile0 + at0 + R <= p.total) {
+        Run<false, V> out;
+        out.set(h);
+        out.store(p.ckpt, (tile0 + at0) / kGatedSave * p.dim + d);
+      }
+    }
+  };
+  // most tiles lie inside a sequence: without the cases of the others they take half the instructions
+  if (rows.inside() && ch.count == kGatedChannels) body(std::false_type{});
+  else body(std::true_type{});
 }
 
 // Backward.  With g = dy silu(z) (+ dlast at a sequence's last row), from the last row on:
@@ -407,191 +514,255 @@ __global__ __launch_bounds__(kGatedThreads) void gated_scan_kernel(const GatedAr
 // q is 0 where w is (a = 1): l / w -> 0 as l -> 0, so the product has that limit though dw/dl has none.
 // The states come from the checkpoint before the tile and the tile's own rows; a G is carried from tile
 // to tile like the forward's state, tiles taken from the last one on.
-template <bool BF16, int V, int R>
+// V channels of sequence s in a (batch, dim) tensor of states, zeros without one
+template <int V>
+__device__ __forceinline__ Run<false, V> batch_state(const void* states, int32_t s, int64_t dim, int64_t d) {
+  Run<false, V> h;
+#pragma unroll
+  for (int v = 0; v < V; ++v) h.w[v] = 0u;
+  if (states) h.load(states, s * dim + d);
+  return h;
+}
+
+template <bool BF16, bool Z, int V, int R>
 __global__ __launch_bounds__(kGatedThreads) void gated_scan_bwd_kernel(const GatedArgs p) {
   using S = GatedShape<V, R>;
   static_assert(S::kRows == kGatedSave, "a tile begins behind a checkpoint");
   __shared__ TileRows<S::kRows> rows;
-  __shared__ PartMaps<S::kParts> fwd;      // the states' maps
+  __shared__ PartMaps<S::kParts> fwd;  // the states' maps
   __shared__ float back[S::kParts][kGatedChannels];
-  __shared__ uint8_t ends[S::kParts];      // the part holds a sequence's last row
+  __shared__ uint8_t ends[S::kParts];  // the part holds a sequence's last row
+  __shared__ float rate[kGatedChannels];
+  __shared__ float starts[S::kRows][kGatedChannels];  // where a sequence begins: its initial state, then that one's gradient
   __shared__ uint32_t ticket;
-  const int64_t n = take_ticket(p, &ticket);
-  const int64_t turn = n / p.chains, tile = p.tiles - 1 - turn;
-  const int64_t c0 = (n - turn * p.chains) * kGatedChannels;
-  const int lane = threadIdx.x % S::kLanes, part = threadIdx.x / S::kLanes;
-  const int64_t row0 = tile * S::kRows + part * R;
-  const LaneChannels<V> ch(c0 + lane * V, p.dim);
-  const bool has_z = p.z != nullptr;
+  const uint32_t n = take_ticket(p, &ticket);
+  const uint32_t turn = n / static_cast<uint32_t>(p.chains), tile = static_cast<uint32_t>(p.tiles) - 1u - turn;
+  const Channels<V> ch(n - turn * static_cast<uint32_t>(p.chains), p.dim);
+  const int lane = threadIdx.x % S::kLanes, part = threadIdx.x / S::kLanes, at0 = part * R, wave = threadIdx.x / 64;
+  const int64_t tile0 = static_cast<int64_t>(tile) * S::kRows, d = ch.of(lane);
 
-  Run<BF16, V> x[R], ag[R], xg[R], z[R], dy[R];
-  const void* zsrc = has_z ? p.z : p.x;
+  const float param = p.param[ch.of(threadIdx.x % kGatedChannels / V) + threadIdx.x % V];
+  find_rows(rows, p, static_cast<uint32_t>(tile0));
+  float se[V], sa[V], sx[V];  // sums over the lane's rows
 #pragma unroll
-  for (int j = 0; j < R; ++j) {
-    const int64_t row = row0 + j < p.total ? row0 + j : p.total - 1;
-    x[j].load(p.x, row * p.dim + ch.d);
-    ag[j].load(p.ag, row * p.dim + ch.d);
-    xg[j].load(p.xg, row * p.dim + ch.d);
-    z[j].load(zsrc, row * p.dim + ch.d);
-    dy[j].load(p.dy, row * p.dim + ch.d);
-  }
-  const LaneParams<V> par(p, ch.d);
-  find_rows(rows, p, tile * S::kRows);
+  for (int v = 0; v < V; ++v) se[v] = sa[v] = sx[v] = 0.0f;
   __syncthreads();
-  const int at0 = part * R;
-  const uint32_t bits = (1u << R) - 1u;
-  const uint32_t first = static_cast<uint32_t>(rows.first[at0 >> 6] >> (at0 & 63)) & bits;
-  const uint32_t last = static_cast<uint32_t>(rows.last[at0 >> 6] >> (at0 & 63)) & bits;
-  const uint32_t live = static_cast<uint32_t>(rows.live[at0 >> 6] >> (at0 & 63)) & bits;
-
-  float a[R][V], h[R][V], g[R][V], f[R][V], r[R][V], i[R][V], w[R][V];
-  float A[V], B[V];
+  auto body = [&](auto edges) {
+    constexpr bool EDGES = decltype(edges)::value;
+    Run<BF16, V> x[R], ag[R], xg[R], z[R], dy[R];
+    load_rows<!EDGES>(ag, p.ag, p.dim, tile0, at0, d, p.total);
+    load_rows<!EDGES>(xg, p.xg, p.dim, tile0, at0, d, p.total);
+    load_rows<!EDGES>(x, p.x, p.dim, tile0, at0, d, p.total);
+    if constexpr (Z) load_rows<!EDGES>(z, p.z, p.dim, tile0, at0, d, p.total);
+    load_rows<!EDGES>(dy, p.dy, p.dim, tile0, at0, d, p.total);
+    float ab[V], xb[V], k[V];
+    load_bias<V>(p.ab, d, ab);
+    load_bias<V>(p.xb, d, xb);
+    if (threadIdx.x < kGatedChannels) rate[threadIdx.x] = decay_rate(p.scale, param);
+    __syncthreads();
 #pragma unroll
-  for (int v = 0; v < V; ++v) A[v] = 1.0f, B[v] = 0.0f;
+    for (int v = 0; v < V; ++v) k[v] = rate[lane * V + v];
+    const PartRows<R> in(rows, at0);
+    if constexpr (EDGES) {
 #pragma unroll
-  for (int j = 0; j < R; ++j) {
-    const bool on = live >> j & 1;
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      r[j][v] = sigmoid_f32(ag[j].get(v) + par.ab[v]);
-      i[j][v] = sigmoid_f32(xg[j].get(v) + par.xb[v]);
-      const float l = par.k[v] * r[j][v], e = hw_exp2(l * kLog2e);
-      w[j][v] = input_weight(l, e);
-      a[j][v] = on ? e : 1.0f;
-      h[j][v] = on ? w[j][v] * (i[j][v] * x[j].get(v)) : 0.0f;
-      const float d = on ? dy[j].get(v) : 0.0f, zv = z[j].get(v), o = sigmoid_f32(zv);
-      g[j][v] = on && has_z ? d * (zv * o) : d;
-      f[j][v] = d * (o * fmaf(zv, 1.0f - o, 1.0f));
-    }
-    if (first >> j & 1) {
-      float h0[V];
-      initial_state<V>(p, rows.seq[at0 + j], ch.d, h0);
-#pragma unroll
-      for (int v = 0; v < V; ++v) h[j][v] = fmaf(a[j][v], h0[v], h[j][v]);
-    }
-    if ((last >> j & 1) && p.dlast) {
-#pragma unroll
-      for (int v = 0; v < V; ++v) g[j][v] += p.dlast[static_cast<int64_t>(rows.seq[at0 + j]) * p.dim + ch.d + v];
-    }
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      A[v] *= a[j][v];
-      B[v] = first >> j & 1 ? h[j][v] : fmaf(a[j][v], B[v], h[j][v]);
-    }
-  }
-  float C[V];  // a G of the row that the part begins with
-#pragma unroll
-  for (int v = 0; v < V; ++v) C[v] = 0.0f;
-#pragma unroll
-  for (int j = R - 1; j >= 0; --j)
-#pragma unroll
-    for (int v = 0; v < V; ++v) C[v] = a[j][v] * (last >> j & 1 ? g[j][v] : g[j][v] + C[v]);
-#pragma unroll
-  for (int v = 0; v < V; ++v) {
-    fwd.a[part][lane * V + v] = A[v];
-    fwd.b[part][lane * V + v] = B[v];
-    back[part][lane * V + v] = C[v];
-  }
-  if (lane == 0) {
-    fwd.own[part] = first != 0;
-    ends[part] = last != 0;
-  }
-  __syncthreads();
-
-  // the first wave runs the states through the parts, the second the adjoint
-  const int wave = threadIdx.x / 64;
-  if (wave < 2) {
-    const int c = threadIdx.x & 63, l = c / V, v = c - l * V;
-    const LaneChannels<V> my(c0 + l * V, p.dim);
-    const bool on = v >= my.own;
-    const int64_t d = my.d + v;
-    float pa[S::kParts], pb[S::kParts];
-#pragma unroll
-    for (int k = 0; k < S::kParts; ++k) {
-      pa[k] = fwd.a[k][c];
-      pb[k] = wave == 0 ? fwd.b[k][c] : back[k][c];
-    }
-    if (wave == 0) {
-      float s = tile > 0 ? p.ckpt[(tile - 1) * p.dim + d] : 0.0f;
-#pragma unroll
-      for (int k = 0; k < S::kParts; ++k) {
-        fwd.b[k][c] = s;
-        s = fwd.own[k] ? pb[k] : fmaf(pa[k], s, pb[k]);
+      for (int j = 0; j < R; ++j) {
+        const bool off = !(in.live >> j & 1);
+        no_row<BF16, V>(ag[j], off, true);
+        no_row<BF16, V>(xg[j], off, false);
+        no_row<BF16, V>(x[j], off, false);
+        if constexpr (Z) no_row<BF16, V>(z[j], off, false);
+        no_row<BF16, V>(dy[j], off, false);
       }
-    } else {
-      float ta = 1.0f, tb = 0.0f;
-      bool own = false;
+    }
+    float a[R][V], h[R][V], g[R][V], f[R][V], r[R][V], i[R][V], w[R][V];
 #pragma unroll
-      for (int k = S::kParts - 1; k >= 0; --k) {
-        if (ends[k]) {
-          own = true;
-          tb = pb[k];
-        } else {
-          ta *= pa[k];
-          tb = fmaf(pa[k], tb, pb[k]);
+    for (int j = 0; j < R; ++j)
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        r[j][v] = sigmoid_f32(ag[j].get(v), ab[v]);
+        i[j][v] = sigmoid_f32(xg[j].get(v), xb[v]);
+        const float l = k[v] * r[j][v];
+        a[j][v] = hw_exp2(l * kLog2e);
+        w[j][v] = input_weight(l, a[j][v]);
+        h[j][v] = w[j][v] * (i[j][v] * x[j].get(v));
+        g[j][v] = dy[j].get(v);
+        if constexpr (Z) {
+          const float zv = z[j].get(v), o = sigmoid_f32(zv), od = g[j][v] * o;
+          g[j][v] = od * zv;
+          f[j][v] = od * fmaf(zv, 1.0f - o, 1.0f);
+          asm volatile("" : "+v"(f[j][v]));  // (worked out here, not where it is used: one register for three)
         }
       }
-      float s = 0.0f;
-      if (p.ticket) {
-        const int64_t at = tile * p.dim + d;
-        if (on && !own) publish(p.maps + at, ta, tb);
-        if (on && own) publish(p.ends + at, tb);
-        s = look_back(p.maps + at + p.dim, p.ends + at + p.dim, p.dim, turn, on && !(rows.last[0] >> 63));
-        if (on && !own) publish(p.ends + at, fmaf(ta, s, tb));
-      }
+    if constexpr (EDGES) {
+      for (uint32_t bits = in.first; bits; bits &= bits - 1) {
+        const int at = __builtin_ctz(bits);
+        const Run<false, V> h0 = batch_state<V>(p.in.data, rows.seq[at0 + at], p.dim, d);
 #pragma unroll
-      for (int k = S::kParts - 1; k >= 0; --k) {
-        back[k][c] = s;
-        s = ends[k] ? pb[k] : fmaf(pa[k], s, pb[k]);
+        for (int v = 0; v < V; ++v) {
+          starts[at0 + at][lane * V + v] = h0.get(v);
+#pragma unroll
+          for (int j = 0; j < R; ++j) h[j][v] = j == at ? fmaf(a[j][v], h0.get(v), h[j][v]) : h[j][v];
+        }
+      }
+      if (p.dlast) {
+        for (uint32_t bits = in.last; bits; bits &= bits - 1) {
+          const int at = __builtin_ctz(bits);
+          const Run<false, V> end = batch_state<V>(p.dlast, rows.seq[at0 + at], p.dim, d);
+#pragma unroll
+          for (int v = 0; v < V; ++v)
+#pragma unroll
+            for (int j = 0; j < R; ++j) g[j][v] = j == at ? g[j][v] + end.get(v) : g[j][v];
+        }
       }
     }
-  }
-  __syncthreads();
-
-  float enter[V], se[V], sa[V], sx[V];
+    float A[V], B[V], C[V];  // C: a G of the row that the part begins with
 #pragma unroll
-  for (int v = 0; v < V; ++v) {
-    enter[v] = fwd.b[part][lane * V + v];
-    C[v] = back[part][lane * V + v];
-    se[v] = sa[v] = sx[v] = 0.0f;
-  }
+    for (int v = 0; v < V; ++v) A[v] = 1.0f, B[v] = C[v] = 0.0f;
 #pragma unroll
-  for (int j = 0; j < R; ++j)
+    for (int j = 0; j < R; ++j)
 #pragma unroll
-    for (int v = 0; v < V; ++v) h[j][v] = first >> j & 1 ? h[j][v] : fmaf(a[j][v], j > 0 ? h[j - 1][v] : enter[v], h[j][v]);
+      for (int v = 0; v < V; ++v) {
+        A[v] *= a[j][v];
+        B[v] = EDGES && (in.first >> j & 1) ? h[j][v] : fmaf(a[j][v], B[v], h[j][v]);
+      }
 #pragma unroll
-  for (int j = R - 1; j >= 0; --j) {
-    float prev[V], odx[V], oda[V], odg[V], odz[V];
+    for (int j = R - 1; j >= 0; --j)
 #pragma unroll
-    for (int v = 0; v < V; ++v) prev[v] = j > 0 ? h[j > 0 ? j - 1 : 0][v] : enter[v];
-    if (first >> j & 1) initial_state<V>(p, rows.seq[at0 + j], ch.d, prev);
-    const bool on = live >> j & 1;
+      for (int v = 0; v < V; ++v) C[v] = a[j][v] * (EDGES && (in.last >> j & 1) ? g[j][v] : g[j][v] + C[v]);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const float G = last >> j & 1 ? g[j][v] : g[j][v] + C[v];
-      const float xv = x[j].get(v), l = par.k[v] * r[j][v];
-      const float la = l * a[j][v];
-      const float q = w[j][v] > 0.0f ? -la * a[j][v] * hw_rcp(w[j][v]) : 0.0f;
-      const float E = on ? G * fmaf(la, prev[v], i[j][v] * xv * q) : 0.0f;
-      odz[v] = f[j][v] * h[j][v];
-      oda[v] = E * (1.0f - r[j][v]);
-      odx[v] = G * w[j][v] * i[j][v];
-      odg[v] = on ? odx[v] * xv * (1.0f - i[j][v]) : 0.0f;
-      se[v] += E;
-      sa[v] += oda[v];
-      sx[v] += odg[v];
-      C[v] = a[j][v] * G;
+      fwd.a[part][lane * V + v] = A[v];
+      fwd.b[part][lane * V + v] = B[v];
+      back[part][lane * V + v] = C[v];
     }
-    if (on) {
-      const int64_t at = (row0 + j) * p.dim + ch.d;
-      store_own<BF16, V>(p.dx, at, ch.own, odx);
-      store_own<BF16, V>(p.dag, at, ch.own, oda);
-      store_own<BF16, V>(p.dxg, at, ch.own, odg);
-      if (has_z) store_own<BF16, V>(p.dz, at, ch.own, odz);
-      if ((first >> j & 1) && p.dh0)
-        store_own<false, V>(p.dh0, static_cast<int64_t>(rows.seq[at0 + j]) * p.dim + ch.d, ch.own, C);
+    if (EDGES && lane == 0) {
+      fwd.own[part] = in.first != 0;
+      ends[part] = in.last != 0;
     }
-  }
+    __syncthreads();
+
+    // the first wave runs the states through the parts, the second the adjoint
+    if (wave < 2) {
+      const int c = threadIdx.x & 63;
+      const bool on = ch.has(c / V);
+      const int64_t dc = ch.of(c / V) + c % V;
+      float pa[S::kParts], pb[S::kParts];
+#pragma unroll
+      for (int q = 0; q < S::kParts; ++q) {
+        pa[q] = fwd.a[q][c];
+        pb[q] = wave == 0 ? fwd.b[q][c] : back[q][c];
+      }
+      if (wave == 0) {
+        float s = tile > 0 ? p.ckpt[(tile - 1) * p.dim + dc] : 0.0f;
+#pragma unroll
+        for (int q = 0; q < S::kParts; ++q) {
+          fwd.b[q][c] = s;
+          s = EDGES && fwd.own[q] ? pb[q] : fmaf(pa[q], s, pb[q]);
+        }
+      } else {
+        float ta = 1.0f, tb = 0.0f;
+        bool own = false;
+#pragma unroll
+        for (int q = S::kParts - 1; q >= 0; --q) {
+          const bool stops = EDGES && ends[q];
+          own |= stops;
+          ta *= pa[q];
+          tb = stops ? pb[q] : fmaf(pa[q], tb, pb[q]);
+        }
+        float s = 0.0f;
+        if (p.ticket) {
+          const int64_t at = tile * p.dim + dc;
+          if (on && !own) publish(p.maps + at, ta, tb);
+          if (on && own) publish(p.ends + at, tb);
+          s = look_back(p.maps + at + p.dim, p.ends + at + p.dim, p.dim, turn, on && !(EDGES && (rows.last[0] >> 63)));
+          if (on && !own) publish(p.ends + at, fmaf(ta, s, tb));
+        }
+#pragma unroll
+        for (int q = S::kParts - 1; q >= 0; --q) {
+          back[q][c] = s;
+          s = EDGES && ends[q] ? pb[q] : fmaf(pa[q], s, pb[q]);
+        }
+      }
+    }
+    __syncthreads();
+
+    // what the rest works out again rather than holds: the compiler would keep every common term in registers
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+#pragma unroll
+      for (int q = 0; q < Run<BF16, V>::kWords; ++q) asm volatile("" : "+v"(x[j].w[q]));
+#pragma unroll
+      for (int v = 0; v < V; ++v) asm volatile("" : "+v"(r[j][v]), "+v"(i[j][v]));
+    }
+    if (!EDGES || ch.has(lane)) {
+      float enter[V];
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        enter[v] = fwd.b[part][lane * V + v];
+        C[v] = back[part][lane * V + v];
+      }
+#pragma unroll
+      for (int j = 0; j < R; ++j)
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          const float next = fmaf(a[j][v], j > 0 ? h[j > 0 ? j - 1 : 0][v] : enter[v], h[j][v]);
+          h[j][v] = EDGES && (in.first >> j & 1) ? h[j][v] : next;
+        }
+#pragma unroll
+      for (int j = R - 1; j >= 0; --j) {
+        float prev[V], odx[V], oda[V], odg[V], odz[V];
+        const bool on = !EDGES || (in.live >> j & 1);
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          prev[v] = j > 0 ? h[j > 0 ? j - 1 : 0][v] : enter[v];
+          if (EDGES && (in.first >> j & 1)) prev[v] = starts[at0 + j][lane * V + v];
+        }
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          const float G = EDGES && (in.last >> j & 1) ? g[j][v] : g[j][v] + C[v];
+          const float xv = x[j].get(v), la = k[v] * r[j][v] * a[j][v];
+          const float q = w[j][v] > 0.0f ? -la * a[j][v] * hw_rcp(w[j][v]) : 0.0f;
+          float E = G * fmaf(la, prev[v], i[j][v] * xv * q);
+          odx[v] = G * w[j][v] * i[j][v];
+          odg[v] = odx[v] * xv * (1.0f - i[j][v]);
+          if (EDGES && !on) E = odg[v] = 0.0f;
+          if constexpr (Z) odz[v] = f[j][v] * h[j][v];
+          oda[v] = E * (1.0f - r[j][v]);
+          se[v] += E;
+          sa[v] += oda[v];
+          sx[v] += odg[v];
+          C[v] = a[j][v] * G;
+          if (EDGES && (in.first >> j & 1)) starts[at0 + j][lane * V + v] = C[v];
+        }
+        if (on) {
+          constexpr int ES = BF16 ? 2 : 4;
+          const uint32_t off = (static_cast<uint32_t>(at0) * static_cast<uint32_t>(p.dim) + static_cast<uint32_t>(d)) * ES;
+          auto store = [&](void* base, const float(&val)[V]) {
+            Run<BF16, V> out;
+            out.set(val);
+            out.store_bytes(static_cast<char*>(base) + (tile0 + j) * p.dim * ES + off);
+          };
+          store(p.dx, odx);
+          store(p.dag, oda);
+          store(p.dxg, odg);
+          if constexpr (Z) store(p.dz, odz);
+        }
+      }
+      if constexpr (EDGES) {
+        if (p.dh0) {
+          for (uint32_t bits = in.first; bits; bits &= bits - 1) {
+            const int at = at0 + __builtin_ctz(bits);
+            Run<false, V> out;
+#pragma unroll
+            for (int v = 0; v < V; ++v) out.w[v] = __builtin_bit_cast(uint32_t, starts[at][lane * V + v]);
+            out.store(p.dh0, static_cast<int64_t>(rows.seq[at]) * p.dim + d);
+          }
+        }
+      }
+    }
+  };
+  if (rows.inside() && ch.count == kGatedChannels) body(std::false_type{});
+  else body(std::true_type{});
   // sums over the tile's rows, in the order of its parts
   __syncthreads();
 #pragma unroll
@@ -602,12 +773,11 @@ __global__ __launch_bounds__(kGatedThreads) void gated_scan_bwd_kernel(const Gat
   }
   __syncthreads();
   if (wave < 3) {
-    const int c = threadIdx.x & 63, l = c / V, v = c - l * V;
-    const LaneChannels<V> my(c0 + l * V, p.dim);
+    const int c = threadIdx.x & 63;
     float s = 0.0f;
 #pragma unroll
-    for (int k = 0; k < S::kParts; ++k) s += wave == 0 ? fwd.a[k][c] : wave == 1 ? fwd.b[k][c] : back[k][c];
-    if (v >= my.own) p.partial[(tile * 3 + wave) * p.dim + my.d + v] = s;
+    for (int q = 0; q < S::kParts; ++q) s += wave == 0 ? fwd.a[q][c] : wave == 1 ? fwd.b[q][c] : back[q][c];
+    if (ch.has(c / V)) p.partial[(static_cast<int64_t>(tile) * 3 + wave) * p.dim + ch.of(c / V) + c % V] = s;
   }
 }
 
@@ -659,6 +829,23 @@ __global__ __launch_bounds__(256) static void gated_keep_kernel(const float* in,
   if (i < n) out[i] = in ? in[i] : 0.0f;
 }
 
+// V values from the skip-th on
+template <bool BF16, int V>
+__device__ __forceinline__ void store_from(void* base, int64_t idx, int skip, const float (&val)[V]) {
+  Run<BF16, V> r;
+  r.set(val);
+  if (skip == 0) {
+    r.store(base, idx);
+  } else {
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      if (v < skip) continue;
+      if constexpr (BF16) static_cast<uint16_t*>(base)[idx + v] = static_cast<uint16_t>(r.w[v >> 1] >> (16 * (v & 1)));
+      else static_cast<uint32_t*>(base)[idx + v] = r.w[v];
+    }
+  }
+}
+
 // One token on a cache: a thread owns V channels of R entries.
 struct GatedStepArgs {
   GatedArgs g;      // rows are the batch's entries; in: the cache
@@ -670,8 +857,15 @@ __global__ __launch_bounds__(kGatedThreads) void gated_step_kernel(const GatedSt
   const GatedArgs& p = q.g;
   const int64_t natural = (static_cast<int64_t>(blockIdx.x) * kGatedThreads + threadIdx.x) * V;
   if (natural >= p.dim) return;
-  const LaneChannels<V> ch(natural, p.dim);
-  const LaneParams<V> par(p, ch.d);
+  // the last lane's channels begin further left where dim is no multiple of V; those that are its neighbour's
+  // (the first `skip`) it does not store, since it may read their state after the neighbour has written it
+  const int64_t d = natural < p.dim - V ? natural : p.dim - V;
+  const int skip = static_cast<int>(natural - d);
+  float ab[V], xb[V], rate[V];
+  load_bias<V>(p.ab, d, ab);
+  load_bias<V>(p.xb, d, xb);
+#pragma unroll
+  for (int v = 0; v < V; ++v) rate[v] = decay_rate(p.scale, p.param[d + v]);
   const bool has_z = p.z != nullptr;
   const void* zsrc = has_z ? p.z : p.x;
   const int64_t zstride = has_z ? p.sz : p.sx;
@@ -687,26 +881,26 @@ __global__ __launch_bounds__(kGatedThreads) void gated_step_kernel(const GatedSt
 #pragma unroll
     for (int k = 0; k < R; ++k) {
       // every load on every path: an entry past the batch or without a slot reads entry b0 and slot 0
-      x[k].load(p.x, e[k] * p.sx + ch.d);
-      ag[k].load(p.ag, e[k] * p.sag + ch.d);
-      xg[k].load(p.xg, e[k] * p.sxg + ch.d);
-      z[k].load(zsrc, e[k] * zstride + ch.d);
-      st[k].load(p.in.data, (at[k] < 0 ? 0 : at[k]) + ch.d);
+      x[k].load(p.x, e[k] * p.sx + d);
+      ag[k].load(p.ag, e[k] * p.sag + d);
+      xg[k].load(p.xg, e[k] * p.sxg + d);
+      z[k].load(zsrc, e[k] * zstride + d);
+      st[k].load(p.in.data, (at[k] < 0 ? 0 : at[k]) + d);
     }
 #pragma unroll
     for (int k = 0; k < R; ++k) {
       float h[V], y[V];
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        const float l = par.k[v] * sigmoid_f32(ag[k].get(v) + par.ab[v]);
-        const float i = sigmoid_f32(xg[k].get(v) + par.xb[v]);
+        const float l = rate[v] * sigmoid_f32(ag[k].get(v), ab[v]);
+        const float i = sigmoid_f32(xg[k].get(v), xb[v]);
         const float a = hw_exp2(l * kLog2e);
         h[v] = fmaf(a, st[k].get(v), input_weight(l, a) * (i * x[k].get(v)));
         y[v] = has_z ? h[v] * silu_f32(z[k].get(v)) : h[v];
       }
       if (at[k] < 0) continue;
-      store_own<CB16, V>(p.in.data, at[k] + ch.d, ch.own, h);
-      store_own<BF16, V>(p.y, (b0 + k) * p.sy + ch.d, ch.own, y);
+      store_from<CB16, V>(p.in.data, at[k] + d, skip, h);
+      store_from<BF16, V>(p.y, (b0 + k) * p.sy + d, skip, y);
     }
   }
 }
