@@ -714,10 +714,11 @@ SSM_API ssm_status_t ssm_cache_load_q8(int64_t count, int64_t rows, int64_t dsta
  * states through the caller's workspace; the results do not depend on timing.
  * workspace: at least ssm_gated_scan_workspace bytes, 16-byte aligned, the
  * caller's until the call's work is done (each call that may run at the same
- * time needs its own); may be NULL where that is 0.
+ * time needs its own); may be NULL where that is 0.  Packed prompts need that of
+ * one sequence of `total` rows.
  */
-SSM_API ssm_status_t ssm_gated_scan_workspace(int64_t rows, int64_t dim, ssm_dtype_t dtype, int backward,
-                                              int64_t *bytes);
+SSM_API ssm_status_t ssm_gated_scan_workspace(int64_t batch, int64_t seqlen, int64_t dim, ssm_dtype_t dtype,
+                                              int backward, int64_t *bytes);
 
 /*
  * Forward over a batch.
@@ -725,9 +726,11 @@ SSM_API ssm_status_t ssm_gated_scan_workspace(int64_t rows, int64_t dim, ssm_dty
  *   initial_state                (batch, dim) fp32, or NULL: zeros
  *   last_state                   (batch, dim) fp32, or NULL: not written.  With
  *                                seqlen 0 it is the initial state
- *   checkpoints                  (batch * seqlen / 64, dim) fp32 (rounded down)
- *                                for the backward, or NULL: the state after
- *                                every 64th row of the batch's rows
+ *   checkpoints                  (n, dim) fp32 for the backward, or NULL: the
+ *                                state after every 64th row, of each sequence
+ *                                if there are several of 256 rows or more (n =
+ *                                batch * (seqlen / 64), rounded down), else of
+ *                                the batch's rows (n = batch * seqlen / 64)
  * Outputs must not overlap inputs or each other.
  */
 SSM_API ssm_status_t ssm_gated_scan_fwd(int64_t batch, int64_t seqlen, int64_t dim, ssm_dtype_t dtype, const void *x,
@@ -738,7 +741,7 @@ SSM_API ssm_status_t ssm_gated_scan_fwd(int64_t batch, int64_t seqlen, int64_t d
 
 /*
  * Gradients of sum(dy y) + sum(dlast_state last_state), from the forward's
- * inputs and its checkpoints (NULL where the batch has at most 64 rows).
+ * inputs and its checkpoints (may be NULL where the batch has at most 64 rows).
  *   dy, dx, da_gate, dx_gate, dz  (batch, seqlen, dim) dtype; dz is needed with
  *                                 z and not written without
  *   dlast_state                   (batch, dim) fp32, or NULL: zeros

@@ -151,7 +151,7 @@ def load_library(path: str = LIBRARY) -> ctypes.CDLL:
     lib.ssm_cache_store_q8.argtypes = [i64, i64, i64, cache, vp, i64, vp, vp, vp, vp]
     lib.ssm_cache_load_q8.argtypes = [i64, i64, i64, i64, vp, vp, vp, cache, vp, vp]
     gstrides, f32 = ctypes.POINTER(GatedStrides), ctypes.c_float
-    lib.ssm_gated_scan_workspace.argtypes = [i64, i64, i32, i32, ctypes.POINTER(i64)]
+    lib.ssm_gated_scan_workspace.argtypes = [i64, i64, i64, i32, i32, ctypes.POINTER(i64)]
     lib.ssm_gated_scan_fwd.argtypes = [i64, i64, i64, i32] + [vp] * 7 + [f32] + [vp] * 5 + [i64, vp]
     lib.ssm_gated_scan_bwd.argtypes = [i64, i64, i64, i32] + [vp] * 7 + [f32] + [vp] * 13 + [i64, vp]
     lib.ssm_gated_scan_packed_fwd.argtypes = [packed, i64, i32] + [vp] * 7 + [f32, vp, cache, gstrides, vp, i64, vp]

@@ -38,17 +38,24 @@ Tiled backward_kernel(bool bf16, int64_t dim, bool z) {
   return bf16 ? backward_of<true, 2, 8>(z) : backward_of<false, 2, 8>(z);
 }
 
-constexpr int64_t kTicketBytes = 16;
-
-// Tiles of `rows` rows and the bytes that they publish through (0 where one tile has no other to tell)
-ssm_status_t tiles_of(const Tiled& t, int64_t rows, int64_t dim, int64_t* tiles, int64_t* published) {
-  *tiles = (rows + t.rows - 1) / t.rows;
-  *published = 0;
+// How the rows are cut: tiles of sequences by themselves where these are long enough that a last, shorter tile
+// of each costs little, else of all rows, which may share tiles.  The tiles and the bytes that they publish
+// through (0 where no tile enters another).
+constexpr int64_t kOwnTiles = 256;  // rows of a sequence from which on it has tiles of its own
+struct Cut {
+  int64_t tiles, each, published, maps;  // each: of a sequence (0: shared); maps: where they begin
+};
+int64_t chains_of(int64_t dim) { return (dim + ssm::kGatedChannels - 1) / ssm::kGatedChannels; }
+ssm_status_t cut_rows(const Tiled& t, int64_t sequences, int64_t seqlen, int64_t rows, int64_t dim, Cut* out) {
+  *out = Cut{};
+  if (sequences > 1 && seqlen >= kOwnTiles) out->each = (seqlen + t.rows - 1) / t.rows;
+  out->tiles = out->each ? out->each * sequences : (rows + t.rows - 1) / t.rows;
+  if (out->tiles <= 1) return SSM_OK;
   int64_t n;
-  if (*tiles <= 1) return SSM_OK;
-  if (!mul_ok(*tiles, dim, &n) || !mul_ok(n, 12, &n) || __builtin_add_overflow(n, kTicketBytes + 15, &n))
+  out->maps = 16;  // the ticket's line
+  if (!mul_ok(out->tiles, dim, &n) || !mul_ok(n, 12, &n) || __builtin_add_overflow(n, out->maps + 15, &n))
     return fail(SSM_ERR_INVALID_ARG, "workspace size overflows int64");
-  *published = n / 16 * 16;
+  out->published = n / 16 * 16;
   return SSM_OK;
 }
 
@@ -64,14 +71,17 @@ ssm_status_t check_sizes(int64_t rows, int64_t dim, ssm_dtype_t dtype) {
   return SSM_OK;
 }
 
-ssm_status_t workspace_of(int64_t rows, int64_t dim, bool bf16, bool backward, int64_t* bytes) {
-  int64_t tiles;
+ssm_status_t workspace_of(int64_t sequences, int64_t seqlen, int64_t rows, int64_t dim, bool bf16, bool backward,
+                          int64_t* bytes) {
   *bytes = 0;
   if (rows == 0 || dim == 0) return SSM_OK;
-  SSM_TRY(tiles_of(backward ? backward_kernel(bf16, dim, true) : forward_kernel(bf16, dim, true), rows, dim, &tiles, bytes));
+  Cut c;
+  SSM_TRY(cut_rows(backward ? backward_kernel(bf16, dim, true) : forward_kernel(bf16, dim, true), sequences, seqlen, rows,
+                   dim, &c));
+  *bytes = c.published;
   if (backward) {
     int64_t n;
-    if (!mul_ok(tiles, dim, &n) || !mul_ok(n, 12, &n) || __builtin_add_overflow(*bytes, n, bytes))
+    if (!mul_ok(c.tiles, dim, &n) || !mul_ok(n, 12, &n) || __builtin_add_overflow(*bytes, n, bytes))
       return fail(SSM_ERR_INVALID_ARG, "workspace size overflows int64");
   }
   return SSM_OK;
@@ -95,20 +105,21 @@ ssm_status_t check_workspace(const void* workspace, int64_t bytes, int64_t need)
 }
 
 // Clears the words that tiles publish and launches the kernel over all tiles.
-ssm_status_t launch_tiles(const Tiled& t, ssm::GatedArgs& a, int64_t tiles, int64_t published, void* workspace,
-                          hipStream_t st, const char* what) {
+ssm_status_t launch_tiles(const Tiled& t, ssm::GatedArgs& a, const Cut& cut, void* workspace, hipStream_t st,
+                          const char* what) {
   int64_t grid;
-  const int64_t chains = (a.dim + ssm::kGatedChannels - 1) / ssm::kGatedChannels;
-  if (!mul_ok(chains, tiles, &grid) || grid > kMaxBlocks) return fail(SSM_ERR_UNSUPPORTED, "grid too large");
-  const int64_t words = published / 16, blocks = (words + 255) / 256;
+  const int64_t chains = chains_of(a.dim);
+  if (!mul_ok(chains, cut.tiles, &grid) || grid > kMaxBlocks) return fail(SSM_ERR_UNSUPPORTED, "grid too large");
+  const int64_t words = cut.published / 16, blocks = (words + 255) / 256;
   if (blocks > kMaxBlocks) return fail(SSM_ERR_UNSUPPORTED, "grid too large");
-  a.tiles = tiles;
+  a.tiles = cut.tiles;
+  a.each = cut.each;
   a.chains = static_cast<int32_t>(chains);
-  if (published) {
+  if (cut.published) {
     char* w = static_cast<char*>(workspace);
     a.ticket = reinterpret_cast<uint32_t*>(w);
-    a.maps = reinterpret_cast<uint64_t*>(w + kTicketBytes);
-    a.ends = reinterpret_cast<uint32_t*>(w + kTicketBytes + tiles * a.dim * 8);
+    a.maps = reinterpret_cast<uint64_t*>(w + cut.maps);
+    a.ends = reinterpret_cast<uint32_t*>(a.maps + cut.tiles * a.dim);
     hipLaunchKernelGGL(ssm::gated_clear_kernel, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, st,
                        reinterpret_cast<ssm::U32x4*>(w), words);
     SSM_TRY(check_launch("gated scan (clear)"));
@@ -126,6 +137,7 @@ ssm_status_t keep_states(const float* in, float* out, int64_t n, hipStream_t st)
 
 struct Batch {
   int64_t rows, elems, bytes, states;  // bytes of a (batch, seqlen, dim) tensor and of a (batch, dim) fp32 one
+  int64_t saved;                       // checkpoints
 };
 ssm_status_t check_batch(int64_t batch, int64_t seqlen, int64_t dim, ssm_dtype_t dtype, Batch* b) {
   if (batch < 0 || seqlen < 0 || dim < 0)
@@ -136,6 +148,7 @@ ssm_status_t check_batch(int64_t batch, int64_t seqlen, int64_t dim, ssm_dtype_t
       !mul_ok(batch, dim, &b->states) || !mul_ok(b->states, 4, &b->states))
     return fail(SSM_ERR_INVALID_ARG, "tensor size overflows int64");
   if (batch > kMaxIndex) return fail(SSM_ERR_UNSUPPORTED, "batch exceeds int32");
+  b->saved = batch > 1 && seqlen >= kOwnTiles ? batch * (seqlen / ssm::kGatedSave) : b->rows / ssm::kGatedSave;
   return check_sizes(b->rows, dim, dtype);
 }
 
@@ -149,12 +162,13 @@ ssm_status_t first_misaligned(const Arg* args, size_t n) {
 
 extern "C" {
 
-ssm_status_t ssm_gated_scan_workspace(int64_t rows, int64_t dim, ssm_dtype_t dtype, int backward, int64_t* bytes) {
+ssm_status_t ssm_gated_scan_workspace(int64_t batch, int64_t seqlen, int64_t dim, ssm_dtype_t dtype, int backward,
+                                      int64_t* bytes) {
   g_err[0] = '\0';
   if (!bytes) return fail(SSM_ERR_INVALID_ARG, "NULL bytes");
-  if (rows < 0) return fail(SSM_ERR_INVALID_ARG, "negative size (rows=%lld)", (long long)rows);
-  SSM_TRY(check_sizes(rows, dim, dtype));
-  return workspace_of(rows, dim, dtype == SSM_BF16, backward != 0, bytes);
+  Batch n;
+  SSM_TRY(check_batch(batch, seqlen, dim, dtype, &n));
+  return workspace_of(batch, seqlen, n.rows, dim, dtype == SSM_BF16, backward != 0, bytes);
 }
 
 ssm_status_t ssm_gated_scan_fwd(int64_t batch, int64_t seqlen, int64_t dim, ssm_dtype_t dtype, const void* x,
@@ -180,10 +194,10 @@ ssm_status_t ssm_gated_scan_fwd(int64_t batch, int64_t seqlen, int64_t dim, ssm_
   if (!x || !a_gate || !x_gate || !a_param || !y)
     return fail(SSM_ERR_INVALID_ARG, "NULL required pointer (x, a_gate, x_gate, a_param and y)");
   const Tiled t = forward_kernel(dtype == SSM_BF16, dim, z != nullptr);
-  int64_t tiles, published;
-  SSM_TRY(tiles_of(t, n.rows, dim, &tiles, &published));
-  SSM_TRY(check_workspace(workspace, workspace_bytes, published));
-  const Range outs[] = {{y, n.bytes}, r1, {checkpoints, n.rows / ssm::kGatedSave * dim * 4}, {workspace, published}};
+  Cut cut;
+  SSM_TRY(cut_rows(t, batch, seqlen, n.rows, dim, &cut));
+  SSM_TRY(check_workspace(workspace, workspace_bytes, cut.published));
+  const Range outs[] = {{y, n.bytes}, r1, {checkpoints, n.saved * dim * 4}, {workspace, cut.published}};
   const Range ins[] = {{x, n.bytes}, {a_gate, n.bytes}, {x_gate, n.bytes}, {z, n.bytes}, r0,
                        {a_param, dim * 4}, {a_bias, dim * 4}, {x_bias, dim * 4}};
   SSM_TRY(check_overlap(outs, count_of(outs), ins, count_of(ins)));
@@ -195,7 +209,7 @@ ssm_status_t ssm_gated_scan_fwd(int64_t batch, int64_t seqlen, int64_t dim, ssm_
   a.in = {const_cast<float*>(initial_state), batch, dim};
   a.out = {last_state, batch, dim};
   a.ckpt = checkpoints;
-  return launch_tiles(t, a, tiles, published, workspace, st, "gated scan");
+  return launch_tiles(t, a, cut, workspace, st, "gated scan");
 }
 
 ssm_status_t ssm_gated_scan_bwd(int64_t batch, int64_t seqlen, int64_t dim, ssm_dtype_t dtype, const void* x,
@@ -221,12 +235,13 @@ ssm_status_t ssm_gated_scan_bwd(int64_t batch, int64_t seqlen, int64_t dim, ssm_
     return fail(SSM_ERR_INVALID_ARG, "NULL required pointer (x, a_gate, x_gate, dy, dx, da_gate and dx_gate)");
   if (n.elems > 0 && z && !dz) return fail(SSM_ERR_INVALID_ARG, "z needs dz");
   const Tiled t = backward_kernel(dtype == SSM_BF16, dim, z != nullptr);
-  int64_t tiles, published, need;
-  SSM_TRY(tiles_of(t, n.rows, dim, &tiles, &published));
-  SSM_TRY(workspace_of(n.rows, dim, dtype == SSM_BF16, true, &need));
+  Cut cut;
+  int64_t need;
+  SSM_TRY(cut_rows(t, batch, seqlen, n.rows, dim, &cut));
+  SSM_TRY(workspace_of(batch, seqlen, n.rows, dim, dtype == SSM_BF16, true, &need));
   SSM_TRY(check_workspace(workspace, workspace_bytes, need));
-  const int64_t saved = n.rows / ssm::kGatedSave * dim * 4;
-  if (tiles > 1 && !checkpoints) return fail(SSM_ERR_INVALID_ARG, "NULL checkpoints");
+  const int64_t saved = n.saved * dim * 4;
+  if (cut.tiles > 1 && !checkpoints) return fail(SSM_ERR_INVALID_ARG, "NULL checkpoints");
   const Range outs[] = {{dx, n.bytes}, {da_gate, n.bytes}, {dx_gate, n.bytes}, {z ? dz : nullptr, n.bytes},
                         {da_param, dim * 4}, {da_bias, dim * 4}, {dx_bias, dim * 4}, {dinitial_state, n.states},
                         {workspace, need}};
@@ -245,10 +260,10 @@ ssm_status_t ssm_gated_scan_bwd(int64_t batch, int64_t seqlen, int64_t dim, ssm_
     a.in = {const_cast<float*>(initial_state), batch, dim};
     a.ckpt = const_cast<float*>(checkpoints);
     a.dlast = dlast_state; a.dx = dx; a.dag = da_gate; a.dxg = dx_gate; a.dz = dz; a.dh0 = dinitial_state;
-    a.partial = reinterpret_cast<float*>(static_cast<char*>(workspace) + published);
+    a.partial = reinterpret_cast<float*>(static_cast<char*>(workspace) + cut.published);
     sum.partial = a.partial;
-    sum.tiles = tiles;
-    SSM_TRY(launch_tiles(t, a, tiles, published, workspace, st, "gated scan backward"));
+    sum.tiles = cut.tiles;
+    SSM_TRY(launch_tiles(t, a, cut, workspace, st, "gated scan backward"));
   } else if (dinitial_state && n.states > 0) {
     SSM_TRY(keep_states(dlast_state, dinitial_state, n.states / 4, st));
   }
@@ -285,10 +300,10 @@ ssm_status_t ssm_gated_scan_packed_fwd(const ssm_packed_t* seqs, int64_t dim, ss
   Range idx[3];
   SSM_TRY(check_packed_pointers(seqs, idx));
   const Tiled k = forward_kernel(dtype == SSM_BF16, dim, z != nullptr);
-  int64_t tiles, published;
-  SSM_TRY(tiles_of(k, seqs->total, dim, &tiles, &published));
-  SSM_TRY(check_workspace(workspace, workspace_bytes, published));
-  const Range outs[] = {{y, t[4].bytes}, rc, {workspace, published}};
+  Cut cut;
+  SSM_TRY(cut_rows(k, 1, seqs->total, seqs->total, dim, &cut));
+  SSM_TRY(check_workspace(workspace, workspace_bytes, cut.published));
+  const Range outs[] = {{y, t[4].bytes}, rc, {workspace, cut.published}};
   const Range ins[] = {{x, t[0].bytes}, {a_gate, t[1].bytes}, {x_gate, t[2].bytes}, {z, t[3].bytes}, {a_param, dim * 4},
                        {a_bias, dim * 4}, {x_bias, dim * 4}, idx[0], idx[1], idx[2]};
   SSM_TRY(check_overlap(outs, count_of(outs), ins, count_of(ins)));
@@ -299,7 +314,7 @@ ssm_status_t ssm_gated_scan_packed_fwd(const ssm_packed_t* seqs, int64_t dim, ss
   a.cu = seqs->cu_seqlens; a.slots = seqs->cache_slots; a.has_initial = seqs->has_initial;
   a.out = a.in;
   a.cb16 = cache && cache->dtype == SSM_BF16;
-  return launch_tiles(k, a, tiles, published, workspace, static_cast<hipStream_t>(stream), "gated scan (packed)");
+  return launch_tiles(k, a, cut, workspace, static_cast<hipStream_t>(stream), "gated scan (packed)");
 }
 
 ssm_status_t ssm_gated_update_cache(int64_t batch, int64_t dim, ssm_dtype_t dtype, const ssm_cache_t* cache,

@@ -28,7 +28,6 @@ namespace ssm {
 constexpr int kGatedThreads = 256;
 constexpr int kGatedChannels = 64;   // channels of a workgroup: one 128-byte line of a bf16 row
 constexpr uint32_t kEmpty = 0xffffffffu;
-constexpr int kGatedWindow = 2;      // tiles that one look back covers
 constexpr int kGatedSave = 64;       // rows between checkpoints
 
 struct GatedArgs {
@@ -45,10 +44,10 @@ struct GatedArgs {
   CacheRef in, out;              // initial and final states by slot
   int32_t cb16;                  // they are bf16
   float* ckpt;                   // state after every kGatedSave-th row
-  uint32_t* ticket;              // NULL: one tile, nothing is published
-  uint64_t* maps;
+  uint32_t* ticket;              // NULL: no tile enters another
+  uint64_t* maps;                // (tiles, dim), in the order in which tiles are taken
   uint32_t* ends;
-  int64_t tiles;
+  int64_t tiles, each;           // tiles, and those of a sequence if none holds rows of two (else 0)
   int32_t chains;                // blocks of kGatedChannels channels
   // backward
   const void* dy;
@@ -78,19 +77,20 @@ __device__ __forceinline__ void publish(uint64_t* p, float a, float b) {
   __hip_atomic_store(p, (static_cast<uint64_t>(hi) << 32) | lo, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
-// The state that leaves the k-th tile before this one (k = 0: the one just before), in the order in
-// which tiles are taken; `first` of them exist.  maps and ends point at the nearest one's words, `step` elements apart.
+// The state that leaves the tile before this one.  maps and ends point at that tile's words; those of the tiles
+// before it lie `step` elements on each, `first` tiles in all.  WINDOW tiles' words are asked for at once.
 // Every lane of the wave calls it; lanes with `on` false (no channel, or nothing enters) get 0.
+template <int WINDOW>
 __device__ __forceinline__ float look_back(const uint64_t* maps, const uint32_t* ends, int64_t step, int64_t first,
                                            bool on) {
   float h = 0.0f;
   bool done = !on;
   while (!__all(done)) {
     if (!done) {
-      uint32_t e[kGatedWindow];
-      uint64_t m[kGatedWindow];
+      uint32_t e[WINDOW];
+      uint64_t m[WINDOW];
 #pragma unroll
-      for (int k = 0; k < kGatedWindow; ++k) {
+      for (int k = 0; k < WINDOW; ++k) {
         // before the first tile the state is 0
         e[k] = k < first ? __hip_atomic_load(ends + k * step, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : 0u;
         m[k] = k < first ? __hip_atomic_load(maps + k * step, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : 0u;
@@ -98,7 +98,7 @@ __device__ __forceinline__ float look_back(const uint64_t* maps, const uint32_t*
       int near = 0;  // tiles over whose maps the nearest end state comes here
       bool open = true;
 #pragma unroll
-      for (int k = 0; k < kGatedWindow; ++k) {
+      for (int k = 0; k < WINDOW; ++k) {
         if (open && e[k] != kEmpty) {
           done = true;
           open = false;
@@ -108,7 +108,7 @@ __device__ __forceinline__ float look_back(const uint64_t* maps, const uint32_t*
       }
       if (done) {
 #pragma unroll
-        for (int k = kGatedWindow - 1; k >= 0; --k) {
+        for (int k = WINDOW - 1; k >= 0; --k) {
           const float a = __builtin_bit_cast(float, static_cast<uint32_t>(m[k]));
           const float b = __builtin_bit_cast(float, static_cast<uint32_t>(m[k] >> 32));
           if (k == near) h = __builtin_bit_cast(float, e[k]);
@@ -151,11 +151,11 @@ __device__ inline int64_t last_not_above(const int32_t* cu, int64_t nseq, int64_
 // not above its first row on (64 probes at a time: one round trip up to 63 sequences, two up to 4095), and
 // its lanes search them in its registers.
 template <int ROWS>
-__device__ __forceinline__ void find_rows(TileRows<ROWS>& t, const GatedArgs& p, uint32_t row0) {
+__device__ __forceinline__ void find_rows(TileRows<ROWS>& t, const GatedArgs& p, uint32_t row0, int64_t end) {
   const uint32_t at = threadIdx.x;
   if (at >= (ROWS < 64 ? 64 : ROWS)) return;  // whole waves
   const int32_t row = static_cast<int32_t>(row0 + at);  // (total is at most 2^31 - 1; rows behind it are not live)
-  bool first = false, last = false, live = at < ROWS && row0 + at < p.total;
+  bool first = false, last = false, live = at < ROWS && row0 + at < end;
   int32_t s = -1;
   if (!p.cu) {
     if (live) {
@@ -180,18 +180,18 @@ __device__ __forceinline__ void find_rows(TileRows<ROWS>& t, const GatedArgs& p,
 #pragma unroll
     for (int k = 32; k; k >>= 1) c += __shfl(entry, c + k - 1) <= row ? k : 0;
     c += __shfl(entry, c < 64 ? c : 63) <= row && c < 64 ? 1 : 0;
-    int32_t begin = __shfl(entry, c > 0 ? c - 1 : 0), end = __shfl(entry, c < 64 ? c : 63);
+    int32_t begin = __shfl(entry, c > 0 ? c - 1 : 0), stop = __shfl(entry, c < 64 ? c : 63);
     int64_t n = s0 + c - 1;
     if (live && c == 64) {  // more sequences than that begin here
       n = last_not_above(p.cu, p.nseq, row);
       begin = n >= 0 ? p.cu[n] : 0;
-      end = n >= 0 && n < p.nseq ? p.cu[n + 1] : 0;
+      stop = n >= 0 && n < p.nseq ? p.cu[n + 1] : 0;
     }
     live = live && c > 0 && n >= 0 && n < p.nseq;
     if (live) {
       s = static_cast<int32_t>(n);
       first = begin == row;
-      last = end == row + 1;
+      last = stop == row + 1;
     }
   }
   if (at < ROWS) t.seq[at] = s;
@@ -341,13 +341,59 @@ struct PartMaps {
   uint8_t own[PARTS];  // the part holds a state of its own
 };
 
-// A tile's number, in the order in which tiles are taken
-__device__ __forceinline__ uint32_t take_ticket(const GatedArgs& p, uint32_t* shared) {
-  if (!p.ticket) return blockIdx.x;
-  if (threadIdx.x == 0)
-    *shared = __hip_atomic_fetch_add(p.ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) + 1u;  // (cleared to ~0)
-  __syncthreads();
-  return __builtin_amdgcn_readfirstlane(*shared);
+// The tile that a workgroup takes: the next one.  Tiles of a sequence that share no row with another come in the
+// order (their place in the sequence, sequence, channels), so that a tile waits for one that was taken a batch
+// earlier: 8 x 2048 x 1536 rows take 73 us forward and 127 backward, and 80 and 150 in the order of the rows.
+// (A counter for each block of channels in place of one for all: 71 and 130, and one sequence of 30011 x 2560
+// 204 and 397 us for 190 and 359, since the blocks' rows drift apart.  Workgroups that stay and take tile after
+// tile with the next number asked for ahead: 112 us, since the tile that a number stands for then waits.)
+struct Turn {
+  uint32_t block, turn;  // in the order in which tiles are taken
+  uint32_t before;       // tiles before it that may enter it
+  uint32_t apart;        // turns between those
+  uint32_t s;            // its sequence, where tiles have one
+  int64_t row0;          // its first row
+  int64_t end;           // where its rows end at the latest
+  template <int ROWS>
+  __device__ __forceinline__ static Turn take(const GatedArgs& p, uint32_t* shared, bool backward) {
+    Turn t;
+    uint32_t n = blockIdx.x;
+    if (p.ticket) {
+      if (threadIdx.x == 0)
+        *shared = __hip_atomic_fetch_add(p.ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) + 1u;  // (cleared to ~0)
+      __syncthreads();
+      n = __builtin_amdgcn_readfirstlane(*shared);
+    }
+    t.turn = n / static_cast<uint32_t>(p.chains);
+    t.block = n - t.turn * static_cast<uint32_t>(p.chains);
+    const uint32_t tiles = static_cast<uint32_t>(p.tiles);
+    if (p.each) {
+      const uint32_t each = static_cast<uint32_t>(p.each), batch = static_cast<uint32_t>(p.nseq);
+      const uint32_t place = t.turn / batch;
+      t.s = t.turn - place * batch;
+      t.before = place;
+      t.apart = batch;
+      t.row0 = t.s * p.seqlen + static_cast<int64_t>(backward ? each - 1 - place : place) * ROWS;
+      t.end = (t.s + int64_t{1}) * p.seqlen;
+    } else {
+      t.before = t.turn;
+      t.apart = 1;
+      t.s = 0;
+      t.row0 = static_cast<int64_t>(backward ? tiles - 1 - t.turn : t.turn) * ROWS;
+      t.end = p.total;
+    }
+    return t;
+  }
+};
+
+// Checkpoints: the state after every kGatedSave-th row, of each sequence by itself where tiles are (`each`), else
+// of the batch's rows.  The index of the one before row `next` (a multiple of kGatedSave from its sequence's or the
+// batch's first on), or -1: none.
+__device__ __forceinline__ int64_t checkpoint_after(const GatedArgs& p, const Turn& tile, int64_t next) {
+  const uint32_t from = static_cast<uint32_t>(next - (p.each ? tile.end - p.seqlen : 0));
+  if (next > tile.end || from < kGatedSave || from % kGatedSave) return -1;
+  const uint32_t n = p.each ? tile.s * (static_cast<uint32_t>(p.seqlen) / kGatedSave) : 0;  // (fewer than rows)
+  return n + from / kGatedSave - 1;
 }
 
 template <bool BF16, bool Z, int V, int R>
@@ -357,24 +403,23 @@ __global__ __launch_bounds__(kGatedThreads) void gated_scan_kernel(const GatedAr
   __shared__ PartMaps<S::kParts> maps;
   __shared__ float entering[kGatedChannels], rate[kGatedChannels];
   __shared__ uint32_t ticket;
-  const uint32_t n = take_ticket(p, &ticket);
-  const uint32_t tile = n / static_cast<uint32_t>(p.chains);
-  const Channels<V> ch(n - tile * static_cast<uint32_t>(p.chains), p.dim);
+  const Turn tile = Turn::take<S::kRows>(p, &ticket, false);
+  const Channels<V> ch(tile.block, p.dim);
   const int lane = threadIdx.x % S::kLanes, part = threadIdx.x / S::kLanes, at0 = part * R;
-  const int64_t tile0 = static_cast<int64_t>(tile) * S::kRows, d = ch.of(lane);
+  const int64_t tile0 = tile.row0, d = ch.of(lane);
 
   const float param = p.param[ch.of(threadIdx.x % kGatedChannels / V) + threadIdx.x % V];
-  find_rows(rows, p, static_cast<uint32_t>(tile0));
+  find_rows(rows, p, static_cast<uint32_t>(tile0), tile.end);
   __syncthreads();
 
   auto body = [&](auto edges) {
     constexpr bool EDGES = decltype(edges)::value;
     // (each variant loads for itself: rows loaded before the branch would stay in registers beside the other's)
     Run<BF16, V> x[R], ag[R], xg[R], z[R];
-    load_rows<!EDGES>(ag, p.ag, p.sag, tile0, at0, d, p.total);
-    load_rows<!EDGES>(xg, p.xg, p.sxg, tile0, at0, d, p.total);
-    load_rows<!EDGES>(x, p.x, p.sx, tile0, at0, d, p.total);
-    if constexpr (Z) load_rows<!EDGES>(z, p.z, p.sz, tile0, at0, d, p.total);
+    load_rows<!EDGES>(ag, p.ag, p.sag, tile0, at0, d, tile.end);
+    load_rows<!EDGES>(xg, p.xg, p.sxg, tile0, at0, d, tile.end);
+    load_rows<!EDGES>(x, p.x, p.sx, tile0, at0, d, tile.end);
+    if constexpr (Z) load_rows<!EDGES>(z, p.z, p.sz, tile0, at0, d, tile.end);
     float ab[V], xb[V];
     load_bias<V>(p.ab, d, ab);
     load_bias<V>(p.xb, d, xb);
@@ -445,10 +490,10 @@ __global__ __launch_bounds__(kGatedThreads) void gated_scan_kernel(const GatedAr
       }
       float h = 0.0f;
       if (p.ticket) {
-        const int64_t at = tile * p.dim + ch.of(c / V) + c % V;
+        const int64_t at = tile.turn * p.dim + ch.of(c / V) + c % V, step = -(tile.apart * p.dim);
         if (on && !own) publish(p.maps + at, ta, tb);
         if (on && own) publish(p.ends + at, tb);
-        h = look_back(p.maps + at - p.dim, p.ends + at - p.dim, -p.dim, tile, on && !(EDGES && (rows.first[0] & 1)));
+        h = look_back<4>(p.maps + at + step, p.ends + at + step, step, tile.before, on && !(EDGES && (rows.first[0] & 1)));
         if (on && !own) publish(p.ends + at, fmaf(ta, h, tb));
       }
       entering[c] = h;
@@ -496,10 +541,13 @@ __global__ __launch_bounds__(kGatedThreads) void gated_scan_kernel(const GatedAr
         }
       }
       static_assert(kGatedSave % R == 0, "a checkpoint is the state after a part");
-      if (p.ckpt && (at0 + R + tile0) % kGatedSave == 0 && tile0 + at0 + R <= p.total) {
-        Run<false, V> out;
-        out.set(h);
-        out.store(p.ckpt, (tile0 + at0) / kGatedSave * p.dim + d);
+      if (p.ckpt) {
+        const int64_t row = checkpoint_after(p, tile, tile0 + at0 + R);
+        if (row >= 0) {
+          Run<false, V> out;
+          out.set(h);
+          out.store(p.ckpt, row * p.dim + d);
+        }
       }
     }
   };
@@ -525,7 +573,7 @@ __device__ __forceinline__ Run<false, V> batch_state(const void* states, int32_t
 }
 
 template <bool BF16, bool Z, int V, int R>
-__global__ __launch_bounds__(kGatedThreads) void gated_scan_bwd_kernel(const GatedArgs p) {
+__global__ __launch_bounds__(kGatedThreads, 3) void gated_scan_bwd_kernel(const GatedArgs p) {
   using S = GatedShape<V, R>;
   static_assert(S::kRows == kGatedSave, "a tile begins behind a checkpoint");
   __shared__ TileRows<S::kRows> rows;
@@ -535,14 +583,13 @@ __global__ __launch_bounds__(kGatedThreads) void gated_scan_bwd_kernel(const Gat
   __shared__ float rate[kGatedChannels];
   __shared__ float starts[S::kRows][kGatedChannels];  // where a sequence begins: its initial state, then that one's gradient
   __shared__ uint32_t ticket;
-  const uint32_t n = take_ticket(p, &ticket);
-  const uint32_t turn = n / static_cast<uint32_t>(p.chains), tile = static_cast<uint32_t>(p.tiles) - 1u - turn;
-  const Channels<V> ch(n - turn * static_cast<uint32_t>(p.chains), p.dim);
+  const Turn tile = Turn::take<S::kRows>(p, &ticket, true);
+  const Channels<V> ch(tile.block, p.dim);
   const int lane = threadIdx.x % S::kLanes, part = threadIdx.x / S::kLanes, at0 = part * R, wave = threadIdx.x / 64;
-  const int64_t tile0 = static_cast<int64_t>(tile) * S::kRows, d = ch.of(lane);
+  const int64_t tile0 = tile.row0, d = ch.of(lane);
 
   const float param = p.param[ch.of(threadIdx.x % kGatedChannels / V) + threadIdx.x % V];
-  find_rows(rows, p, static_cast<uint32_t>(tile0));
+  find_rows(rows, p, static_cast<uint32_t>(tile0), tile.end);
   float se[V], sa[V], sx[V];  // sums over the lane's rows
 #pragma unroll
   for (int v = 0; v < V; ++v) se[v] = sa[v] = sx[v] = 0.0f;
@@ -550,11 +597,11 @@ __global__ __launch_bounds__(kGatedThreads) void gated_scan_bwd_kernel(const Gat
   auto body = [&](auto edges) {
     constexpr bool EDGES = decltype(edges)::value;
     Run<BF16, V> x[R], ag[R], xg[R], z[R], dy[R];
-    load_rows<!EDGES>(ag, p.ag, p.dim, tile0, at0, d, p.total);
-    load_rows<!EDGES>(xg, p.xg, p.dim, tile0, at0, d, p.total);
-    load_rows<!EDGES>(x, p.x, p.dim, tile0, at0, d, p.total);
-    if constexpr (Z) load_rows<!EDGES>(z, p.z, p.dim, tile0, at0, d, p.total);
-    load_rows<!EDGES>(dy, p.dy, p.dim, tile0, at0, d, p.total);
+    load_rows<!EDGES>(ag, p.ag, p.dim, tile0, at0, d, tile.end);
+    load_rows<!EDGES>(xg, p.xg, p.dim, tile0, at0, d, tile.end);
+    load_rows<!EDGES>(x, p.x, p.dim, tile0, at0, d, tile.end);
+    if constexpr (Z) load_rows<!EDGES>(z, p.z, p.dim, tile0, at0, d, tile.end);
+    load_rows<!EDGES>(dy, p.dy, p.dim, tile0, at0, d, tile.end);
     float ab[V], xb[V], k[V];
     load_bias<V>(p.ab, d, ab);
     load_bias<V>(p.xb, d, xb);
@@ -653,7 +700,8 @@ __global__ __launch_bounds__(kGatedThreads) void gated_scan_bwd_kernel(const Gat
         pb[q] = wave == 0 ? fwd.b[q][c] : back[q][c];
       }
       if (wave == 0) {
-        float s = tile > 0 ? p.ckpt[(tile - 1) * p.dim + dc] : 0.0f;
+        const int64_t saved = checkpoint_after(p, tile, tile0);
+        float s = saved >= 0 ? p.ckpt[saved * p.dim + dc] : 0.0f;
 #pragma unroll
         for (int q = 0; q < S::kParts; ++q) {
           fwd.b[q][c] = s;
@@ -671,10 +719,10 @@ __global__ __launch_bounds__(kGatedThreads) void gated_scan_bwd_kernel(const Gat
         }
         float s = 0.0f;
         if (p.ticket) {
-          const int64_t at = tile * p.dim + dc;
+          const int64_t at = tile.turn * p.dim + dc, step = -(tile.apart * p.dim);
           if (on && !own) publish(p.maps + at, ta, tb);
           if (on && own) publish(p.ends + at, tb);
-          s = look_back(p.maps + at + p.dim, p.ends + at + p.dim, p.dim, turn, on && !(EDGES && (rows.last[0] >> 63)));
+          s = look_back<2>(p.maps + at + step, p.ends + at + step, step, tile.before, on && !(EDGES && (rows.last[0] >> 63)));
           if (on && !own) publish(p.ends + at, fmaf(ta, s, tb));
         }
 #pragma unroll
@@ -777,7 +825,7 @@ __global__ __launch_bounds__(kGatedThreads) void gated_scan_bwd_kernel(const Gat
     float s = 0.0f;
 #pragma unroll
     for (int q = 0; q < S::kParts; ++q) s += wave == 0 ? fwd.a[q][c] : wave == 1 ? fwd.b[q][c] : back[q][c];
-    if (ch.has(c / V)) p.partial[(static_cast<int64_t>(tile) * 3 + wave) * p.dim + ch.of(c / V) + c % V] = s;
+    if (ch.has(c / V)) p.partial[(static_cast<int64_t>(tile.turn) * 3 + wave) * p.dim + ch.of(c / V) + c % V] = s;
   }
 }
 
