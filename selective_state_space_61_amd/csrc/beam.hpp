@@ -19,7 +19,6 @@ namespace ssm {
 
 constexpr int kBeamThreads = 256;
 constexpr int kBeamMost = 64;   // beams, and rows of a sequence
-constexpr int kBeamValues = 32;  // values of a lane
 
 struct BeamArgs {
   const void* logits;
@@ -29,7 +28,7 @@ struct BeamArgs {
   int32_t rows, beams, eos;
   int64_t batch, vocab;
   int32_t chunks, blocks;   // stretches of a row, 16-byte blocks of a stretch
-  uint64_t* best;           // (batch * rows, chunks, beams): key and token, largest first
+  uint64_t* best;           // (batch * rows, beams, chunks): key and token, a stretch's largest first
   float* stats;             // (batch * rows, chunks, 2): largest logit, sum of exp(logit - it)
   int32_t *parents, *tokens;
   float* out_scores;
@@ -66,9 +65,25 @@ __device__ __forceinline__ uint32_t kth_key(uint32_t key, int k) {
   uint32_t t = bit == 31 ? 0u : hi >> (bit + 1) << (bit + 1);
   for (; bit >= 12; --bit) {  // (11 bits of the mantissa: the few values more do not matter)
     const uint32_t c = t | (1u << bit);
-    if (__popcll(__ballot(key >= c)) >= k) t = c;
+    const int reach = __popcll(__ballot(key >= c));
+    if (reach >= k) t = c;
+    if (reach == k) break;
   }
   return t;
+}
+
+// Appends the words of the lanes in `on` to a wave's list of at most 64, `count` of which are there
+__device__ __forceinline__ void append(uint64_t* list, int& count, uint64_t on, uint64_t word) {
+  const int lane = threadIdx.x & 63;
+  const int at = count + __builtin_amdgcn_mbcnt_hi(static_cast<uint32_t>(on >> 32),
+                                                   __builtin_amdgcn_mbcnt_lo(static_cast<uint32_t>(on), 0));
+  if ((on >> lane & 1) && at < 64) list[at] = word;
+  count += __popcll(on);
+}
+// A wave's LDS writes before its reads
+__device__ __forceinline__ void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
 }
 
 // Rank of a lane's word among those of the first n lanes (no two of which are equal)
@@ -84,44 +99,44 @@ __device__ __forceinline__ int rank_of(uint64_t w, int n) {
 
 __device__ __forceinline__ bool is_finite(float v) { return __builtin_isfinite(v); }
 
-template <bool BF16>
+// VALUES of a row a lane.
+template <bool BF16, int VALUES>
 __global__ __launch_bounds__(kBeamThreads) void beam_rows_kernel(const BeamArgs p) {
-  constexpr int EPB = BF16 ? 8 : 4, IT = kBeamValues / EPB, ES = BF16 ? 2 : 4;
+  constexpr int EPB = BF16 ? 8 : 4, IT = VALUES / EPB, ES = BF16 ? 2 : 4;
   __shared__ uint64_t lists[kBeamThreads / 64][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t n = static_cast<int64_t>(blockIdx.x) * (kBeamThreads / 64) + wave;
-  const int64_t row = n / p.chunks;
-  const int chunk = static_cast<int>(n - row * p.chunks);
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const uint32_t n = blockIdx.x * (kBeamThreads / 64) + wave;
+  const uint32_t row = n / static_cast<uint32_t>(p.chunks), chunk = n - row * static_cast<uint32_t>(p.chunks);
   if (row >= p.batch * p.rows) return;
   // what a finished or dead row holds does not matter
   if (!is_finite(p.scores[row]) || (p.finished && p.finished[row])) return;
-  const int64_t seq = row / p.rows;
-  const char* base = static_cast<const char*>(p.logits) + (seq * p.sb + (row - seq * p.rows) * p.sr) * ES;
+  const uint32_t seq = row / static_cast<uint32_t>(p.rows);
+  const char* base = static_cast<const char*>(p.logits) + (seq * p.sb + (row - seq * static_cast<uint32_t>(p.rows)) * p.sr) * ES;
   // Blocks of 16 bytes by token, at whatever alignment the row has (gfx950 takes wide loads at any), so that
   // rows of the same values have the same sums, and tie.
-  const int64_t block0 = static_cast<int64_t>(chunk) * p.blocks;
+  const uint32_t token0 = chunk * static_cast<uint32_t>(p.blocks) * EPB;  // of the stretch
+  const uint32_t vocab = static_cast<uint32_t>(p.vocab);
+  // its values: of a vocabulary of very many stretches the last ones may have none
+  const uint32_t rest = vocab > token0 ? vocab - token0 : 0u, most = static_cast<uint32_t>(p.blocks) * EPB;
+  const uint32_t left = rest < most ? rest : most;
+  base += static_cast<int64_t>(token0) * ES;
   uint32_t raw[IT][4];
-  uint32_t live = 0;  // blocks that hold values of the row
 #pragma unroll
   for (int i = 0; i < IT; ++i) {
-    const int at = i * 64 + lane;
-    const int64_t first = (block0 + at) * EPB;  // the block's first token
+    const uint32_t first = (i * 64 + lane) * EPB;
     raw[i][0] = raw[i][1] = raw[i][2] = raw[i][3] = BF16 ? 0xff80ff80u : 0xff800000u;  // -inf
-    if (at < p.blocks && first < p.vocab) {
-      live |= 1u << i;
-      if (first + EPB <= p.vocab) {
-        const U32x4 v = *reinterpret_cast<const typename Words<ES>::U4*>(base + first * ES);
-        raw[i][0] = v.x; raw[i][1] = v.y; raw[i][2] = v.z; raw[i][3] = v.w;
-      } else {
+    if (first + EPB <= left) {
+      const U32x4 v = *reinterpret_cast<const typename Words<ES>::U4*>(base + first * ES);
+      raw[i][0] = v.x; raw[i][1] = v.y; raw[i][2] = v.z; raw[i][3] = v.w;
+    } else if (first < left) {
 #pragma unroll
-        for (int e = 0; e < EPB; ++e) {
-          if (first + e >= p.vocab) continue;
-          if constexpr (BF16) {
-            const uint32_t h = reinterpret_cast<const uint16_t*>(base)[first + e];
-            raw[i][e >> 1] = e & 1 ? (raw[i][e >> 1] & 0xffffu) | h << 16 : (raw[i][e >> 1] & 0xffff0000u) | h;
-          } else {
-            raw[i][e] = reinterpret_cast<const uint32_t*>(base)[first + e];
-          }
+      for (int e = 0; e < EPB; ++e) {
+        if (first + e >= left) continue;
+        if constexpr (BF16) {
+          const uint32_t h = reinterpret_cast<const uint16_t*>(base)[first + e];
+          raw[i][e >> 1] = e & 1 ? (raw[i][e >> 1] & 0xffffu) | h << 16 : (raw[i][e >> 1] & 0xffff0000u) | h;
+        } else {
+          raw[i][e] = reinterpret_cast<const uint32_t*>(base)[first + e];
         }
       }
     }
@@ -135,74 +150,68 @@ __global__ __launch_bounds__(kBeamThreads) void beam_rows_kernel(const BeamArgs 
   for (int i = 0; i < IT; ++i)
 #pragma unroll
     for (int e = 0; e < EPB; ++e) top = fmaxf(top, value(i, e));
-  const uint32_t key = live ? beam_key(top) : 0u;
+  const uint32_t key = static_cast<uint32_t>(lane * EPB) < left ? beam_key(top) : 0u;
   const float m = group_reduce<64>(top, [](float a, float b) { return fmaxf(a, b); });
   const float shift = m == -INFINITY ? 0.0f : m;  // (NaN and +inf leave a NaN in the sum)
   float s = 0.0f;
 #pragma unroll
   for (int i = 0; i < IT; ++i)
 #pragma unroll
-    for (int e = 0; e < EPB; ++e) s += hw_exp2((value(i, e) - shift) * kLog2e);
+    for (int e = 0; e < EPB; ++e) s += hw_exp2((value(i, e) - shift) * kLog2e);  // (fused, a large shift's rounding would scale them all)
   s = group_sum<64>(s);
   if (lane == 0) {
-    p.stats[2 * n] = m;
-    p.stats[2 * n + 1] = s;
+    p.stats[2 * static_cast<int64_t>(n)] = m;
+    p.stats[2 * static_cast<int64_t>(n) + 1] = s;
   }
 
   const int k = p.beams;
-  const uint32_t bound = kth_key(key, k);
+  const uint32_t reach = kth_key(key, k);
+  const float bound = reach >= 0x00800000u ? beam_logit(reach) : -INFINITY;  // (keys below are those of -inf and of no value)
   uint64_t* list = lists[wave];
   int count = 0;
 #pragma unroll
-  for (int i = 0; i < IT; ++i) {
-    const int64_t first = (block0 + i * 64 + lane) * EPB;
+  for (int i = 0; i < IT; ++i)
 #pragma unroll
     for (int e = 0; e < EPB; ++e) {
-      const uint32_t ke = beam_key(value(i, e));
-      const uint64_t on = __ballot((live >> i & 1) && ke >= bound && first + e < p.vocab);
-      if (on) {
-        const int at = count + __builtin_amdgcn_mbcnt_hi(static_cast<uint32_t>(on >> 32),
-                                                         __builtin_amdgcn_mbcnt_lo(static_cast<uint32_t>(on), 0));
-        if ((on >> lane & 1) && at < 64) list[at] = beam_word(ke, static_cast<uint32_t>(first + e));
-        count += __popcll(on);
-      }
+      const uint32_t at = (i * 64 + lane) * EPB + e;
+      const uint64_t on = __ballot(value(i, e) >= bound);
+      if (on) append(list, count, on & __ballot(at < left), beam_word(beam_key(value(i, e)), token0 + at));
     }
-  }
-  uint64_t* out = p.best + n * k;
+  uint64_t* out = p.best + static_cast<int64_t>(row) * k * p.chunks + chunk;
   if (count <= 64) {
-    // the wave's own LDS: its writes are done before its reads
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-    __builtin_amdgcn_wave_barrier();
+    wave_sync();
     const uint64_t w = lane < count ? list[lane] : 0u;
     const int rank = rank_of(w, count);
-    if (lane < count && rank < k) out[rank] = w;
-    if (lane >= count && lane < k) out[lane] = 0u;  // fewer values than beams
+    if (lane < count && rank < k) out[rank * p.chunks] = w;
+    if (lane >= count && lane < k) out[lane * p.chunks] = 0u;  // fewer values than beams
     return;
   }
   uint64_t last = ~0ull;
   for (int r = 0; r < k; ++r) {
     uint64_t best = 0u;
 #pragma unroll
-    for (int i = 0; i < IT; ++i) {
-      const int64_t first = (block0 + i * 64 + lane) * EPB;
+    for (int i = 0; i < IT; ++i)
 #pragma unroll
       for (int e = 0; e < EPB; ++e) {
-        const uint64_t w = beam_word(beam_key(value(i, e)), static_cast<uint32_t>(first + e));
-        if ((live >> i & 1) && first + e < p.vocab && w < last && w > best) best = w;
+        const uint32_t at = (i * 64 + lane) * EPB + e;
+        const uint64_t w = beam_word(beam_key(value(i, e)), token0 + at);
+        if (at < left && w < last && w > best) best = w;
       }
-    }
     last = wave_max(best);
-    if (lane == 0) out[r] = last;
+    if (lane == 0) out[r * p.chunks] = last;
     if (last == 0u) last = 1u;  // none left: the rest is 0 too
   }
 }
 
-// One sequence a workgroup.
+// One sequence a workgroup: a wave joins a row's stretches, then all rank the rows' candidates.
 __global__ __launch_bounds__(1024) static void beam_join_kernel(const BeamArgs p) {
   __shared__ double values[kBeamMost * kBeamMost];
   __shared__ int32_t tokens[kBeamMost * kBeamMost];
-  __shared__ uint64_t lists[16][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
+  __shared__ union {
+    uint64_t lists[16][64];              // of the waves, while they join rows
+    int32_t ranks[kBeamMost * kBeamMost];  // after that
+  } room;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
   const int k = static_cast<int>(p.vocab < p.beams ? p.vocab : p.beams);  // candidates of a row
   const int64_t seq = blockIdx.x;
   for (int j = wave; j < p.rows; j += waves) {
@@ -211,8 +220,14 @@ __global__ __launch_bounds__(1024) static void beam_join_kernel(const BeamArgs p
     const bool done = p.finished && p.finished[row];
     double lse = 0.0;
     bool dead = !is_finite(score);
-    uint64_t* list = lists[wave];
+    uint64_t* list = room.lists[wave];
+    const uint64_t* best = p.best + row * p.beams * p.chunks;
+    // A stretch's words fall, so its first says whether the others matter: the first four of 64 stretches at once.
+    constexpr int kAhead = 4;
+    uint64_t head[kAhead], top = 0u;
     if (!dead && !done) {
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) head[i] = i < k && lane < p.chunks ? best[static_cast<int64_t>(i) * p.chunks + lane] : 0u;
       const float* st = p.stats + 2 * row * p.chunks;
       float m = -INFINITY;
       for (int c = lane; c < p.chunks; c += 64) m = fmaxf(m, st[2 * c]);
@@ -238,36 +253,40 @@ __global__ __launch_bounds__(1024) static void beam_join_kernel(const BeamArgs p
       }
       continue;
     }
-    const uint64_t* best = p.best + row * p.chunks * p.beams;
-    const int n = p.chunks * p.beams;
-    uint64_t top = 0u;
-    for (int i = lane; i < n; i += 64) top = best[i] > top ? best[i] : top;
+    top = head[0];
+    for (int c = lane + 64; c < p.chunks; c += 64) top = best[c] > top ? best[c] : top;
     const uint32_t bound = kth_key(static_cast<uint32_t>(top >> 32), k);
     int count = 0;
-    for (int i = lane; i - lane < n; i += 64) {
-      const uint64_t w = i < n ? best[i] : 0u;
-      const uint64_t on = __ballot(w != 0u && static_cast<uint32_t>(w >> 32) >= bound);
-      const int at = count + __builtin_amdgcn_mbcnt_hi(static_cast<uint32_t>(on >> 32),
-                                                       __builtin_amdgcn_mbcnt_lo(static_cast<uint32_t>(on), 0));
-      if ((on >> lane & 1) && at < 64) list[at] = w;
-      count += __popcll(on);
+    for (int c0 = 0; c0 < p.chunks; c0 += 64) {
+      for (int i0 = 0; i0 < k; i0 += kAhead) {
+        if (c0 > 0 || i0 > 0) {
+#pragma unroll
+          for (int i = 0; i < kAhead; ++i)
+            head[i] = i0 + i < k && c0 + lane < p.chunks ? best[static_cast<int64_t>(i0 + i) * p.chunks + c0 + lane] : 0u;
+        }
+        uint64_t on = 0u;
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+          on = __ballot(head[i] != 0u && static_cast<uint32_t>(head[i] >> 32) >= bound);
+          if (on) append(list, count, on, head[i]);
+        }
+        if (!on) break;  // what follows is smaller
+      }
     }
     uint64_t mine = 0u;  // the lane-th largest
     if (count <= 64) {
-      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-      __builtin_amdgcn_wave_barrier();
+      wave_sync();
       const uint64_t w = lane < count ? list[lane] : 0u;
       const int rank = rank_of(w, count);
-      __builtin_amdgcn_wave_barrier();
+      wave_sync();
       if (lane < count) list[rank] = w;
-      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-      __builtin_amdgcn_wave_barrier();
+      wave_sync();
       mine = lane < k ? list[lane] : 0u;
     } else {
       uint64_t last = ~0ull;
       for (int r = 0; r < k; ++r) {
         uint64_t b = 0u;
-        for (int i = lane; i < n; i += 64) {
+        for (int64_t i = lane; i < static_cast<int64_t>(p.chunks) * p.beams; i += 64) {
           const uint64_t w = best[i];
           if (w < last && w > b) b = w;
         }
@@ -275,44 +294,51 @@ __global__ __launch_bounds__(1024) static void beam_join_kernel(const BeamArgs p
         if (lane == r) mine = last;
       }
     }
-    // by value now: logits that differ may give one value, which then goes by the token
     const double v = score + (static_cast<double>(beam_logit(static_cast<uint32_t>(mine >> 32))) - lse);
     const int32_t t = static_cast<int32_t>(0xffffffffu - static_cast<uint32_t>(mine));
-    int rank = 0;
-    for (int i = 0; i < k; ++i) {
-      const double o = __shfl(v, i);
-      const int32_t u = __shfl(t, i);
-      rank += o > v || (o == v && u < t);
+    int rank = lane;
+    // by value now: logits that differ may give one value, which then goes by the token
+    const bool tie = lane > 0 && lane < k && __shfl_up(v, 1) == v;
+    if (__any(tie)) {
+      rank = 0;
+      for (int i = 0; i < k; ++i) {
+        const double o = __shfl(v, i);
+        const int32_t u = __shfl(t, i);
+        rank += o > v || (o == v && u < t);
+      }
     }
     if (lane < k) {
       values[j * k + rank] = v;
       tokens[j * k + rank] = t;
     }
   }
+  int32_t* ranks = room.ranks;
   __syncthreads();
-  // each candidate's rank: its place in its own row, and how many of every other row come before it
-  for (int i = threadIdx.x; i < p.rows * k; i += blockDim.x) {
-    const int j = i / k;
+  for (int i = threadIdx.x; i < p.rows * k; i += blockDim.x) ranks[i] = i % k;  // its place in its own row
+  __syncthreads();
+  // how many of every other row come before each candidate: a pair of them and a row a thread
+  for (int q = threadIdx.x; q < p.rows * k * p.rows; q += blockDim.x) {
+    const int i = q / p.rows, o = q - i * p.rows, j = i / k;
+    if (o == j) continue;
     const double v = values[i];
-    int rank = i - j * k;
-    for (int o = 0; o < p.rows && rank < p.beams; ++o) {
-      if (o == j) continue;
-      int lo = 0, hi = k;  // the first that does not come before (rows above win ties)
-      while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        const double w = values[o * k + mid];
-        if (w > v || (w == v && o < j)) lo = mid + 1;
-        else hi = mid;
-      }
-      rank += lo;
+    int lo = 0, hi = k;  // the first that does not come before (rows above win ties)
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      const double w = values[o * k + mid];
+      if (w > v || (w == v && o < j)) lo = mid + 1;
+      else hi = mid;
     }
-    if (rank < p.beams) {
-      const int64_t at = seq * p.beams + rank;
-      p.parents[at] = j;
-      p.tokens[at] = tokens[i];
-      p.out_scores[at] = static_cast<float>(v);
-      if (p.out_finished) p.out_finished[at] = p.finished[seq * p.rows + j] || tokens[i] == p.eos;
-    }
+    if (lo) atomicAdd(&ranks[i], lo);
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < p.rows * k; i += blockDim.x) {
+    if (ranks[i] >= p.beams) continue;
+    const int j = i / k;
+    const int64_t at = seq * p.beams + ranks[i];
+    p.parents[at] = j;
+    p.tokens[at] = tokens[i];
+    p.out_scores[at] = static_cast<float>(values[i]);
+    if (p.out_finished) p.out_finished[at] = p.finished[seq * p.rows + j] || tokens[i] == p.eos;
   }
 }
 

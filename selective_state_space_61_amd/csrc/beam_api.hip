@@ -10,19 +10,21 @@ using namespace ssm_host;
 
 namespace {
 
-// How a row is cut: into stretches of at most 64 lanes x kBeamValues values, all about as long.
+// How a row is cut: into stretches of at most 64 lanes x `values` values, all about as long.
 struct BeamShape {
-  int64_t chunks, blocks, bytes;
+  int64_t values, chunks, blocks, bytes;
 };
 
 ssm_status_t beam_shape(int64_t batch, int64_t rows, int64_t vocab, int64_t beams, bool bf16, BeamShape* out) {
-  const int64_t epb = bf16 ? 8 : 4, wave = 64 * (ssm::kBeamValues / epb);
-  const int64_t blocks = (vocab + epb - 1) / epb;
+  const int64_t epb = bf16 ? 8 : 4, blocks = (vocab + epb - 1) / epb;
+  out->values = 32;
+  const int64_t wave = 64 * (out->values / epb);
   out->chunks = (blocks + wave - 1) / wave;
   out->blocks = (blocks + out->chunks - 1) / out->chunks;
   int64_t n;
   if (!mul_ok(batch * rows, out->chunks, &n) || !mul_ok(n, 8 * (beams + 1), &out->bytes))
     return fail(SSM_ERR_INVALID_ARG, "workspace size overflows int64");
+  if (n > kMaxIndex) return fail(SSM_ERR_UNSUPPORTED, "grid too large");
   return SSM_OK;
 }
 
@@ -107,10 +109,8 @@ ssm_status_t ssm_beam_select(int64_t batch, int64_t rows, int64_t vocab, int64_t
   hipStream_t st = static_cast<hipStream_t>(stream);
   const int64_t waves = batch * rows * s.chunks, blocks = (waves + ssm::kBeamThreads / 64 - 1) / (ssm::kBeamThreads / 64);
   if (blocks > kMaxBlocks || batch > 0xffffffffll / 1024) return fail(SSM_ERR_UNSUPPORTED, "grid too large");
-  if (dtype == SSM_BF16)
-    hipLaunchKernelGGL(ssm::beam_rows_kernel<true>, dim3(static_cast<unsigned>(blocks)), dim3(ssm::kBeamThreads), 0, st, a);
-  else
-    hipLaunchKernelGGL(ssm::beam_rows_kernel<false>, dim3(static_cast<unsigned>(blocks)), dim3(ssm::kBeamThreads), 0, st, a);
+  const auto k = dtype == SSM_BF16 ? ssm::beam_rows_kernel<true, 32> : ssm::beam_rows_kernel<false, 32>;
+  hipLaunchKernelGGL(k, dim3(static_cast<unsigned>(blocks)), dim3(ssm::kBeamThreads), 0, st, a);
   SSM_TRY(check_launch("beam selection (rows)"));
   const unsigned threads = 64u * static_cast<unsigned>(rows < 16 ? rows : 16);
   hipLaunchKernelGGL(ssm::beam_join_kernel, dim3(static_cast<unsigned>(batch)), dim3(threads), 0, st, a);
