@@ -2,15 +2,16 @@
 // reordering of the states that follows it.
 //
 // Selection.  A candidate (j, v) of a sequence has the value score_j + (logit[j, v] - lse_j) with lse_j =
-// log sum_v exp(logit[j, v]); the `beams` largest are taken.  Two launches: every wave takes a stretch
-// of one row into registers, sums exp(logit - its largest) and keeps its largest `beams` logits; then a
+// log sum_v exp(logit[j, v]); the `beams` largest are taken.  Two launches: a workgroup takes a stretch of
+// one row into registers, sums exp(logit - a wave's largest) and keeps its largest `beams` logits; then a
 // workgroup a sequence joins its rows' stretches, adds lse and score in 64 bits (they rank candidates of
 // different rows) and ranks what is left.  Logits are read once.
 //
-// The largest k of a wave's values: the k-th largest of the 64 lanes' largest ones is a bound that at
-// least k values reach and few others do.  It is found bit by bit with a ballot each, what reaches it is
-// gathered (by ballots again) and ranked by comparing all with all.  Where more than 64 values reach
-// it (rows of few different values) the k are found one after another.
+// The largest k of a stretch: its values are taken for 64 columns, of which each lane of the four waves holds a
+// quarter; the k-th largest of the columns' largest values is a bound that at least k values reach and few others
+// do.  It is found bit by bit with a ballot each, what reaches it is gathered (by ballots again) and ranked by
+// comparing all with all.
+// Where more than 64 values reach it (rows of few different values) the k are found one after another.
 #pragma once
 
 #include "cache.hpp"
@@ -18,6 +19,8 @@
 namespace ssm {
 
 constexpr int kBeamThreads = 256;
+constexpr int kBeamWaves = kBeamThreads / 64;
+constexpr int kBeamValues = 32;  // of a row, a lane
 constexpr int kBeamMost = 64;   // beams, and rows of a sequence
 
 struct BeamArgs {
@@ -29,7 +32,7 @@ struct BeamArgs {
   int64_t batch, vocab;
   int32_t chunks, blocks;   // stretches of a row, 16-byte blocks of a stretch
   uint64_t* best;           // (batch * rows, beams, chunks): key and token, a stretch's largest first
-  float* stats;             // (batch * rows, chunks, 2): largest logit, sum of exp(logit - it)
+  float* stats;             // (batch * rows, chunks, waves, 2): largest logit, sum of exp(logit - it)
   int32_t *parents, *tokens;
   float* out_scores;
   uint8_t* out_finished;
@@ -99,15 +102,14 @@ __device__ __forceinline__ int rank_of(uint64_t w, int n) {
 
 __device__ __forceinline__ bool is_finite(float v) { return __builtin_isfinite(v); }
 
-// VALUES of a row a lane.
-template <bool BF16, int VALUES>
+template <bool BF16>
 __global__ __launch_bounds__(kBeamThreads) void beam_rows_kernel(const BeamArgs p) {
-  constexpr int EPB = BF16 ? 8 : 4, IT = VALUES / EPB, ES = BF16 ? 2 : 4;
-  __shared__ uint64_t lists[kBeamThreads / 64][64];
+  constexpr int EPB = BF16 ? 8 : 4, IT = kBeamValues / EPB, ES = BF16 ? 2 : 4;
+  __shared__ uint64_t lists[kBeamWaves][64];
+  __shared__ float tops[kBeamWaves][64];
+  __shared__ int32_t counts[kBeamWaves];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const uint32_t n = blockIdx.x * (kBeamThreads / 64) + wave;
-  const uint32_t row = n / static_cast<uint32_t>(p.chunks), chunk = n - row * static_cast<uint32_t>(p.chunks);
-  if (row >= p.batch * p.rows) return;
+  const uint32_t row = blockIdx.x / static_cast<uint32_t>(p.chunks), chunk = blockIdx.x - row * static_cast<uint32_t>(p.chunks);
   // what a finished or dead row holds does not matter
   if (!is_finite(p.scores[row]) || (p.finished && p.finished[row])) return;
   const uint32_t seq = row / static_cast<uint32_t>(p.rows);
@@ -123,7 +125,7 @@ __global__ __launch_bounds__(kBeamThreads) void beam_rows_kernel(const BeamArgs 
   uint32_t raw[IT][4];
 #pragma unroll
   for (int i = 0; i < IT; ++i) {
-    const uint32_t first = (i * 64 + lane) * EPB;
+    const uint32_t first = (i * kBeamThreads + threadIdx.x) * EPB;
     raw[i][0] = raw[i][1] = raw[i][2] = raw[i][3] = BF16 ? 0xff80ff80u : 0xff800000u;  // -inf
     if (first + EPB <= left) {
       const U32x4 v = *reinterpret_cast<const typename Words<ES>::U4*>(base + first * ES);
@@ -150,42 +152,62 @@ __global__ __launch_bounds__(kBeamThreads) void beam_rows_kernel(const BeamArgs 
   for (int i = 0; i < IT; ++i)
 #pragma unroll
     for (int e = 0; e < EPB; ++e) top = fmaxf(top, value(i, e));
-  const uint32_t key = static_cast<uint32_t>(lane * EPB) < left ? beam_key(top) : 0u;
+  const int k = p.beams;
+  tops[wave][lane] = top;
   const float m = group_reduce<64>(top, [](float a, float b) { return fmaxf(a, b); });
   const float shift = m == -INFINITY ? 0.0f : m;  // (NaN and +inf leave a NaN in the sum)
   float s = 0.0f;
 #pragma unroll
   for (int i = 0; i < IT; ++i)
 #pragma unroll
-    for (int e = 0; e < EPB; ++e) s += hw_exp2((value(i, e) - shift) * kLog2e);  // (fused, a large shift's rounding would scale them all)
+    for (int e = 0; e < EPB; ++e)
+      s += hw_exp2((value(i, e) - shift) * kLog2e);  // (fused, a large shift's rounding would scale them all)
   s = group_sum<64>(s);
   if (lane == 0) {
-    p.stats[2 * static_cast<int64_t>(n)] = m;
-    p.stats[2 * static_cast<int64_t>(n) + 1] = s;
+    float* st = p.stats + 2 * (static_cast<int64_t>(blockIdx.x) * kBeamWaves + wave);
+    st[0] = m;
+    st[1] = s;
   }
+  __syncthreads();
 
-  const int k = p.beams;
-  const uint32_t reach = kth_key(key, k);
+  top = tops[0][lane];
+#pragma unroll
+  for (int i = 1; i < kBeamWaves; ++i) top = fmaxf(top, tops[i][lane]);
+  // (the first wave has the first blocks: its lanes without a value are those of columns without one)
+  const uint32_t reach = kth_key(lane * EPB < left ? beam_key(top) : 0u, k);
   const float bound = reach >= 0x00800000u ? beam_logit(reach) : -INFINITY;  // (keys below are those of -inf and of no value)
-  uint64_t* list = lists[wave];
   int count = 0;
 #pragma unroll
   for (int i = 0; i < IT; ++i)
 #pragma unroll
     for (int e = 0; e < EPB; ++e) {
-      const uint32_t at = (i * 64 + lane) * EPB + e;
+      const uint32_t at = (i * kBeamThreads + threadIdx.x) * EPB + e;
       const uint64_t on = __ballot(value(i, e) >= bound);
-      if (on) append(list, count, on & __ballot(at < left), beam_word(beam_key(value(i, e)), token0 + at));
+      if (on) append(lists[wave], count, on & __ballot(at < left), beam_word(beam_key(value(i, e)), token0 + at));
     }
+  if (lane == 0) counts[wave] = count;
+  __syncthreads();
+
   uint64_t* out = p.best + static_cast<int64_t>(row) * k * p.chunks + chunk;
-  if (count <= 64) {
-    wave_sync();
-    const uint64_t w = lane < count ? list[lane] : 0u;
-    const int rank = rank_of(w, count);
-    if (lane < count && rank < k) out[rank * p.chunks] = w;
-    if (lane >= count && lane < k) out[lane * p.chunks] = 0u;  // fewer values than beams
+  int all = 0, before[kBeamWaves];
+#pragma unroll
+  for (int i = 0; i < kBeamWaves; ++i) {
+    before[i] = all;
+    all += counts[i];
+  }
+  all = __builtin_amdgcn_readfirstlane(all);
+  if (all <= 64) {
+    if (wave > 0) return;
+    uint64_t w = 0u;
+#pragma unroll
+    for (int i = 0; i < kBeamWaves; ++i)
+      if (lane >= before[i] && lane < before[i] + counts[i]) w = lists[i][lane - before[i]];
+    const int rank = rank_of(w, all);
+    if (lane < all && rank < k) out[rank * p.chunks] = w;
+    if (lane >= all && lane < k) out[lane * p.chunks] = 0u;  // fewer values than beams
     return;
   }
+  // each wave's largest one after another, then those of all four
   uint64_t last = ~0ull;
   for (int r = 0; r < k; ++r) {
     uint64_t best = 0u;
@@ -193,48 +215,69 @@ __global__ __launch_bounds__(kBeamThreads) void beam_rows_kernel(const BeamArgs 
     for (int i = 0; i < IT; ++i)
 #pragma unroll
       for (int e = 0; e < EPB; ++e) {
-        const uint32_t at = (i * 64 + lane) * EPB + e;
+        const uint32_t at = (i * kBeamThreads + threadIdx.x) * EPB + e;
         const uint64_t w = beam_word(beam_key(value(i, e)), token0 + at);
         if (at < left && w < last && w > best) best = w;
       }
     last = wave_max(best);
-    if (lane == 0) out[r * p.chunks] = last;
+    if (lane == 0) lists[wave][r] = last;
     if (last == 0u) last = 1u;  // none left: the rest is 0 too
+  }
+  __syncthreads();
+  if (wave > 0) return;
+  uint64_t words[kBeamWaves];
+#pragma unroll
+  for (int i = 0; i < kBeamWaves; ++i) words[i] = lane < k ? lists[i][lane] : 0u;
+  last = ~0ull;
+  for (int r = 0; r < k; ++r) {
+    uint64_t best = 0u;
+#pragma unroll
+    for (int i = 0; i < kBeamWaves; ++i)
+      if (words[i] < last && words[i] > best) best = words[i];
+    last = wave_max(best);
+    if (lane == 0) out[r * p.chunks] = last;
+    if (last == 0u) last = 1u;
   }
 }
 
 // One sequence a workgroup: a wave joins a row's stretches, then all rank the rows' candidates.
 __global__ __launch_bounds__(1024) static void beam_join_kernel(const BeamArgs p) {
-  __shared__ double values[kBeamMost * kBeamMost];
+  __shared__ double values[kBeamMost * kBeamMost];  // of row j from j << shift on
   __shared__ int32_t tokens[kBeamMost * kBeamMost];
   __shared__ union {
-    uint64_t lists[16][64];              // of the waves, while they join rows
+    uint64_t lists[16][64];                // of the waves, while they join rows
     int32_t ranks[kBeamMost * kBeamMost];  // after that
   } room;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
   const int k = static_cast<int>(p.vocab < p.beams ? p.vocab : p.beams);  // candidates of a row
+  const int shift = k > 1 ? 32 - __builtin_clz(k - 1) : 0;
   const int64_t seq = blockIdx.x;
   for (int j = wave; j < p.rows; j += waves) {
     const int64_t row = seq * p.rows + j;
+    const uint64_t* best = p.best + row * p.beams * p.chunks;
+    const float* st = p.stats + 2 * row * p.chunks * kBeamWaves;
+    const int sums = p.chunks * kBeamWaves;
+    // The words by rank (all stretches' largest, then all second ones): the first 256, before it is known whether
+    // the row counts.
+    const int64_t n = static_cast<int64_t>(p.chunks) * k;
+    constexpr int kAhead = 4;
+    uint64_t word[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) word[i] = i * 64 + lane < n ? best[i * 64 + lane] : 0u;
+    float m = -INFINITY, m0 = -INFINITY, s0 = 0.0f;
+    if (lane < sums) m0 = st[2 * lane], s0 = st[2 * lane + 1];
     const float score = p.scores[row];
     const bool done = p.finished && p.finished[row];
     double lse = 0.0;
     bool dead = !is_finite(score);
     uint64_t* list = room.lists[wave];
-    const uint64_t* best = p.best + row * p.beams * p.chunks;
-    // A stretch's words fall, so its first says whether the others matter: the first four of 64 stretches at once.
-    constexpr int kAhead = 4;
-    uint64_t head[kAhead], top = 0u;
     if (!dead && !done) {
-#pragma unroll
-      for (int i = 0; i < kAhead; ++i) head[i] = i < k && lane < p.chunks ? best[static_cast<int64_t>(i) * p.chunks + lane] : 0u;
-      const float* st = p.stats + 2 * row * p.chunks;
-      float m = -INFINITY;
-      for (int c = lane; c < p.chunks; c += 64) m = fmaxf(m, st[2 * c]);
+      m = m0;
+      for (int c = lane + 64; c < sums; c += 64) m = fmaxf(m, st[2 * c]);
       m = group_reduce<64>(m, [](float a, float b) { return fmaxf(a, b); });
-      double s = 0.0;
-      for (int c = lane; c < p.chunks; c += 64)
-        s += st[2 * c + 1] * static_cast<double>(st[2 * c] == m ? 1.0f : hw_exp2((st[2 * c] - m) * kLog2e));
+      auto share = [&](float mc, float sc) { return sc * static_cast<double>(mc == m ? 1.0f : hw_exp2((mc - m) * kLog2e)); };
+      double s = share(m0, s0);
+      for (int c = lane + 64; c < sums; c += 64) s += share(st[2 * c], st[2 * c + 1]);
       for (int o = 32; o; o >>= 1) s += __shfl_xor(s, o);
       lse = m + log(s);
       dead = !is_finite(m) || !(s > 0.0) || !__builtin_isfinite(lse);
@@ -248,29 +291,26 @@ __global__ __launch_bounds__(1024) static void beam_join_kernel(const BeamArgs p
           t = lane == 0 ? p.eos : (lane <= p.eos ? lane - 1 : lane);
           if (lane == 0) v = score;
         }
-        values[j * k + lane] = v;
-        tokens[j * k + lane] = t;
+        values[(j << shift) + lane] = v;
+        tokens[(j << shift) + lane] = t;
       }
       continue;
     }
-    top = head[0];
-    for (int c = lane + 64; c < p.chunks; c += 64) top = best[c] > top ? best[c] : top;
+    uint64_t top = word[0];
+#pragma unroll
+    for (int i = 1; i < kAhead; ++i) top = word[i] > top ? word[i] : top;
     const uint32_t bound = kth_key(static_cast<uint32_t>(top >> 32), k);
-    int count = 0;
-    for (int c0 = 0; c0 < p.chunks; c0 += 64) {
-      for (int i0 = 0; i0 < k; i0 += kAhead) {
-        if (c0 > 0 || i0 > 0) {
+    int count = 0, quiet = 0;  // words since the last that reaches the bound: a whole rank of them, and none follows
+    for (int64_t i0 = 0; i0 < n && quiet < p.chunks; i0 += 64 * kAhead) {
+      if (i0 > 0) {
 #pragma unroll
-          for (int i = 0; i < kAhead; ++i)
-            head[i] = i0 + i < k && c0 + lane < p.chunks ? best[static_cast<int64_t>(i0 + i) * p.chunks + c0 + lane] : 0u;
-        }
-        uint64_t on = 0u;
+        for (int i = 0; i < kAhead; ++i) word[i] = i0 + i * 64 + lane < n ? best[i0 + i * 64 + lane] : 0u;
+      }
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
-          on = __ballot(head[i] != 0u && static_cast<uint32_t>(head[i] >> 32) >= bound);
-          if (on) append(list, count, on, head[i]);
-        }
-        if (!on) break;  // what follows is smaller
+      for (int i = 0; i < kAhead; ++i) {
+        const uint64_t on = __ballot(word[i] != 0u && static_cast<uint32_t>(word[i] >> 32) >= bound);
+        quiet = on ? 0 : quiet + 64;
+        if (on) append(list, count, on, word[i]);
       }
     }
     uint64_t mine = 0u;  // the lane-th largest
@@ -286,7 +326,7 @@ __global__ __launch_bounds__(1024) static void beam_join_kernel(const BeamArgs p
       uint64_t last = ~0ull;
       for (int r = 0; r < k; ++r) {
         uint64_t b = 0u;
-        for (int64_t i = lane; i < static_cast<int64_t>(p.chunks) * p.beams; i += 64) {
+        for (int64_t i = lane; i < n; i += 64) {
           const uint64_t w = best[i];
           if (w < last && w > b) b = w;
         }
@@ -308,32 +348,34 @@ __global__ __launch_bounds__(1024) static void beam_join_kernel(const BeamArgs p
       }
     }
     if (lane < k) {
-      values[j * k + rank] = v;
-      tokens[j * k + rank] = t;
+      values[(j << shift) + rank] = v;
+      tokens[(j << shift) + rank] = t;
     }
   }
+  const int items = p.rows << shift;
   int32_t* ranks = room.ranks;
   __syncthreads();
-  for (int i = threadIdx.x; i < p.rows * k; i += blockDim.x) ranks[i] = i % k;  // its place in its own row
+  for (int i = threadIdx.x; i < items; i += blockDim.x) ranks[i] = i & ((1 << shift) - 1);  // its place in its own row
   __syncthreads();
-  // how many of every other row come before each candidate: a pair of them and a row a thread
-  for (int q = threadIdx.x; q < p.rows * k * p.rows; q += blockDim.x) {
-    const int i = q / p.rows, o = q - i * p.rows, j = i / k;
-    if (o == j) continue;
-    const double v = values[i];
-    int lo = 0, hi = k;  // the first that does not come before (rows above win ties)
-    while (lo < hi) {
-      const int mid = (lo + hi) >> 1;
-      const double w = values[o * k + mid];
-      if (w > v || (w == v && o < j)) lo = mid + 1;
-      else hi = mid;
+  // how many of each other row come before each candidate: a row a wave, a candidate a lane
+  for (int o = wave; o < p.rows; o += waves)
+    for (int i = lane; i < items; i += 64) {
+      const int j = i >> shift;
+      if (j == o || (i & ((1 << shift) - 1)) >= k) continue;
+      const double v = values[i];
+      int lo = 0, hi = k;  // the first that does not come before (rows above win ties)
+      while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        const double w = values[(o << shift) + mid];
+        if (w > v || (w == v && o < j)) lo = mid + 1;
+        else hi = mid;
+      }
+      if (lo) atomicAdd(&ranks[i], lo);
     }
-    if (lo) atomicAdd(&ranks[i], lo);
-  }
   __syncthreads();
-  for (int i = threadIdx.x; i < p.rows * k; i += blockDim.x) {
-    if (ranks[i] >= p.beams) continue;
-    const int j = i / k;
+  for (int i = threadIdx.x; i < items; i += blockDim.x) {
+    if ((i & ((1 << shift) - 1)) >= k || ranks[i] >= p.beams) continue;
+    const int j = i >> shift;
     const int64_t at = seq * p.beams + ranks[i];
     p.parents[at] = j;
     p.tokens[at] = tokens[i];

@@ -10,21 +10,21 @@ using namespace ssm_host;
 
 namespace {
 
-// How a row is cut: into stretches of at most 64 lanes x `values` values, all about as long.
+// How a row is cut: into stretches of at most what a workgroup holds, all about as long.
 struct BeamShape {
-  int64_t values, chunks, blocks, bytes;
+  int64_t chunks, blocks, words, bytes;
 };
 
 ssm_status_t beam_shape(int64_t batch, int64_t rows, int64_t vocab, int64_t beams, bool bf16, BeamShape* out) {
   const int64_t epb = bf16 ? 8 : 4, blocks = (vocab + epb - 1) / epb;
-  out->values = 32;
-  const int64_t wave = 64 * (out->values / epb);
-  out->chunks = (blocks + wave - 1) / wave;
+  const int64_t group = ssm::kBeamThreads * (ssm::kBeamValues / epb);
+  out->chunks = (blocks + group - 1) / group;
   out->blocks = (blocks + out->chunks - 1) / out->chunks;
   int64_t n;
-  if (!mul_ok(batch * rows, out->chunks, &n) || !mul_ok(n, 8 * (beams + 1), &out->bytes))
+  if (!mul_ok(batch * rows, out->chunks, &n) || !mul_ok(n, 8 * (beams + ssm::kBeamWaves), &out->bytes))
     return fail(SSM_ERR_INVALID_ARG, "workspace size overflows int64");
-  if (n > kMaxIndex) return fail(SSM_ERR_UNSUPPORTED, "grid too large");
+  if (n > kMaxBlocks) return fail(SSM_ERR_UNSUPPORTED, "grid too large");
+  out->words = n;
   return SSM_OK;
 }
 
@@ -104,13 +104,12 @@ ssm_status_t ssm_beam_select(int64_t batch, int64_t rows, int64_t vocab, int64_t
   a.batch = batch; a.vocab = vocab;
   a.chunks = static_cast<int32_t>(s.chunks); a.blocks = static_cast<int32_t>(s.blocks);
   a.best = static_cast<uint64_t*>(workspace);
-  a.stats = reinterpret_cast<float*>(a.best + batch * rows * s.chunks * beams);
+  a.stats = reinterpret_cast<float*>(a.best + s.words * beams);
   a.parents = parents; a.tokens = tokens; a.out_scores = out_scores; a.out_finished = out_finished;
   hipStream_t st = static_cast<hipStream_t>(stream);
-  const int64_t waves = batch * rows * s.chunks, blocks = (waves + ssm::kBeamThreads / 64 - 1) / (ssm::kBeamThreads / 64);
-  if (blocks > kMaxBlocks || batch > 0xffffffffll / 1024) return fail(SSM_ERR_UNSUPPORTED, "grid too large");
-  const auto k = dtype == SSM_BF16 ? ssm::beam_rows_kernel<true, 32> : ssm::beam_rows_kernel<false, 32>;
-  hipLaunchKernelGGL(k, dim3(static_cast<unsigned>(blocks)), dim3(ssm::kBeamThreads), 0, st, a);
+  if (batch > 0xffffffffll / 1024) return fail(SSM_ERR_UNSUPPORTED, "grid too large");
+  const auto k = dtype == SSM_BF16 ? ssm::beam_rows_kernel<true> : ssm::beam_rows_kernel<false>;
+  hipLaunchKernelGGL(k, dim3(static_cast<unsigned>(s.words)), dim3(ssm::kBeamThreads), 0, st, a);
   SSM_TRY(check_launch("beam selection (rows)"));
   const unsigned threads = 64u * static_cast<unsigned>(rows < 16 ? rows : 16);
   hipLaunchKernelGGL(ssm::beam_join_kernel, dim3(static_cast<unsigned>(batch)), dim3(threads), 0, st, a);
