@@ -10,12 +10,20 @@ of later steps); scores: (batch, rows) fp32, the hypotheses' sums of log-probabi
 from __future__ import annotations
 
 import ctypes
+import functools
 from typing import Optional, Sequence, Tuple, Union
 
 import torch
 
 from . import SSM_BF16, SSM_F32, Entries, _check, load_library
 from .serving import _dense, _row_stride, _run
+
+
+@functools.lru_cache(maxsize=256)  # of the sizes alone, and a call into the library costs a microsecond
+def _workspace_bytes(batch: int, rows: int, vocab: int, beams: int, code: int) -> int:
+    n = ctypes.c_int64(0)
+    _check(load_library().ssm_beam_select_workspace(batch, rows, vocab, beams, code, ctypes.byref(n)))
+    return n.value
 
 
 def ssm_beam_select(logits: torch.Tensor, scores: torch.Tensor, beams: int, *, finished: Optional[torch.Tensor] = None,
@@ -53,16 +61,16 @@ def ssm_beam_select(logits: torch.Tensor, scores: torch.Tensor, beams: int, *, f
         _dense(workspace, "workspace", workspace.shape, torch.uint8, dev)
 
     def call(st):
-        n = ctypes.c_int64(0)
+        size = _workspace_bytes(batch, rows, vocab, beams, code)  # (and refuses bad sizes before anything is allocated)
         if workspace is None:
-            _check(lib.ssm_beam_select_workspace(batch, rows, vocab, beams, code, ctypes.byref(n)))
-            ws, size = logits.new_empty(n.value, dtype=torch.uint8), n.value
+            ws = logits.new_empty(size, dtype=torch.uint8)
         else:
             ws, size = workspace, workspace.numel()
-        ids = logits.new_empty((2, batch, max(beams, 0)), dtype=torch.int32)
-        out = logits.new_empty((batch, max(beams, 0)), dtype=torch.float32)
-        fin = None if pf is None else logits.new_empty((batch, max(beams, 0)), dtype=torch.bool)
-        parents, tokens = ids.unbind(0)
+        kept = (batch, beams)
+        parents = logits.new_empty(kept, dtype=torch.int32)
+        tokens = logits.new_empty(kept, dtype=torch.int32)
+        out = logits.new_empty(kept, dtype=torch.float32)
+        fin = None if pf is None else logits.new_empty(kept, dtype=torch.bool)
         # a stride of one row is any: given as that of contiguous ones
         _check(lib.ssm_beam_select(batch, rows, vocab, beams, code, logits.data_ptr(), sb if batch > 1 else 0,
                                    sr if rows > 1 else 0, ps, pf, int(eos), parents.data_ptr(), tokens.data_ptr(),
@@ -74,11 +82,7 @@ def ssm_beam_select(logits: torch.Tensor, scores: torch.Tensor, beams: int, *, f
 
 def ssm_beam_select_workspace(batch: int, rows: int, vocab: int, beams: int, dtype: torch.dtype) -> int:
     """Bytes of workspace of ssm_beam_select for these sizes."""
-    lib = load_library()
-    n = ctypes.c_int64(0)
-    _check(lib.ssm_beam_select_workspace(batch, rows, vocab, beams, SSM_BF16 if dtype == torch.bfloat16 else SSM_F32,
-                                         ctypes.byref(n)))
-    return n.value
+    return _workspace_bytes(batch, rows, vocab, beams, SSM_BF16 if dtype == torch.bfloat16 else SSM_F32)
 
 
 def ssm_cache_reorder(caches: Union[torch.Tensor, Sequence[torch.Tensor]], cache_slots: Optional[torch.Tensor],

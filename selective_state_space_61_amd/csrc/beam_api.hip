@@ -41,12 +41,19 @@ ssm_status_t check_beams(int64_t batch, int64_t rows, int64_t vocab, int64_t bea
   return SSM_OK;
 }
 
-using ReorderKernel = void (*)(const ssm::ReorderArgs);
-ReorderKernel reorder_of(int64_t beams) {
-  return beams <= 4 ? ssm::reorder_kernel<4>
-                    : beams <= 8 ? ssm::reorder_kernel<8>
-                                 : beams <= 16 ? ssm::reorder_kernel<16>
-                                               : beams <= 32 ? ssm::reorder_kernel<32> : ssm::reorder_kernel<64>;
+struct Reorder {
+  void (*kernel)(const ssm::ReorderArgs);
+  int64_t bytes;  // of an entry that a workgroup takes
+};
+template <int BEAMS, int COLUMNS>
+constexpr Reorder reorder_with() {
+  return {ssm::reorder_kernel<BEAMS, COLUMNS>, int64_t{COLUMNS} * ssm::kBeamThreads * 16};
+}
+Reorder reorder_of(int64_t beams) {
+  return beams <= 4 ? reorder_with<4, 2>()
+                    : beams <= 8 ? reorder_with<8, 2>()
+                                 : beams <= 16 ? reorder_with<16, 1>()
+                                               : beams <= 32 ? reorder_with<32, 1>() : reorder_with<64, 1>();
 }
 
 }  // namespace
@@ -146,7 +153,7 @@ ssm_status_t ssm_cache_reorder(int64_t batch, int64_t beams, const ssm_entries_t
   if (!parents) return fail(SSM_ERR_INVALID_ARG, "NULL parents");
   if (!aligned(parents, 4) || !aligned(cache_slots, 4))
     return fail(SSM_ERR_MISALIGNED, "parents or cache_slots is not 4-byte aligned");
-  const ReorderKernel k = reorder_of(beams);
+  const Reorder k = reorder_of(beams);
   for (int64_t i = 0; i < count;) {
     ssm::ReorderArgs a{};
     a.slots = cache_slots; a.parents = parents; a.batch = batch; a.beams = static_cast<int32_t>(beams);
@@ -155,10 +162,10 @@ ssm_status_t ssm_cache_reorder(int64_t batch, int64_t beams, const ssm_entries_t
       const ssm_entries_t& c = caches[i];
       if (c.slots == 0 || c.bytes == 0) continue;
       a.c[a.caches++] = {static_cast<char*>(c.data), c.slots, c.slot_stride == 0 ? c.bytes : c.slot_stride, c.bytes, blocks};
-      blocks += ((c.bytes + 15) / 16 + ssm::kBeamThreads - 1) / ssm::kBeamThreads;
+      blocks += (c.bytes + k.bytes - 1) / k.bytes;
     }
     if (a.caches == 0) break;
-    hipLaunchKernelGGL(k, dim3(static_cast<unsigned>(blocks), grid_y(batch)), dim3(ssm::kBeamThreads), 0,
+    hipLaunchKernelGGL(k.kernel, dim3(static_cast<unsigned>(blocks), grid_y(batch)), dim3(ssm::kBeamThreads), 0,
                        static_cast<hipStream_t>(stream), a);
     SSM_TRY(check_launch("cache reorder"));
   }

@@ -16,6 +16,7 @@ runs on, so that calls may be captured into a graph.
 from __future__ import annotations
 
 import ctypes
+import functools
 from typing import Optional, Tuple
 
 import torch
@@ -38,22 +39,25 @@ def _param_ptrs(a_param, a_bias, x_bias, dim: int, dev: int):
             _optional(x_bias, "x_bias", (dim,), f, dev))
 
 
-def ssm_gated_scan_workspace(batch: int, seqlen: int, dim: int, dtype: torch.dtype, backward: bool = False) -> int:
-    """Bytes of workspace of a forward or backward over a batch (packed prompts: one sequence of all rows)."""
-    lib = load_library()
+@functools.lru_cache(maxsize=256)  # of the sizes alone, and a call into the library costs a microsecond
+def _workspace_bytes(batch: int, seqlen: int, dim: int, code: int, backward: int) -> int:
     n = ctypes.c_int64(0)
-    _check(lib.ssm_gated_scan_workspace(batch, seqlen, dim, SSM_BF16 if dtype == torch.bfloat16 else SSM_F32, int(bool(backward)),
-                                        ctypes.byref(n)))
+    _check(load_library().ssm_gated_scan_workspace(batch, seqlen, dim, code, backward, ctypes.byref(n)))
     return n.value
 
 
-def _workspace(lib, given: Optional[torch.Tensor], x: torch.Tensor, batch: int, seqlen: int, code: int, backward: int):
+def ssm_gated_scan_workspace(batch: int, seqlen: int, dim: int, dtype: torch.dtype, backward: bool = False) -> int:
+    """Bytes of workspace of a forward or backward over a batch (packed prompts: one sequence of all rows)."""
+    return _workspace_bytes(batch, seqlen, dim, SSM_BF16 if dtype == torch.bfloat16 else SSM_F32, int(bool(backward)))
+
+
+def _workspace(given: Optional[torch.Tensor], x: torch.Tensor, batch: int, seqlen: int, code: int, backward: int):
+    """(the tensor, to be kept until the call is made, its address and size)"""
     if given is None:
-        n = ctypes.c_int64(0)
-        _check(lib.ssm_gated_scan_workspace(batch, seqlen, x.shape[-1], code, backward, ctypes.byref(n)))
-        if n.value == 0:
+        n = _workspace_bytes(batch, seqlen, x.shape[-1], code, backward)
+        if n == 0:
             return None, None, 0
-        given = x.new_empty(n.value, dtype=torch.uint8)
+        given = x.new_empty(n, dtype=torch.uint8)
     return given, given.data_ptr(), given.numel()
 
 
@@ -92,7 +96,7 @@ def _forward(x, a_gate, x_gate, a_param, a_bias, x_bias, z, a_scale, initial_sta
         out = torch.empty_like(x) if y is None else y
         last = x.new_empty((batch, dim), dtype=f) if last_state is None and return_last_state else last_state
         saved = x.new_empty(gated_checkpoint_shape(batch, seqlen, dim), dtype=f) if checkpoints is None and save else checkpoints
-        _keep, ws, n = _workspace(lib, workspace, x, batch, seqlen, code, 0)
+        _keep, ws, n = _workspace(workspace, x, batch, seqlen, code, 0)
         _check(lib.ssm_gated_scan_fwd(batch, seqlen, dim, code, *ptrs, a_scale, h0, out.data_ptr(),
                                       None if last is None else last.data_ptr(),
                                       None if saved is None else saved.data_ptr(), ws, n, st))
@@ -156,7 +160,7 @@ def ssm_gated_scan_bwd_ckpt(x: torch.Tensor, a_gate: torch.Tensor, x_gate: torch
                "dx_bias": None if x_bias is None else x.new_empty((dim,), dtype=f),
                "dinitial_state": None if initial_state is None else x.new_empty((batch, dim), dtype=f)}
         p = {k: None if t is None else t.data_ptr() for k, t in out.items()}
-        _keep, ws, n = _workspace(lib, workspace, x, batch, seqlen, code, 1)
+        _keep, ws, n = _workspace(workspace, x, batch, seqlen, code, 1)
         _check(lib.ssm_gated_scan_bwd(batch, seqlen, dim, code, *ptrs, a_scale, h0, saved, pdy, dlast, p["dx"],
                                       p["da_gate"], p["dx_gate"], p["da_param"], p["da_bias"], p["dx_bias"], p["dz"],
                                       p["dinitial_state"], ws, n, st))
@@ -200,7 +204,7 @@ def ssm_gated_scan_packed_fwd(x: torch.Tensor, a_gate: torch.Tensor, x_gate: tor
 
     def call(st):
         out = x.new_empty((total, dim)) if y is None else y
-        _keep, ws, n = _workspace(lib, workspace, x, 1, total, code, 0)
+        _keep, ws, n = _workspace(workspace, x, 1, total, code, 0)
         _check(lib.ssm_gated_scan_packed_fwd(seqs, dim, code, *ptrs, a_scale, out.data_ptr(), ref, strides, ws, n, st))
         return out
 
