@@ -77,6 +77,8 @@ ssm_status_t ssm_beam_select(int64_t batch, int64_t rows, int64_t vocab, int64_t
                              uint8_t* out_finished, void* workspace, int64_t workspace_bytes, void* stream) {
   g_err[0] = '\0';
   SSM_TRY(check_beams(batch, rows, vocab, beams, dtype));
+  BeamShape s;
+  SSM_TRY(beam_shape(batch, rows, vocab, beams, dtype == SSM_BF16, &s));
   if (finished && (eos < 0 || eos >= vocab))
     return fail(SSM_ERR_INVALID_ARG, "eos %lld is not in 0..%lld", (long long)eos, (long long)(vocab - 1));
   if (out_finished && !finished) return fail(SSM_ERR_INVALID_ARG, "out_finished needs finished");
@@ -89,8 +91,6 @@ ssm_status_t ssm_beam_select(int64_t batch, int64_t rows, int64_t vocab, int64_t
       !mul_ok(rows - 1, stride_row, &n) || __builtin_add_overflow(span, n, &span) ||
       __builtin_add_overflow(span, vocab, &span) || !mul_ok(span, es, &span))
     return fail(SSM_ERR_INVALID_ARG, "bad strides (%lld, %lld)", (long long)stride_batch, (long long)stride_row);
-  BeamShape s;
-  SSM_TRY(beam_shape(batch, rows, vocab, beams, dtype == SSM_BF16, &s));
   if (batch == 0) return SSM_OK;
   if (!logits || !scores || !parents || !tokens || !out_scores)
     return fail(SSM_ERR_INVALID_ARG, "NULL required pointer (logits, scores, parents, tokens and out_scores)");

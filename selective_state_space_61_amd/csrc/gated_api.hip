@@ -50,8 +50,9 @@ ssm_status_t cut_rows(const Tiled& t, int64_t sequences, int64_t seqlen, int64_t
   *out = Cut{};
   if (sequences > 1 && seqlen >= kOwnTiles) out->each = (seqlen + t.rows - 1) / t.rows;
   out->tiles = out->each ? out->each * sequences : (rows + t.rows - 1) / t.rows;
-  if (out->tiles <= 1) return SSM_OK;
   int64_t n;
+  if (!mul_ok(chains_of(dim), out->tiles, &n) || n > kMaxBlocks) return fail(SSM_ERR_UNSUPPORTED, "grid too large");
+  if (out->tiles <= 1) return SSM_OK;
   out->maps = 16;  // the ticket's line
   if (!mul_ok(out->tiles, dim, &n) || !mul_ok(n, 12, &n) || __builtin_add_overflow(n, out->maps + 15, &n))
     return fail(SSM_ERR_INVALID_ARG, "workspace size overflows int64");
@@ -107,9 +108,7 @@ ssm_status_t check_workspace(const void* workspace, int64_t bytes, int64_t need)
 // Clears the words that tiles publish and launches the kernel over all tiles.
 ssm_status_t launch_tiles(const Tiled& t, ssm::GatedArgs& a, const Cut& cut, void* workspace, hipStream_t st,
                           const char* what) {
-  int64_t grid;
-  const int64_t chains = chains_of(a.dim);
-  if (!mul_ok(chains, cut.tiles, &grid) || grid > kMaxBlocks) return fail(SSM_ERR_UNSUPPORTED, "grid too large");
+  const int64_t chains = chains_of(a.dim), grid = chains * cut.tiles;
   const int64_t words = cut.published / 16, blocks = (words + 255) / 256;
   if (blocks > kMaxBlocks) return fail(SSM_ERR_UNSUPPORTED, "grid too large");
   a.tiles = cut.tiles;
