@@ -22,7 +22,7 @@ from typing import Optional, Tuple
 import torch
 
 from . import SSM_BF16, SSM_F32, GatedStrides, _check, load_library
-from .serving import _cache, _dense, _indices, _optional, _packed, _row_stride, _run
+from .serving import _cache, _dense, _indices, _optional, _packed, _refuse, _row_stride, _run
 
 
 def _code(x: torch.Tensor) -> int:
@@ -169,18 +169,30 @@ def ssm_gated_scan_bwd_ckpt(x: torch.Tensor, a_gate: torch.Tensor, x_gate: torch
     return _run(call, dev, stream)
 
 
+def _row2(t: Optional[torch.Tensor], name: str, shape, dtype, device: int) -> int:
+    """_row_stride of a matrix: elements between its rows."""
+    if t is None or t.shape != shape or t.dtype is not dtype or t.get_device() != device:
+        _refuse(t, name, shape, dtype, device)
+    row, one = t.stride()
+    rows, width = shape
+    if one == 1 and row >= width:
+        return row
+    return _row_stride(t, name, shape, dtype, device)
+
+
 def _rows(x, a_gate, x_gate, a_param, a_bias, x_bias, z, y):
     """(shape, device, code, pointers of the inputs, strides) of a call on rows that may lie apart."""
     if x is None or x.dim() != 2:
         raise ValueError("x must be (rows, dim)")
     shape = x.shape
     dev, ty, code = x.get_device(), x.dtype, _code(x)
-    strides = GatedStrides(_row_stride(x, "x", shape, ty, dev), _row_stride(a_gate, "a_gate", shape, ty, dev),
-                           _row_stride(x_gate, "x_gate", shape, ty, dev),
-                           0 if z is None else _row_stride(z, "z", shape, ty, dev),
-                           0 if y is None else _row_stride(y, "y", shape, ty, dev))
-    params = _param_ptrs(a_param, a_bias, x_bias, shape[1], dev)
-    return shape, dev, code, (x.data_ptr(), a_gate.data_ptr(), x_gate.data_ptr(), *params,
+    strides = GatedStrides(_row2(x, "x", shape, ty, dev), _row2(a_gate, "a_gate", shape, ty, dev),
+                           _row2(x_gate, "x_gate", shape, ty, dev), 0 if z is None else _row2(z, "z", shape, ty, dev),
+                           0 if y is None else _row2(y, "y", shape, ty, dev))
+    f, one = torch.float32, shape[1:]
+    return shape, dev, code, (x.data_ptr(), a_gate.data_ptr(), x_gate.data_ptr(), _dense(a_param, "a_param", one, f, dev),
+                              None if a_bias is None else _dense(a_bias, "a_bias", one, f, dev),
+                              None if x_bias is None else _dense(x_bias, "x_bias", one, f, dev),
                               None if z is None else z.data_ptr()), strides
 
 

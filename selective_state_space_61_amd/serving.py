@@ -35,6 +35,8 @@ from . import SSM_BF16, SSM_F32, Cache, Packed, RowStrides, _check, _dtype_code,
 # the current stream's handle; the public call makes a Stream object first, which takes a microsecond
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda device: torch.cuda.current_stream(device).cuda_stream)
+# the current device, likewise (its tensors are there, so the GPU is initialised)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _refuse(t, name: str, shape, dtype, device: int) -> None:
@@ -137,7 +139,7 @@ def _run(call, device: int, stream):
     it allocates then belongs to the stream that uses it."""
     if device < 0:
         raise ValueError("the tensors are on the host, expected a GPU")
-    if stream is None and torch.cuda.current_device() == device:
+    if stream is None and _current_device() == device:
         return call(_raw_stream(device))
     with _other(device, stream):
         return call(_raw_stream(device))
