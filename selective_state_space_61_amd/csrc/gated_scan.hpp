@@ -289,9 +289,10 @@ struct Channels {
 };
 
 // l = k r of a channel: k = -a_scale softplus(a_param), by the library's exp and log1p (once a workgroup and
-// channel, not once a lane).  Finite, so that l a is 0 and not NaN where a is 0.
+// channel, not once a lane).  Not infinite, so that l a is 0 and not NaN where a is 0; NaN where a_param is.
 __device__ __forceinline__ float decay_rate(float scale, float q) {
-  return -fminf(scale * (fmaxf(q, 0.0f) + log1pf(expf(-fabsf(q)))), 1e30f);
+  const float k = scale * (fmaxf(q, 0.0f) + log1pf(expf(-fabsf(q))));
+  return k > 1e30f ? -1e30f : -k;
 }
 
 // -bias log2(e) of a lane's channels (sigmoid_f32)
@@ -771,9 +772,9 @@ __global__ __launch_bounds__(kGatedThreads, 3) void gated_scan_bwd_kernel(const 
         for (int v = 0; v < V; ++v) {
           const float G = EDGES && (in.last >> j & 1) ? g[j][v] : g[j][v] + C[v];
           const float xv = x[j].get(v), la = k[v] * r[j][v] * a[j][v];
-          // (w below 1e-30: l is 0, and what 1 / w is multiplied with has to be finite)
-          const float q = a[j][v] * hw_rcp(fmaxf(w[j][v], 1e-30f));
-          float E = G * la * fmaf(-i[j][v] * xv, q, prev[v]);
+          // l a^2 / w before x, whatever x is: at most w / 2, and 0 where l is (a w below 1e-19 has no normal l)
+          const float q = la * a[j][v] * hw_rcp(fmaxf(w[j][v], 1e-19f));
+          float E = G * fmaf(-i[j][v] * xv, q, la * prev[v]);
           odx[v] = G * w[j][v] * i[j][v];
           odg[v] = odx[v] * xv;
           odg[v] = fmaf(-odg[v], i[j][v], odg[v]);

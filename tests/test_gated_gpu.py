@@ -260,6 +260,66 @@ def test_closed_gates_and_extreme_parameters():
     assert ((yc[10:20] - yc[9]).abs() <= ec[10:20] + ec[9]).all()
 
 
+@pytest.mark.parametrize("dtype", [BF, F])
+def test_huge_inputs_behind_closed_gates(dtype):
+    """Inputs up to the type's largest that a closed gate keeps out leave no trace in states and gradients."""
+    t = make((2, 150, 66), dtype, 3)
+    t["a_gate"][:, 20:90] = float("-inf")
+    plain = dict(t, x=torch.where(t["a_gate"].isinf(), torch.zeros_like(t["x"]), t["x"]))
+    t["x"] = torch.where(t["a_gate"].isinf(), t["x"].sign() * torch.finfo(dtype).max, t["x"])
+    dy = torch.randn(2, 150, 66, generator=torch.Generator().manual_seed(6)).to(dtype).cuda()
+    got, want = [], []
+    for out, d in ((got, t), (want, plain)):
+        y, last, saved = ssm.ssm_gated_scan_fwd_ckpt(**d)
+        out += [y, last, *(v for v in ssm.ssm_gated_scan_bwd_ckpt(**d, dy=dy, checkpoints=saved).values() if v is not None)]
+    for a, b in zip(got, want):
+        assert torch.isfinite(b).all() and torch.equal(a, b)
+
+
+def test_a_parameter_that_is_no_number():
+    """NaN in a_param is NaN in its channel's rows, states and gradients, and in no other's."""
+    for shape in ((2, 70, 130), (300, 1, 5)):
+        t = make(shape, BF, 4)
+        bad = dict(t, a_param=t["a_param"].clone())
+        bad["a_param"][3] = float("nan")
+        other = torch.arange(shape[-1]) != 3
+        dy = torch.ones(shape, dtype=BF, device="cuda")
+        outs = []
+        for d in (t, bad):
+            y, last, saved = ssm.ssm_gated_scan_fwd_ckpt(**d)
+            grads = ssm.ssm_gated_scan_bwd_ckpt(**d, dy=dy, checkpoints=saved)
+            cache = torch.ones(shape[0], shape[-1], device="cuda")
+            rows = {k: (v[:, 0].contiguous() if k in ("x", "a_gate", "x_gate", "z") else v) for k, v in d.items()}
+            outs.append([y, last, grads["dx"], grads["da_param"], ssm.ssm_gated_update_cache(cache, None, **rows), cache])
+        for clean, got in zip(*outs):
+            assert torch.equal(clean[..., other], got[..., other])
+            assert got[..., 3].isnan().all()
+
+
+@pytest.mark.parametrize("dim,dtype,cdtype", [(66, BF, F), (65, BF, BF), (67, BF, F), (65, F, BF), (129, BF, BF), (194, BF, F)])
+def test_packed_with_a_short_last_block(dim, dtype, cdtype):
+    """Channels past a multiple of 64 that fill no lane: each state is read and written by one workgroup alone,
+    also where the cache is updated in place; twice as many short sequences begin in a tile as it has rows."""
+    lens = [1, 0, 0, 2, 0] * 60 + [200, 1]
+    cu, starts, total = packed(lens)
+    g = torch.Generator().manual_seed(dim)
+    t = make((total, dim), dtype, dim)
+    cache = torch.randn(len(lens), dim, generator=g).to(cdtype).cuda()
+    before = cache.clone()
+    init = torch.ones(len(lens), dtype=torch.bool).cuda()
+    y = ssm.ssm_gated_scan_packed_fwd(**t, cu_seqlens=cu, cache=cache, has_initial=init)
+    d = host(t)
+    for s, n in enumerate(lens):
+        a, b = starts[s], starts[s + 1]
+        if n == 0:
+            assert torch.equal(cache[s], before[s])
+            continue
+        rows = {k: (v[a:b] if k in ("x", "ag", "xg", "z") else v) for k, v in d.items()}
+        yr, ey, h, eh = R.forward(**rows, h0=R.f64(before[s]))
+        R.check(y[a:b], yr, ey, dtype, f"y of sequence {s}")
+        R.check(cache[s], h[-1], eh[-1], cdtype, f"state of sequence {s}")
+
+
 def test_no_decay_at_all():
     """a_scale 0: the states never move."""
     t = make((2, 200, 10), BF, 1)
