@@ -851,7 +851,8 @@ typedef struct {
  *                Slots must differ from one another
  *   parents      (batch, beams) int32 on the device, as ssm_beam_select gives
  *                them; several beams may have one parent
- *   caches       descriptors, in host memory, of caches that do not overlap
+ *   caches       descriptors, in host memory, of caches that do not overlap (one
+ *                given twice is refused)
  *
  * beams is 1..64.  A beam without a slot (negative, or past the cache's slots),
  * of a parent out of range or without a slot, or that is its own parent keeps

@@ -132,8 +132,14 @@ ssm_status_t ssm_cache_reorder(int64_t batch, int64_t beams, const ssm_entries_t
   if (beams > ssm::kBeamMost)
     return fail(SSM_ERR_UNSUPPORTED, "more than %d beams (%lld)", ssm::kBeamMost, (long long)beams);
   if (count > 0 && !caches) return fail(SSM_ERR_INVALID_ARG, "NULL caches");
+  uintptr_t last = 0;  // the highest address so far: layers mostly come in the order of their addresses
   for (int64_t i = 0; i < count; ++i) {
     const ssm_entries_t& c = caches[i];
+    const uintptr_t at = reinterpret_cast<uintptr_t>(c.data);
+    for (int64_t j = 0; at <= last && c.slots > 0 && c.bytes > 0 && j < i; ++j)
+      if (caches[j].data == c.data && caches[j].slots > 0 && caches[j].bytes > 0)
+        return fail(SSM_ERR_INVALID_ARG, "cache %lld is cache %lld again", (long long)i, (long long)j);
+    last = at > last ? at : last;
     const int64_t stride = c.slot_stride == 0 ? c.bytes : c.slot_stride;
     int64_t span;
     if (c.slots < 0 || c.slots > kMaxIndex || c.bytes < 0 || stride < c.bytes || !mul_ok(c.slots, stride, &span))

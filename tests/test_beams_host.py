@@ -74,6 +74,12 @@ def test_reorder_refusals(lib, kw, status):  # noqa: F811
     assert reorder(lib, **kw) == status
 
 
+@pytest.mark.parametrize("order", [(0, 0), (0, 1, 2, 1), (3, 2, 1, 3), (5, 6, 5)])
+def test_reorder_of_one_cache_twice(lib, order):  # noqa: F811
+    caches = entries(*(dict(data=fake(10 + k)) for k in order))
+    assert reorder(lib, caches=caches) == INVALID and "again" in err(lib)
+
+
 def test_reorder_with_nothing_to_do(lib):  # noqa: F811
     assert reorder(lib, batch=0, parents=None) == OK and reorder(lib, beams=1, parents=None) == OK
     assert reorder(lib, count=0, parents=None) == OK
