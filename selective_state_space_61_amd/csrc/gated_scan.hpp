@@ -78,7 +78,10 @@ __device__ __forceinline__ void publish(uint64_t* p, float a, float b) {
 }
 
 // The state that leaves the tile before this one.  maps and ends point at that tile's words; those of the tiles
-// before it lie `step` elements on each, `first` tiles in all.  WINDOW tiles' words are asked for at once.
+// before it lie `step` elements on each, `first` tiles in all.  WINDOW tiles' words are asked for at once, as
+// many as leave the kernels' registers in place: forward with 4 and 8, 30000 x 256 bf16 rows take 74 and 61 us,
+// but 12288 x 5120 packed ones 170 and 175; backward with 2, 3 and 4, 30011 x 2560 take 351, 341 and 341 us, 8 x
+// 2048 x 1536 120, 121 and 124 (spilled registers; in fp32 3 spills too).
 // Every lane of the wave calls it; lanes with `on` false (no channel, or nothing enters) get 0.
 template <int WINDOW>
 __device__ __forceinline__ float look_back(const uint64_t* maps, const uint32_t* ends, int64_t step, int64_t first,
@@ -88,12 +91,13 @@ __device__ __forceinline__ float look_back(const uint64_t* maps, const uint32_t*
   while (!__all(done)) {
     if (!done) {
       uint32_t e[WINDOW];
-      uint64_t m[WINDOW];
+      uint64_t m[WINDOW - 1];
 #pragma unroll
       for (int k = 0; k < WINDOW; ++k) {
         // before the first tile the state is 0
         e[k] = k < first ? __hip_atomic_load(ends + k * step, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : 0u;
-        m[k] = k < first ? __hip_atomic_load(maps + k * step, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : 0u;
+        if (k < WINDOW - 1)
+          m[k] = k < first ? __hip_atomic_load(maps + k * step, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : 0u;
       }
       int near = 0;  // tiles over whose maps the nearest end state comes here
       bool open = true;
@@ -104,15 +108,18 @@ __device__ __forceinline__ float look_back(const uint64_t* maps, const uint32_t*
           open = false;
           near = k;
         }
-        if (m[k] == ~0ull) open = false;
+        if (k < WINDOW - 1 && m[k] == ~0ull) open = false;
       }
       if (done) {
 #pragma unroll
         for (int k = WINDOW - 1; k >= 0; --k) {
-          const float a = __builtin_bit_cast(float, static_cast<uint32_t>(m[k]));
-          const float b = __builtin_bit_cast(float, static_cast<uint32_t>(m[k] >> 32));
-          if (k == near) h = __builtin_bit_cast(float, e[k]);
-          else if (k < near) h = fmaf(a, h, b);
+          if (k == near) {
+            h = __builtin_bit_cast(float, e[k]);
+          } else if (k < WINDOW - 1) {
+            const float a = __builtin_bit_cast(float, static_cast<uint32_t>(m[k]));
+            const float b = __builtin_bit_cast(float, static_cast<uint32_t>(m[k] >> 32));
+            if (k < near) h = fmaf(a, h, b);
+          }
         }
       }
     }
@@ -342,10 +349,10 @@ struct PartMaps {
 
 // The tile that a workgroup takes: the next one.  Tiles of a sequence that share no row with another come in the
 // order (their place in the sequence, sequence, channels), so that a tile waits for one that was taken a batch
-// earlier: 8 x 2048 x 1536 rows take 73 us forward and 127 backward, and 80 and 150 in the order of the rows.
-// (A counter for each block of channels in place of one for all: 71 and 130, and one sequence of 30011 x 2560
-// 204 and 397 us for 190 and 359, since the blocks' rows drift apart.  Workgroups that stay and take tile after
-// tile with the next number asked for ahead: 112 us, since the tile that a number stands for then waits.)
+// earlier: 8 x 2048 x 1536 bf16 rows take 10% less forward than in the order of the rows, and 15% less backward.
+// (A counter for each block of channels in place of one for all: one sequence of 30011 x 2560 takes 8% and 10%
+// more, since the blocks' rows drift apart.  Workgroups that stay and take tile after
+// tile with the next number asked for ahead: half as much again, since the tile that a number stands for waits.)
 struct Turn {
   uint32_t block, turn;  // in the order in which tiles are taken
   uint32_t before;       // tiles before it that may enter it
@@ -691,24 +698,20 @@ __global__ __launch_bounds__(kGatedThreads, 3) void gated_scan_bwd_kernel(const 
     }
     __syncthreads();
 
-    // the first wave runs the states through the parts, the second the adjoint
+    // The first wave runs the states through the parts, the second the adjoint.  (The parts' maps stay in the LDS:
+    // in registers over the look-back they made the kernel spill, 8 x 2048 x 1536 in 126 us for 120.)
     if (wave < 2) {
       const int c = threadIdx.x & 63;
       const bool on = ch.has(c / V);
       const int64_t dc = ch.of(c / V) + c % V;
-      float pa[S::kParts], pb[S::kParts];
-#pragma unroll
-      for (int q = 0; q < S::kParts; ++q) {
-        pa[q] = fwd.a[q][c];
-        pb[q] = wave == 0 ? fwd.b[q][c] : back[q][c];
-      }
       if (wave == 0) {
         const int64_t saved = checkpoint_after(p, tile, tile0);
         float s = saved >= 0 ? p.ckpt[saved * p.dim + dc] : 0.0f;
 #pragma unroll
         for (int q = 0; q < S::kParts; ++q) {
+          const float pa = fwd.a[q][c], pb = fwd.b[q][c];
           fwd.b[q][c] = s;
-          s = EDGES && fwd.own[q] ? pb[q] : fmaf(pa[q], s, pb[q]);
+          s = EDGES && fwd.own[q] ? pb : fmaf(pa, s, pb);
         }
       } else {
         float ta = 1.0f, tb = 0.0f;
@@ -716,22 +719,24 @@ __global__ __launch_bounds__(kGatedThreads, 3) void gated_scan_bwd_kernel(const 
 #pragma unroll
         for (int q = S::kParts - 1; q >= 0; --q) {
           const bool stops = EDGES && ends[q];
+          const float pa = fwd.a[q][c], pb = back[q][c];
           own |= stops;
-          ta *= pa[q];
-          tb = stops ? pb[q] : fmaf(pa[q], tb, pb[q]);
+          ta *= pa;
+          tb = stops ? pb : fmaf(pa, tb, pb);
         }
         float s = 0.0f;
         if (p.ticket) {
           const int64_t at = tile.turn * p.dim + dc, step = -(tile.apart * p.dim);
           if (on && !own) publish(p.maps + at, ta, tb);
           if (on && own) publish(p.ends + at, tb);
-          s = look_back<2>(p.maps + at + step, p.ends + at + step, step, tile.before, on && !(EDGES && (rows.last[0] >> 63)));
+          s = look_back<BF16 ? 3 : 2>(p.maps + at + step, p.ends + at + step, step, tile.before, on && !(EDGES && (rows.last[0] >> 63)));
           if (on && !own) publish(p.ends + at, fmaf(ta, s, tb));
         }
 #pragma unroll
         for (int q = S::kParts - 1; q >= 0; --q) {
+          const float pa = fwd.a[q][c], pb = back[q][c];
           back[q][c] = s;
-          s = EDGES && ends[q] ? pb[q] : fmaf(pa[q], s, pb[q]);
+          s = EDGES && ends[q] ? pb : fmaf(pa, s, pb);
         }
       }
     }
