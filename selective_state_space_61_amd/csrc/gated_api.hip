@@ -39,20 +39,25 @@ Tiled backward_kernel(bool bf16, int64_t dim, bool z) {
 }
 
 // How the rows are cut: tiles of sequences by themselves where these are long enough that a last, shorter tile
-// of each costs little, else of all rows, which may share tiles.  The tiles and the bytes that they publish
-// through (0 where no tile enters another).
+// of each costs little; tiles of several whole sequences where these fill three quarters of one or more (then no
+// tile waits: 2000 x 40 x 1024 bf16 rows forward, 120 of 128, 207 us for 218, 60 x 40 x 1024 15 for 20; backward, 40
+// of 64, 496 for 401); else of all rows, which may share tiles.  The tiles and the bytes that they publish through
+// (0 where no tile enters another).
 constexpr int64_t kOwnTiles = 256;  // rows of a sequence from which on it has tiles of its own
 struct Cut {
-  int64_t tiles, each, published, maps;  // each: of a sequence (0: shared); maps: where they begin
+  int64_t tiles, each, pitch, published, maps;  // each: of a sequence (0: shared); maps: where they begin
 };
 int64_t chains_of(int64_t dim) { return (dim + ssm::kGatedChannels - 1) / ssm::kGatedChannels; }
 ssm_status_t cut_rows(const Tiled& t, int64_t sequences, int64_t seqlen, int64_t rows, int64_t dim, Cut* out) {
   *out = Cut{};
   if (sequences > 1 && seqlen >= kOwnTiles) out->each = (seqlen + t.rows - 1) / t.rows;
-  out->tiles = out->each ? out->each * sequences : (rows + t.rows - 1) / t.rows;
+  const int64_t held = sequences > 1 && seqlen > 0 ? t.rows / seqlen * seqlen : 0;  // rows of whole sequences
+  const bool whole = held * 4 >= t.rows * 3;
+  out->pitch = whole ? held : t.rows;
+  out->tiles = out->each ? out->each * sequences : (rows + out->pitch - 1) / out->pitch;
   int64_t n;
   if (!mul_ok(chains_of(dim), out->tiles, &n) || n > kMaxBlocks) return fail(SSM_ERR_UNSUPPORTED, "grid too large");
-  if (out->tiles <= 1) return SSM_OK;
+  if (out->tiles <= 1 || whole) return SSM_OK;
   out->maps = 16;  // the ticket's line
   if (!mul_ok(out->tiles, dim, &n) || !mul_ok(n, 12, &n) || __builtin_add_overflow(n, out->maps + 15, &n))
     return fail(SSM_ERR_INVALID_ARG, "workspace size overflows int64");
@@ -113,6 +118,7 @@ ssm_status_t launch_tiles(const Tiled& t, ssm::GatedArgs& a, const Cut& cut, voi
   if (blocks > kMaxBlocks) return fail(SSM_ERR_UNSUPPORTED, "grid too large");
   a.tiles = cut.tiles;
   a.each = cut.each;
+  a.pitch = cut.pitch;
   a.chains = static_cast<int32_t>(chains);
   if (cut.published) {
     char* w = static_cast<char*>(workspace);
@@ -260,9 +266,11 @@ ssm_status_t ssm_gated_scan_bwd(int64_t batch, int64_t seqlen, int64_t dim, ssm_
     a.ckpt = const_cast<float*>(checkpoints);
     a.dlast = dlast_state; a.dx = dx; a.dag = da_gate; a.dxg = dx_gate; a.dz = dz; a.dh0 = dinitial_state;
     a.partial = reinterpret_cast<float*>(static_cast<char*>(workspace) + cut.published);
+    a.dparam = da_param; a.dab = da_bias; a.dxb = dx_bias;
     sum.partial = a.partial;
     sum.tiles = cut.tiles;
     SSM_TRY(launch_tiles(t, a, cut, workspace, st, "gated scan backward"));
+    if (cut.tiles == 1) return SSM_OK;  // it has the sums
   } else if (dinitial_state && n.states > 0) {
     SSM_TRY(keep_states(dlast_state, dinitial_state, n.states / 4, st));
   }

@@ -48,6 +48,7 @@ struct GatedArgs {
   uint64_t* maps;                // (tiles, dim), in the order in which tiles are taken
   uint32_t* ends;
   int64_t tiles, each;           // tiles, and those of a sequence if none holds rows of two (else 0)
+  int64_t pitch;                 // rows from a tile to the next, if tiles hold rows of several
   int32_t chains;                // blocks of kGatedChannels channels
   // backward
   const void* dy;
@@ -55,6 +56,7 @@ struct GatedArgs {
   void *dx, *dag, *dxg, *dz;
   float* dh0;
   float* partial;                // (tiles, 3, dim): sums of E, da_gate, dx_gate
+  float *dparam, *dab, *dxb;     // the sums over all rows; the last two may be NULL
 };
 
 // Lanes of a workgroup: kLanes lanes of V channels, the others its rows, R each.
@@ -385,8 +387,8 @@ struct Turn {
       t.before = t.turn;
       t.apart = 1;
       t.s = 0;
-      t.row0 = static_cast<int64_t>(backward ? tiles - 1 - t.turn : t.turn) * ROWS;
-      t.end = p.total;
+      t.row0 = static_cast<int64_t>(backward ? tiles - 1 - t.turn : t.turn) * p.pitch;
+      t.end = t.row0 + p.pitch < p.total ? t.row0 + p.pitch : p.total;
     }
     return t;
   }
@@ -551,10 +553,18 @@ __global__ __launch_bounds__(kGatedThreads) void gated_scan_kernel(const GatedAr
           final_state<V>(p, rows.seq[at0 + at], d, e);
         }
       }
-      static_assert(kGatedSave % R == 0, "a checkpoint is the state after a part");
+      static_assert(kGatedSave % R == 0, "inside a sequence a checkpoint is the state after a part");
       if (p.ckpt) {
-        const int64_t row = checkpoint_after(p, tile, tile0 + at0 + R);
+        const int64_t from = tile0 + at0 - (p.each ? tile.end - p.seqlen : 0);
+        const int at = EDGES ? kGatedSave - 1 - static_cast<int>(from % kGatedSave) : R - 1;
+        const int64_t row = at < R ? checkpoint_after(p, tile, tile0 + at0 + at + 1) : -1;
         if (row >= 0) {
+          if constexpr (EDGES) {
+#pragma unroll
+            for (int j = 0; j < R; ++j)
+#pragma unroll
+              for (int v = 0; v < V; ++v) h[v] = j == at ? b[j][v] : h[v];
+          }
           Run<false, V> out;
           out.set(h);
           out.store(p.ckpt, row * p.dim + d);
@@ -573,6 +583,19 @@ __global__ __launch_bounds__(kGatedThreads) void gated_scan_kernel(const GatedAr
 // E is 0 where w is (a = 1): l / w -> 0 as l -> 0, so the product has that limit though dw/dl has none.
 // The states come from the checkpoint before the tile and the tile's own rows; a G is carried from tile
 // to tile like the forward's state, tiles taken from the last one on.
+
+// Stores the sum over all rows of quantity k: E (da_param), da_gate (da_bias) or dx_gate (dx_bias).
+__device__ __forceinline__ void store_sum(int k, int64_t d, float s, const float* param, float* dparam, float* dab, float* dxb) {
+  if (k == 0) {
+    // d softplus(v) / softplus(v): sigmoid(v) / softplus(v), 1 to fp32 below -17
+    const float v = param[d];
+    const float ratio = v < -17.0f ? 1.0f : 1.0f / (1.0f + expf(-v)) / (fmaxf(v, 0.0f) + log1pf(expf(-fabsf(v))));
+    dparam[d] = s * ratio;
+  } else if (float* out = k == 1 ? dab : dxb) {
+    out[d] = s;
+  }
+}
+
 // V channels of sequence s in a (batch, dim) tensor of states, zeros without one
 template <int V>
 __device__ __forceinline__ Run<false, V> batch_state(const void* states, int32_t s, int64_t dim, int64_t d) {
@@ -835,7 +858,11 @@ __global__ __launch_bounds__(kGatedThreads, 3) void gated_scan_bwd_kernel(const 
     float s = 0.0f;
 #pragma unroll
     for (int q = 0; q < S::kParts; ++q) s += wave == 0 ? fwd.a[q][c] : wave == 1 ? fwd.b[q][c] : back[q][c];
-    if (ch.has(c / V)) p.partial[(static_cast<int64_t>(tile.turn) * 3 + wave) * p.dim + ch.of(c / V) + c % V] = s;
+    if (ch.has(c / V)) {
+      const int64_t dc = ch.of(c / V) + c % V;
+      if (p.tiles == 1) store_sum(wave, dc, s, p.param, p.dparam, p.dab, p.dxb);
+      else p.partial[(static_cast<int64_t>(tile.turn) * 3 + wave) * p.dim + dc] = s;
+    }
   }
 }
 
@@ -864,14 +891,7 @@ __global__ __launch_bounds__(kGatedSumThreads) static void gated_sum_kernel(cons
   if (part == 0 && d < p.dim) {
 #pragma unroll
     for (int i = 1; i < 16; ++i) s += sums[i][c];
-    if (k == 0) {
-      // d softplus(v) / softplus(v): sigmoid(v) / softplus(v), 1 to fp32 below -17
-      const float v = p.param[d];
-      const float ratio = v < -17.0f ? 1.0f : 1.0f / (1.0f + expf(-v)) / (fmaxf(v, 0.0f) + log1pf(expf(-fabsf(v))));
-      p.dparam[d] = s * ratio;
-    } else if (float* out = k == 1 ? p.dab : p.dxb) {
-      out[d] = s;
-    }
+    store_sum(k, d, s, p.param, p.dparam, p.dab, p.dxb);
   }
 }
 

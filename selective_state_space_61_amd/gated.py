@@ -94,7 +94,9 @@ def _forward(x, a_gate, x_gate, a_param, a_bias, x_bias, z, a_scale, initial_sta
 
     def call(st):
         out = torch.empty_like(x) if y is None else y
-        last = x.new_empty((batch, dim), dtype=f) if last_state is None and return_last_state else last_state
+        last = last_state
+        if last is None and return_last_state:
+            last = x.new_empty((batch, dim), dtype=f) if h0 is None else torch.empty_like(initial_state)
         saved = x.new_empty(gated_checkpoint_shape(batch, seqlen, dim), dtype=f) if checkpoints is None and save else checkpoints
         _keep, ws, n = _workspace(workspace, x, batch, seqlen, code, 0)
         _check(lib.ssm_gated_scan_fwd(batch, seqlen, dim, code, *ptrs, a_scale, h0, out.data_ptr(),
@@ -155,10 +157,10 @@ def ssm_gated_scan_bwd_ckpt(x: torch.Tensor, a_gate: torch.Tensor, x_gate: torch
 
     def call(st):
         out = {"dx": torch.empty_like(x), "da_gate": torch.empty_like(x), "dx_gate": torch.empty_like(x),
-               "dz": None if z is None else torch.empty_like(x), "da_param": x.new_empty((dim,), dtype=f),
-               "da_bias": None if a_bias is None else x.new_empty((dim,), dtype=f),
-               "dx_bias": None if x_bias is None else x.new_empty((dim,), dtype=f),
-               "dinitial_state": None if initial_state is None else x.new_empty((batch, dim), dtype=f)}
+               "dz": None if z is None else torch.empty_like(x), "da_param": torch.empty_like(a_param),
+               "da_bias": None if a_bias is None else torch.empty_like(a_bias),
+               "dx_bias": None if x_bias is None else torch.empty_like(x_bias),
+               "dinitial_state": None if initial_state is None else torch.empty_like(initial_state)}
         p = {k: None if t is None else t.data_ptr() for k, t in out.items()}
         _keep, ws, n = _workspace(workspace, x, batch, seqlen, code, 1)
         _check(lib.ssm_gated_scan_bwd(batch, seqlen, dim, code, *ptrs, a_scale, h0, saved, pdy, dlast, p["dx"],

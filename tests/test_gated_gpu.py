@@ -87,6 +87,21 @@ def test_batches(shape, dtype, z, states):
         R.check(v, val, ev, v.dtype, k)
 
 
+@pytest.mark.parametrize("shape", [(9, 40, 70), (11, 41, 33), (50, 2, 64), (13, 20, 130), (3, 128, 65), (3, 64, 66), (200, 31, 5)])
+@pytest.mark.parametrize("dtype", [BF, F])
+def test_batches_of_short_sequences(shape, dtype):
+    """Several whole sequences in a tile, forward, backward or both; the forward's checkpoints then lie anywhere in
+    its tiles."""
+    test_batches(shape, dtype, True, True)
+    batch, seqlen, dim = shape
+    t = make(shape, dtype, 7)
+    y, last, saved = ssm.ssm_gated_scan_fwd_ckpt(**dict(t, z=None))
+    rows = torch.arange(63, batch * seqlen, 64)
+    d = host(dict(t, z=None))
+    _, _, h, eh = R.forward(**d)
+    R.check(saved, h.transpose(0, 1).reshape(-1, dim)[rows], eh.transpose(0, 1).reshape(-1, dim)[rows], F, "checkpoints")
+
+
 @pytest.mark.parametrize("dtype", [BF, F])
 def test_a_long_sequence(dtype):
     """Hundreds of tiles handing states on, forward and backward."""
