@@ -427,7 +427,6 @@ __global__ __launch_bounds__(kGatedThreads) void gated_scan_kernel(const GatedAr
     load_rows<!EDGES>(ag, p.ag, p.sag, tile0, at0, d, tile.end);
     load_rows<!EDGES>(xg, p.xg, p.sxg, tile0, at0, d, tile.end);
     load_rows<!EDGES>(x, p.x, p.sx, tile0, at0, d, tile.end);
-    if constexpr (Z) load_rows<!EDGES>(z, p.z, p.sz, tile0, at0, d, tile.end);
     float ab[V], xb[V];
     load_bias<V>(p.ab, d, ab);
     load_bias<V>(p.xb, d, xb);
@@ -482,6 +481,8 @@ __global__ __launch_bounds__(kGatedThreads) void gated_scan_kernel(const GatedAr
       maps.a[part][lane * V + v] = A[v];
       maps.b[part][lane * V + v] = B[v];
     }
+    // (not with the others: 12 registers fewer, and it arrives while the tile waits; 2% faster)
+    if constexpr (Z) load_rows<!EDGES>(z, p.z, p.sz, tile0, at0, d, tile.end);
     if (EDGES && lane == 0) maps.own[part] = in.first != 0;
     __syncthreads();
 
