@@ -102,8 +102,12 @@ __device__ __forceinline__ int rank_of(uint64_t w, int n) {
 
 __device__ __forceinline__ bool is_finite(float v) { return __builtin_isfinite(v); }
 
+// Neither the memory nor the VALU is busy (each near 60%): a workgroup loads, then ranks, and others fill in.  48 x 8
+// rows of 50257 fp32 values take 16.8 us (4.6 TB/s), 20 x 16 of 131072 bf16 ones, a quarter finished, 20 (3.1 TB/s);
+// seven waves a SIMD, three registers spilled, are 2% and 3% faster than six, eight 15% and 7% slower.  With half the
+// values a lane, whose waves fit eight times, 0% and 16% slower.
 template <bool BF16>
-__global__ __launch_bounds__(kBeamThreads) void beam_rows_kernel(const BeamArgs p) {
+__global__ __launch_bounds__(kBeamThreads, 7) void beam_rows_kernel(const BeamArgs p) {
   constexpr int EPB = BF16 ? 8 : 4, IT = kBeamValues / EPB, ES = BF16 ? 2 : 4;
   __shared__ uint64_t lists[kBeamWaves][64];
   __shared__ float tops[kBeamWaves][64];
@@ -384,7 +388,7 @@ __global__ __launch_bounds__(1024) static void beam_join_kernel(const BeamArgs p
   }
 }
 
-// Reordering.  Beam i of a sequence takes the entry of beam parents[i].  A thread owns 16 bytes of the
+// Reordering.  Beam i of a sequence takes the entry of beam parents[i].  A thread owns 16 bytes (or 8) of the
 // entry in every beam's slot: it reads what moves, then writes it, so that the order of beams does not
 // matter and no copy of the cache is needed.  Bound by the memory: 128 slots of 2.6 MB (16 sequences of 8 beams, parents
 // drawn) take 101 us, 4.8 TB/s; with one 16-byte column a thread 109, with four 102, with plain stores 5% more.
@@ -401,17 +405,20 @@ struct ReorderArgs {
   int32_t beams, caches;
 };
 
-// COLUMNS of 16 bytes a thread, of BEAMS beams at most.
-template <int BEAMS, int COLUMNS>
+// COLUMNS of WORDS 32-bit words a thread, of BEAMS beams at most.  (64 beams of 16 bytes a thread spill: 4 sequences
+// of 64 beams of 2.4 MB take 1507 us, of 8 bytes 401.)
+template <int BEAMS, int COLUMNS, int WORDS>
 __global__ __launch_bounds__(kBeamThreads) void reorder_kernel(const ReorderArgs p) {
+  constexpr int BYTES = 4 * WORDS;
+  using U = std::conditional_t<WORDS == 4, U32x4, U32x2>;
   int k = 0;
   while (k + 1 < p.caches && static_cast<int64_t>(blockIdx.x) >= p.c[k + 1].block0) ++k;
   const ReorderCache& c = p.c[k];
-  const int64_t at = ((static_cast<int64_t>(blockIdx.x) - c.block0) * COLUMNS * kBeamThreads + threadIdx.x) * 16;
+  const int64_t at = ((static_cast<int64_t>(blockIdx.x) - c.block0) * COLUMNS * kBeamThreads + threadIdx.x) * BYTES;
   for (int64_t b = blockIdx.y; b < p.batch; b += gridDim.y) {
     const int32_t* parents = p.parents + b * p.beams;
     auto slot_of = [&](int i) -> int64_t { return p.slots ? p.slots[b * p.beams + i] : b * p.beams + i; };
-    U32x4 v[BEAMS][COLUMNS];
+    U v[BEAMS][COLUMNS];
     uint64_t moves = 0;
 #pragma unroll
     for (int i = 0; i < BEAMS; ++i) {
@@ -423,16 +430,18 @@ __global__ __launch_bounds__(kBeamThreads) void reorder_kernel(const ReorderArgs
       moves |= 1ull << i;
 #pragma unroll
       for (int j = 0; j < COLUMNS; ++j) {
-        const int64_t first = at + j * kBeamThreads * 16, left = c.bytes - first;
+        const int64_t first = at + j * kBeamThreads * BYTES, left = c.bytes - first;
         const char* q = c.data + src * c.stride + first;
-        if (left >= 16) {
-          v[i][j] = *reinterpret_cast<const Words<1>::U4*>(q);
+        if (left >= BYTES) {
+          if constexpr (WORDS == 4) v[i][j] = *reinterpret_cast<const Words<1>::U4*>(q);
+          else v[i][j] = *reinterpret_cast<const Words<1>::U2*>(q);
         } else if (left > 0) {
-          uint32_t w[4] = {0u, 0u, 0u, 0u};
+          uint32_t w[WORDS] = {};
 #pragma unroll
-          for (int e = 0; e < 16; ++e)
+          for (int e = 0; e < BYTES; ++e)
             if (e < left) w[e >> 2] |= static_cast<uint32_t>(static_cast<uint8_t>(q[e])) << (8 * (e & 3));
-          v[i][j] = U32x4{w[0], w[1], w[2], w[3]};
+#pragma unroll
+          for (int e = 0; e < WORDS; ++e) v[i][j][e] = w[e];
         }
       }
     }
@@ -441,13 +450,14 @@ __global__ __launch_bounds__(kBeamThreads) void reorder_kernel(const ReorderArgs
       if (!(moves >> i & 1)) continue;
 #pragma unroll
       for (int j = 0; j < COLUMNS; ++j) {
-        const int64_t first = at + j * kBeamThreads * 16, left = c.bytes - first;
+        const int64_t first = at + j * kBeamThreads * BYTES, left = c.bytes - first;
         char* q = c.data + slot_of(i) * c.stride + first;
-        if (left >= 16) {
-          __builtin_nontemporal_store(v[i][j], reinterpret_cast<Words<1>::U4*>(q));
+        if (left >= BYTES) {
+          if constexpr (WORDS == 4) __builtin_nontemporal_store(v[i][j], reinterpret_cast<Words<1>::U4*>(q));
+          else __builtin_nontemporal_store(v[i][j], reinterpret_cast<Words<1>::U2*>(q));
         } else if (left > 0) {
 #pragma unroll
-          for (int e = 0; e < 16; ++e)
+          for (int e = 0; e < BYTES; ++e)
             if (e < left) q[e] = static_cast<char>(v[i][j][e >> 2] >> (8 * (e & 3)));
         }
       }

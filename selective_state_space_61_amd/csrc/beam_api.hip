@@ -45,15 +45,15 @@ struct Reorder {
   void (*kernel)(const ssm::ReorderArgs);
   int64_t bytes;  // of an entry that a workgroup takes
 };
-template <int BEAMS, int COLUMNS>
+template <int BEAMS, int COLUMNS, int WORDS>
 constexpr Reorder reorder_with() {
-  return {ssm::reorder_kernel<BEAMS, COLUMNS>, int64_t{COLUMNS} * ssm::kBeamThreads * 16};
+  return {ssm::reorder_kernel<BEAMS, COLUMNS, WORDS>, int64_t{4} * WORDS * COLUMNS * ssm::kBeamThreads};
 }
 Reorder reorder_of(int64_t beams) {
-  return beams <= 4 ? reorder_with<4, 2>()
-                    : beams <= 8 ? reorder_with<8, 2>()
-                                 : beams <= 16 ? reorder_with<16, 1>()
-                                               : beams <= 32 ? reorder_with<32, 1>() : reorder_with<64, 1>();
+  return beams <= 4 ? reorder_with<4, 2, 4>()
+                    : beams <= 8 ? reorder_with<8, 2, 4>()
+                                 : beams <= 16 ? reorder_with<16, 1, 4>()
+                                               : beams <= 32 ? reorder_with<32, 1, 4>() : reorder_with<64, 1, 2>();
 }
 
 }  // namespace
@@ -132,6 +132,7 @@ ssm_status_t ssm_cache_reorder(int64_t batch, int64_t beams, const ssm_entries_t
   if (beams > ssm::kBeamMost)
     return fail(SSM_ERR_UNSUPPORTED, "more than %d beams (%lld)", ssm::kBeamMost, (long long)beams);
   if (count > 0 && !caches) return fail(SSM_ERR_INVALID_ARG, "NULL caches");
+  const Reorder k = reorder_of(beams);
   uintptr_t last = 0;  // the highest address so far: layers mostly come in the order of their addresses
   for (int64_t i = 0; i < count; ++i) {
     const ssm_entries_t& c = caches[i];
@@ -146,7 +147,7 @@ ssm_status_t ssm_cache_reorder(int64_t batch, int64_t beams, const ssm_entries_t
       return fail(SSM_ERR_INVALID_ARG, "cache %lld: bad slots (%lld), bytes (%lld) or slot_stride (%lld)", (long long)i,
                   (long long)c.slots, (long long)c.bytes, (long long)c.slot_stride);
     if (!c.data && c.slots > 0 && c.bytes > 0) return fail(SSM_ERR_INVALID_ARG, "NULL cache data (%lld)", (long long)i);
-    if ((c.bytes + 15) / 16 / ssm::kBeamThreads >= kMaxBlocks / ssm::kReorderCaches)
+    if (c.bytes / k.bytes >= kMaxBlocks / ssm::kReorderCaches)
       return fail(SSM_ERR_UNSUPPORTED, "grid too large");
     const Range r{c.data, c.slots > 0 ? (c.slots - 1) * stride + c.bytes : 0};
     if (overlap(r, {parents, batch * beams * 4}) || overlap(r, {cache_slots, batch * beams * 4}))
@@ -159,7 +160,6 @@ ssm_status_t ssm_cache_reorder(int64_t batch, int64_t beams, const ssm_entries_t
   if (!parents) return fail(SSM_ERR_INVALID_ARG, "NULL parents");
   if (!aligned(parents, 4) || !aligned(cache_slots, 4))
     return fail(SSM_ERR_MISALIGNED, "parents or cache_slots is not 4-byte aligned");
-  const Reorder k = reorder_of(beams);
   for (int64_t i = 0; i < count;) {
     ssm::ReorderArgs a{};
     a.slots = cache_slots; a.parents = parents; a.batch = batch; a.beams = static_cast<int32_t>(beams);
