@@ -58,7 +58,7 @@ ssm_status_t cut_rows(const Tiled& t, int64_t sequences, int64_t seqlen, int64_t
   int64_t n;
   if (!mul_ok(chains_of(dim), out->tiles, &n) || n > kMaxBlocks) return fail(SSM_ERR_UNSUPPORTED, "grid too large");
   if (out->tiles <= 1 || whole) return SSM_OK;
-  out->maps = 16;  // the ticket's line
+  out->maps = int64_t{ssm::kGatedQueues} * ssm::kGatedQueueWords * 4;  // behind the queues' counters
   if (!mul_ok(out->tiles, dim, &n) || !mul_ok(n, 12, &n) || __builtin_add_overflow(n, out->maps + 15, &n))
     return fail(SSM_ERR_INVALID_ARG, "workspace size overflows int64");
   out->published = n / 16 * 16;

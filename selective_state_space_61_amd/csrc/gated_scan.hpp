@@ -12,9 +12,9 @@
 // entered.  Each tile publishes its map as soon as it has it and its end state once it knows the
 // entering one, and looks back over the maps of the tiles before it to the nearest end state
 // (the look-back of Merrill and Garland, "Single-pass parallel prefix scan with decoupled look-back").
-//  - Every wait ends: tiles are taken by tickets in the order of the axis, so that a tile waits only for
-//    tiles that running workgroups have taken before it, the first tile waits for none, and a waiting
-//    wave leaves its SIMD to others.
+//  - Every wait ends: a channel's tiles are in one queue and taken from it in the order of the axis, so that a
+//    tile waits only for tiles that running workgroups have taken before it, the first tile waits for none, and
+//    a waiting wave leaves its SIMD to others.
 //  - Results do not depend on timing: whoever computes the end state of a tile does it by the same
 //    operation, fma(A, entering state, B), from the same two words.
 //  - No fences: a published word is written once, by a relaxed atomic store at agent scope (a state is 32
@@ -29,6 +29,7 @@ constexpr int kGatedThreads = 256;
 constexpr int kGatedChannels = 64;   // channels of a workgroup: one 128-byte line of a bf16 row
 constexpr uint32_t kEmpty = 0xffffffffu;
 constexpr int kGatedSave = 64;       // rows between checkpoints
+constexpr uint32_t kGatedQueues = 4, kGatedQueueWords = 32;  // queues of tiles, and words from a counter to the next
 
 struct GatedArgs {
   const void *x, *ag, *xg, *z;
@@ -44,7 +45,7 @@ struct GatedArgs {
   CacheRef in, out;              // initial and final states by slot
   int32_t cb16;                  // they are bf16
   float* ckpt;                   // state after every kGatedSave-th row
-  uint32_t* ticket;              // NULL: no tile enters another
+  uint32_t* ticket;              // the queues' counters (NULL: no tile enters another)
   uint64_t* maps;                // (tiles, dim), in the order in which tiles are taken
   uint32_t* ends;
   int64_t tiles, each;           // tiles, and those of a sequence if none holds rows of two (else 0)
@@ -349,12 +350,15 @@ struct PartMaps {
   uint8_t own[PARTS];  // the part holds a state of its own
 };
 
-// The tile that a workgroup takes: the next one.  Tiles of a sequence that share no row with another come in the
-// order (their place in the sequence, sequence, channels), so that a tile waits for one that was taken a batch
+// The tile that a workgroup takes: the next one of a queue.  Tiles of a sequence that share no row with another come
+// in the order (their place in the sequence, sequence, channels), so that a tile waits for one that was taken a batch
 // earlier: 8 x 2048 x 1536 bf16 rows take 10% less forward than in the order of the rows, and 15% less backward.
-// (A counter for each block of channels in place of one for all: one sequence of 30011 x 2560 takes 8% and 10%
-// more, since the blocks' rows drift apart.  Workgroups that stay and take tile after
-// tile with the next number asked for ahead: half as much again, since the tile that a number stands for waits.)
+// The channels are shared among four queues, which the XCDs take from in turn: neighbouring channels, whose lines
+// may be the same, stay on few XCDs, and fewer workgroups ask for one counter.  With 1, 2, 4 and 8 queues 8 x 2048 x
+// 1536 take 72, 69, 68 and 68 us forward and 122, 119, 118 and 119 backward; 30011 x 2560 180, 180, 179, 185 and 337,
+// 341, 344, 357 (the queues' rows drift apart); 30000 x 256 71, 66, 63, 63 and 144, 136, 129, 129.
+// (Workgroups that stay and take tile after tile with the next number asked for ahead: half as much again, since the
+// tile that a number stands for waits.)
 struct Turn {
   uint32_t block, turn;  // in the order in which tiles are taken
   uint32_t before;       // tiles before it that may enter it
@@ -363,18 +367,31 @@ struct Turn {
   int64_t row0;          // its first row
   int64_t end;           // where its rows end at the latest
   template <int ROWS>
-  __device__ __forceinline__ static Turn take(const GatedArgs& p, uint32_t* shared, bool backward) {
+  __device__ __forceinline__ static Turn take(const GatedArgs& p, uint32_t (&shared)[2], bool backward) {
     Turn t;
-    uint32_t n = blockIdx.x;
+    const uint32_t tiles = static_cast<uint32_t>(p.tiles), chains = static_cast<uint32_t>(p.chains);
+    uint32_t n = blockIdx.x, first = 0, width = chains;
     if (p.ticket) {
-      if (threadIdx.x == 0)
-        *shared = __hip_atomic_fetch_add(p.ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) + 1u;  // (cleared to ~0)
+      const uint32_t groups = chains < kGatedQueues ? chains : kGatedQueues;
+      if (threadIdx.x == 0) {
+        // Workgroups are as many as tiles and take one each, so a queue with one left is found within a round
+        uint32_t g = n % kGatedQueues % groups, k;
+        while (true) {
+          k = __hip_atomic_fetch_add(p.ticket + g * kGatedQueueWords, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) + 1u;  // (from ~0)
+          if (k < ((g + 1) * chains / groups - g * chains / groups) * tiles) break;
+          g = g + 1 < groups ? g + 1 : 0;
+        }
+        shared[0] = k;
+        shared[1] = g;
+      }
       __syncthreads();
-      n = __builtin_amdgcn_readfirstlane(*shared);
+      n = __builtin_amdgcn_readfirstlane(shared[0]);
+      const uint32_t g = __builtin_amdgcn_readfirstlane(shared[1]);
+      first = g * chains / groups;
+      width = (g + 1) * chains / groups - first;
     }
-    t.turn = n / static_cast<uint32_t>(p.chains);
-    t.block = n - t.turn * static_cast<uint32_t>(p.chains);
-    const uint32_t tiles = static_cast<uint32_t>(p.tiles);
+    t.turn = n / width;
+    t.block = first + n - t.turn * width;
     if (p.each) {
       const uint32_t each = static_cast<uint32_t>(p.each), batch = static_cast<uint32_t>(p.nseq);
       const uint32_t place = t.turn / batch;
@@ -410,8 +427,8 @@ __global__ __launch_bounds__(kGatedThreads) void gated_scan_kernel(const GatedAr
   __shared__ TileRows<S::kRows> rows;
   __shared__ PartMaps<S::kParts> maps;
   __shared__ float entering[kGatedChannels], rate[kGatedChannels];
-  __shared__ uint32_t ticket;
-  const Turn tile = Turn::take<S::kRows>(p, &ticket, false);
+  __shared__ uint32_t ticket[2];
+  const Turn tile = Turn::take<S::kRows>(p, ticket, false);
   const Channels<V> ch(tile.block, p.dim);
   const int lane = threadIdx.x % S::kLanes, part = threadIdx.x / S::kLanes, at0 = part * R;
   const int64_t tile0 = tile.row0, d = ch.of(lane);
@@ -617,8 +634,8 @@ __global__ __launch_bounds__(kGatedThreads, 3) void gated_scan_bwd_kernel(const 
   __shared__ uint8_t ends[S::kParts];  // the part holds a sequence's last row
   __shared__ float rate[kGatedChannels];
   __shared__ float starts[S::kRows][kGatedChannels];  // where a sequence begins: its initial state, then that one's gradient
-  __shared__ uint32_t ticket;
-  const Turn tile = Turn::take<S::kRows>(p, &ticket, true);
+  __shared__ uint32_t ticket[2];
+  const Turn tile = Turn::take<S::kRows>(p, ticket, true);
   const Channels<V> ch(tile.block, p.dim);
   const int lane = threadIdx.x % S::kLanes, part = threadIdx.x / S::kLanes, at0 = part * R, wave = threadIdx.x / 64;
   const int64_t tile0 = tile.row0, d = ch.of(lane);
