@@ -28,7 +28,8 @@ Tiled backward_of(bool z) {
           ssm::GatedShape<V, R>::kRows};
 }
 
-// The forward's shape: 8 bytes of a bf16 row or of an fp32 row a lane.  Single channels where dim has fewer.
+// The forward's shape: 8 bytes of a bf16 row or of an fp32 row a lane; the backward's two channels of 64 rows, what
+// its registers hold.  Single channels where dim has fewer.
 Tiled forward_kernel(bool bf16, int64_t dim, bool z) {
   if (dim < 4) return bf16 ? forward_of<true, 1, 8>(z) : forward_of<false, 1, 8>(z);
   return bf16 ? forward_of<true, 4, 8>(z) : forward_of<false, 2, 8>(z);

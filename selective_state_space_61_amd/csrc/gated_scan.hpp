@@ -421,6 +421,10 @@ __device__ __forceinline__ int64_t checkpoint_after(const GatedArgs& p, const Tu
   return n + from / kGatedSave - 1;
 }
 
+// Forward.  Bound by the memory, as far as loading, composing, waiting and storing of three workgroups a CU overlap:
+// 8 x 2048 x 1536 bf16 take 64 us (251 MB, 3.9 TB/s, VALU 53% busy), 30011 x 2560 182 (4.2 TB/s), 12288 x 5120 packed
+// columns of a wider tensor 162 (5.2 TB/s of what it reads: rows that begin anywhere share lines).  Tiles of 128 rows
+// and 64 channels: of half the rows 30% slower, workgroups of 384 or 512 threads 20% and more.
 template <bool BF16, bool Z, int V, int R>
 __global__ __launch_bounds__(kGatedThreads) void gated_scan_kernel(const GatedArgs p) {
   using S = GatedShape<V, R>;
@@ -601,6 +605,8 @@ __global__ __launch_bounds__(kGatedThreads) void gated_scan_kernel(const GatedAr
 // E is 0 where w is (a = 1): l / w -> 0 as l -> 0, so the product has that limit though dw/dl has none.
 // The states come from the checkpoint before the tile and the tile's own rows; a G is carried from tile
 // to tile like the forward's state, tiles taken from the last one on.
+// Bound like the forward: 8 x 2048 x 1536 bf16 take 104 us (453 MB, 4.4 TB/s, VALU 61% busy), 30011 x 2560 329 (4.2
+// TB/s); with the arithmetic taken out the loads and stores alone took nine tenths of the time.
 
 // Stores the sum over all rows of quantity k: E (da_param), da_gate (da_bias) or dx_gate (dx_bias).
 __device__ __forceinline__ void store_sum(int k, int64_t d, float s, const float* param, float* dparam, float* dab, float* dxb) {
@@ -942,7 +948,8 @@ __device__ __forceinline__ void store_from(void* base, int64_t idx, int skip, co
   }
 }
 
-// One token on a cache: a thread owns V channels of R entries.
+// One token on a cache: a thread owns V channels of R entries.  250 x 5120 on a bf16 cache take 9.6 us (launch, one
+// round trip to the memory and 18 MB), less than the call on the host.
 struct GatedStepArgs {
   GatedArgs g;      // rows are the batch's entries; in: the cache
   int64_t batch;
