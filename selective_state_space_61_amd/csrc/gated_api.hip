@@ -46,7 +46,7 @@ Tiled backward_kernel(bool bf16, int64_t dim, bool z) {
 // (0 where no tile enters another).
 constexpr int64_t kOwnTiles = 256;  // rows of a sequence from which on it has tiles of its own
 struct Cut {
-  int64_t tiles, each, pitch, published, maps;  // each: of a sequence (0: shared); maps: where they begin
+  int64_t tiles, each, pitch, published, words;  // each: of a sequence (0: shared); words: where they begin
 };
 int64_t chains_of(int64_t dim) { return (dim + ssm::kGatedChannels - 1) / ssm::kGatedChannels; }
 ssm_status_t cut_rows(const Tiled& t, int64_t sequences, int64_t seqlen, int64_t rows, int64_t dim, Cut* out) {
@@ -59,8 +59,8 @@ ssm_status_t cut_rows(const Tiled& t, int64_t sequences, int64_t seqlen, int64_t
   int64_t n;
   if (!mul_ok(chains_of(dim), out->tiles, &n) || n > kMaxBlocks) return fail(SSM_ERR_UNSUPPORTED, "grid too large");
   if (out->tiles <= 1 || whole) return SSM_OK;
-  out->maps = int64_t{ssm::kGatedQueues} * ssm::kGatedQueueWords * 4;  // behind the queues' counters
-  if (!mul_ok(out->tiles, dim, &n) || !mul_ok(n, 12, &n) || __builtin_add_overflow(n, out->maps + 15, &n))
+  out->words = int64_t{ssm::kGatedQueues} * ssm::kGatedQueueWords * 4;  // behind the queues' counters
+  if (!mul_ok(out->tiles, dim, &n) || !mul_ok(n, 8, &n) || __builtin_add_overflow(n, out->words + 15, &n))
     return fail(SSM_ERR_INVALID_ARG, "workspace size overflows int64");
   out->published = n / 16 * 16;
   return SSM_OK;
@@ -124,8 +124,7 @@ ssm_status_t launch_tiles(const Tiled& t, ssm::GatedArgs& a, const Cut& cut, voi
   if (cut.published) {
     char* w = static_cast<char*>(workspace);
     a.ticket = reinterpret_cast<uint32_t*>(w);
-    a.maps = reinterpret_cast<uint64_t*>(w + cut.maps);
-    a.ends = reinterpret_cast<uint32_t*>(a.maps + cut.tiles * a.dim);
+    a.words = reinterpret_cast<uint64_t*>(w + cut.words);
     hipLaunchKernelGGL(ssm::gated_clear_kernel, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, st,
                        reinterpret_cast<ssm::U32x4*>(w), words);
     SSM_TRY(check_launch("gated scan (clear)"));

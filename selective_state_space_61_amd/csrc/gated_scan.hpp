@@ -17,8 +17,8 @@
 //    a waiting wave leaves its SIMD to others.
 //  - Results do not depend on timing: whoever computes the end state of a tile does it by the same
 //    operation, fma(A, entering state, B), from the same two words.
-//  - No fences: a published word is written once, by a relaxed atomic store at agent scope (a state is 32
-//    bits, a map 64), over a pattern that no published word has, and is itself the sign of its arrival.
+//  - No fences: what a tile publishes is one 64-bit word a channel, written by relaxed atomic stores at agent scope,
+//    and is itself the sign of its arrival.
 #pragma once
 
 #include "cache.hpp"
@@ -27,7 +27,6 @@ namespace ssm {
 
 constexpr int kGatedThreads = 256;
 constexpr int kGatedChannels = 64;   // channels of a workgroup: one 128-byte line of a bf16 row
-constexpr uint32_t kEmpty = 0xffffffffu;
 constexpr int kGatedSave = 64;       // rows between checkpoints
 constexpr uint32_t kGatedQueues = 4, kGatedQueueWords = 32;  // queues of tiles, and words from a counter to the next
 
@@ -46,8 +45,7 @@ struct GatedArgs {
   int32_t cb16;                  // they are bf16
   float* ckpt;                   // state after every kGatedSave-th row
   uint32_t* ticket;              // the queues' counters (NULL: no tile enters another)
-  uint64_t* maps;                // (tiles, dim), in the order in which tiles are taken
-  uint32_t* ends;
+  uint64_t* words;               // (tiles, dim), in the order in which tiles are taken
   int64_t tiles, each;           // tiles, and those of a sequence if none holds rows of two (else 0)
   int64_t pitch;                 // rows from a tile to the next, if tiles hold rows of several
   int32_t chains;                // blocks of kGatedChannels channels
@@ -68,61 +66,53 @@ struct GatedShape {
   static constexpr int kRows = kParts * R;               // rows of a tile
 };
 
-__device__ __forceinline__ void publish(uint32_t* p, float v) {
-  uint32_t b = __builtin_bit_cast(uint32_t, v);
-  b = b == kEmpty ? 0x7fc00000u : b;
-  __hip_atomic_store(p, b, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+// A tile's word: nothing yet (all ones), then its map, then its end state.  A map's factor is in the low half, an end
+// state in the high half above kEnd, which is no factor's.
+constexpr uint32_t kEmpty = 0xffffffffu, kEnd = 0xfffffffeu;
+__device__ __forceinline__ void publish(uint64_t* p, uint32_t lo, float hi) {
+  __hip_atomic_store(p, (static_cast<uint64_t>(__builtin_bit_cast(uint32_t, hi)) << 32) | lo, __ATOMIC_RELAXED,
+                     __HIP_MEMORY_SCOPE_AGENT);
 }
-__device__ __forceinline__ void publish(uint64_t* p, float a, float b) {
-  uint32_t lo = __builtin_bit_cast(uint32_t, a);
-  const uint32_t hi = __builtin_bit_cast(uint32_t, b);
-  lo = lo == kEmpty && hi == kEmpty ? 0x7fc00000u : lo;
-  __hip_atomic_store(p, (static_cast<uint64_t>(hi) << 32) | lo, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+__device__ __forceinline__ void publish_end(uint64_t* p, float h) { publish(p, kEnd, h); }
+__device__ __forceinline__ void publish_map(uint64_t* p, float a, float b) {
+  const uint32_t lo = __builtin_bit_cast(uint32_t, a);
+  publish(p, lo >= kEnd ? 0x7fc00000u : lo, b);  // (those are NaNs)
 }
 
-// The state that leaves the tile before this one.  maps and ends point at that tile's words; those of the tiles
-// before it lie `step` elements on each, `first` tiles in all.  WINDOW tiles' words are asked for at once, as
-// many as leave the kernels' registers in place: forward with 4 and 8, 30000 x 256 bf16 rows take 74 and 61 us,
-// but 12288 x 5120 packed ones 170 and 175; backward with 2, 3 and 4, 30011 x 2560 take 351, 341 and 341 us, 8 x
-// 2048 x 1536 120, 121 and 124 (spilled registers; in fp32 3 spills too).
+// The state that leaves the tile before this one.  words points at that tile's; those of the tiles before it lie
+// `step` elements on each, `first` tiles in all.  WINDOW tiles' words are asked for at once, as many as leave the
+// kernels' registers in place: forward with 4 and 8, 30000 x 256 bf16 rows take 56 and 43 us, but 8 x 2048 x 1536
+// 67 and 69 and 12288 x 5120 packed ones 162 and 165; backward with 3, 4 and 5 30000 x 256 take 117, 101 and 91 us,
+// 2000 x 40 x 1024 403, 408 and 425, and in fp32 with 2 and 3 400 x 33 x 1000 133 and 139.
 // Every lane of the wave calls it; lanes with `on` false (no channel, or nothing enters) get 0.
 template <int WINDOW>
-__device__ __forceinline__ float look_back(const uint64_t* maps, const uint32_t* ends, int64_t step, int64_t first,
-                                           bool on) {
+__device__ __forceinline__ float look_back(const uint64_t* words, int64_t step, int64_t first, bool on) {
   float h = 0.0f;
   bool done = !on;
   while (!__all(done)) {
     if (!done) {
-      uint32_t e[WINDOW];
-      uint64_t m[WINDOW - 1];
+      uint64_t w[WINDOW];
 #pragma unroll
-      for (int k = 0; k < WINDOW; ++k) {
-        // before the first tile the state is 0
-        e[k] = k < first ? __hip_atomic_load(ends + k * step, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : 0u;
-        if (k < WINDOW - 1)
-          m[k] = k < first ? __hip_atomic_load(maps + k * step, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : 0u;
-      }
+      for (int k = 0; k < WINDOW; ++k)  // before the first tile the state is 0
+        w[k] = k < first ? __hip_atomic_load(words + k * step, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : uint64_t{kEnd};
       int near = 0;  // tiles over whose maps the nearest end state comes here
       bool open = true;
 #pragma unroll
       for (int k = 0; k < WINDOW; ++k) {
-        if (open && e[k] != kEmpty) {
+        const uint32_t lo = static_cast<uint32_t>(w[k]);
+        if (open && lo == kEnd) {
           done = true;
-          open = false;
           near = k;
         }
-        if (k < WINDOW - 1 && m[k] == ~0ull) open = false;
+        open = open && lo < kEnd;
       }
       if (done) {
 #pragma unroll
         for (int k = WINDOW - 1; k >= 0; --k) {
-          if (k == near) {
-            h = __builtin_bit_cast(float, e[k]);
-          } else if (k < WINDOW - 1) {
-            const float a = __builtin_bit_cast(float, static_cast<uint32_t>(m[k]));
-            const float b = __builtin_bit_cast(float, static_cast<uint32_t>(m[k] >> 32));
-            if (k < near) h = fmaf(a, h, b);
-          }
+          const float a = __builtin_bit_cast(float, static_cast<uint32_t>(w[k]));
+          const float b = __builtin_bit_cast(float, static_cast<uint32_t>(w[k] >> 32));
+          if (k == near) h = b;
+          else if (k < near) h = fmaf(a, h, b);
         }
       }
     }
@@ -356,7 +346,8 @@ struct PartMaps {
 // The channels are shared among four queues, which the XCDs take from in turn: neighbouring channels, whose lines
 // may be the same, stay on few XCDs, and fewer workgroups ask for one counter.  With 1, 2, 4 and 8 queues 8 x 2048 x
 // 1536 take 72, 69, 68 and 68 us forward and 122, 119, 118 and 119 backward; 30011 x 2560 180, 180, 179, 185 and 337,
-// 341, 344, 357 (the queues' rows drift apart); 30000 x 256 71, 66, 63, 63 and 144, 136, 129, 129.
+// 341, 344, 357 (the queues' rows drift apart); 30000 x 256 10% less each with 4 than
+// with 1.
 // (Workgroups that stay and take tile after tile with the next number asked for ahead: half as much again, since the
 // tile that a number stands for waits.)
 struct Turn {
@@ -526,10 +517,10 @@ __global__ __launch_bounds__(kGatedThreads) void gated_scan_kernel(const GatedAr
       float h = 0.0f;
       if (p.ticket) {
         const int64_t at = tile.turn * p.dim + ch.of(c / V) + c % V, step = -(tile.apart * p.dim);
-        if (on && !own) publish(p.maps + at, ta, tb);
-        if (on && own) publish(p.ends + at, tb);
-        h = look_back<4>(p.maps + at + step, p.ends + at + step, step, tile.before, on && !(EDGES && (rows.first[0] & 1)));
-        if (on && !own) publish(p.ends + at, fmaf(ta, h, tb));
+        if (on && !own) publish_map(p.words + at, ta, tb);
+        if (on && own) publish_end(p.words + at, tb);
+        h = look_back<4>(p.words + at + step, step, tile.before, on && !(EDGES && (rows.first[0] & 1)));
+        if (on && !own) publish_end(p.words + at, fmaf(ta, h, tb));
       }
       entering[c] = h;
     }
@@ -774,10 +765,10 @@ __global__ __launch_bounds__(kGatedThreads, 3) void gated_scan_bwd_kernel(const 
         float s = 0.0f;
         if (p.ticket) {
           const int64_t at = tile.turn * p.dim + dc, step = -(tile.apart * p.dim);
-          if (on && !own) publish(p.maps + at, ta, tb);
-          if (on && own) publish(p.ends + at, tb);
-          s = look_back<BF16 ? 3 : 2>(p.maps + at + step, p.ends + at + step, step, tile.before, on && !(EDGES && (rows.last[0] >> 63)));
-          if (on && !own) publish(p.ends + at, fmaf(ta, s, tb));
+          if (on && !own) publish_map(p.words + at, ta, tb);
+          if (on && own) publish_end(p.words + at, tb);
+          s = look_back<BF16 ? 3 : 2>(p.words + at + step, step, tile.before, on && !(EDGES && (rows.last[0] >> 63)));
+          if (on && !own) publish_end(p.words + at, fmaf(ta, s, tb));
         }
 #pragma unroll
         for (int q = S::kParts - 1; q >= 0; --q) {
