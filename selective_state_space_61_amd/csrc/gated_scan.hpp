@@ -346,8 +346,7 @@ struct PartMaps {
 // The channels are shared among four queues, which the XCDs take from in turn: neighbouring channels, whose lines
 // may be the same, stay on few XCDs, and fewer workgroups ask for one counter.  With 1, 2, 4 and 8 queues 8 x 2048 x
 // 1536 take 72, 69, 68 and 68 us forward and 122, 119, 118 and 119 backward; 30011 x 2560 180, 180, 179, 185 and 337,
-// 341, 344, 357 (the queues' rows drift apart); 30000 x 256 10% less each with 4 than
-// with 1.
+// 341, 344, 357 (the queues' rows drift apart); 30000 x 256 10% less each with 4 than with 1.
 // (Workgroups that stay and take tile after tile with the next number asked for ahead: half as much again, since the
 // tile that a number stands for waits.)
 struct Turn {
@@ -413,8 +412,8 @@ __device__ __forceinline__ int64_t checkpoint_after(const GatedArgs& p, const Tu
 }
 
 // Forward.  Bound by the memory, as far as loading, composing, waiting and storing of three workgroups a CU overlap:
-// 8 x 2048 x 1536 bf16 take 64 us (251 MB, 3.9 TB/s, VALU 53% busy), 30011 x 2560 182 (4.2 TB/s), 12288 x 5120 packed
-// columns of a wider tensor 162 (5.2 TB/s of what it reads: rows that begin anywhere share lines).  Tiles of 128 rows
+// 8 x 2048 x 1536 bf16 take 64 us (251 MB, 3.9 TB/s, VALU 53% busy), 30011 x 2560 179 (4.3 TB/s), 12288 x 5120 packed
+// columns of a wider tensor 160 (5.2 TB/s of what moves: rows that begin anywhere share lines).  Tiles of 128 rows
 // and 64 channels: of half the rows 30% slower, workgroups of 384 or 512 threads 20% and more.
 template <bool BF16, bool Z, int V, int R>
 __global__ __launch_bounds__(kGatedThreads) void gated_scan_kernel(const GatedArgs p) {

@@ -87,7 +87,8 @@ def test_batches(shape, dtype, z, states):
         R.check(v, val, ev, v.dtype, k)
 
 
-@pytest.mark.parametrize("shape", [(9, 40, 70), (11, 41, 33), (50, 2, 64), (13, 20, 130), (3, 128, 65), (3, 64, 66), (200, 31, 5)])
+@pytest.mark.parametrize("shape", [(9, 40, 70), (11, 41, 33), (50, 2, 64), (13, 20, 130), (3, 128, 65), (3, 64, 66), (200, 31, 5),
+                                   (70, 7, 3), (33, 11, 1), (9, 32, 2)])
 @pytest.mark.parametrize("dtype", [BF, F])
 def test_batches_of_short_sequences(shape, dtype):
     """Several whole sequences in a tile, forward, backward or both; the forward's checkpoints then lie anywhere in
