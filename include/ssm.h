@@ -856,8 +856,8 @@ typedef struct {
  *
  * beams is 1..64.  A beam without a slot (negative, or past the cache's slots),
  * of a parent out of range or without a slot, or that is its own parent keeps
- * its entry.  Each entry that is some other beam's parent is read once and each
- * one that changes written once.
+ * its entry.  Nothing is copied aside: each entry that changes is written once, and
+ * those that are some other beam's parent are read.
  */
 SSM_API ssm_status_t ssm_cache_reorder(int64_t batch, int64_t beams, const ssm_entries_t *caches, int64_t count,
                                        const int32_t *cache_slots, const int32_t *parents, void *stream);
