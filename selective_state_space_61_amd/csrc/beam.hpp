@@ -342,7 +342,8 @@ __global__ __launch_bounds__(1024) static void beam_join_kernel(const BeamArgs p
     const int32_t t = static_cast<int32_t>(0xffffffffu - static_cast<uint32_t>(mine));
     int rank = lane;
     // by value now: logits that differ may give one value, which then goes by the token
-    const bool tie = lane > 0 && lane < k && __shfl_up(v, 1) == v;
+    const double up = __shfl_up(v, 1);  // (by all lanes: one that is switched off gives its neighbour a 0)
+    const bool tie = lane > 0 && lane < k && up == v;
     if (__any(tie)) {
       rank = 0;
       for (int i = 0; i < k; ++i) {

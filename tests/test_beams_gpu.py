@@ -97,6 +97,25 @@ def test_ties_go_to_the_lowest(dtype, k):
 
 
 @pytest.mark.parametrize("dtype", [BF, F])
+@pytest.mark.parametrize("vocab", [6, 700, 9001])
+def test_equal_values_of_different_logits(dtype, vocab):
+    """Logits that differ by less than the value's last place in 64 bits: equal values, which go by the token, at
+    every rank that the pair may have, and where the cut falls between the two."""
+    for above in range(3):  # tokens with a larger logit
+        logits = torch.full((1, 2, vocab), -10.0, dtype=dtype)
+        logits[:, 0, 5], logits[:, 0, 3] = 2e-20, 1e-20
+        assert logits[0, 0, 5] > logits[0, 0, 3]
+        for i in range(above):
+            logits[:, 0, (4, 0)[i]] = 4.0 - i
+        logits[:, 1, 1] = 60.0  # a second row whose one candidate of a large value leaves the first k - 1 places
+        logits, scores = logits.cuda(), torch.tensor([[0.0, 20.0]]).cuda()
+        for k in range(2, 6):
+            one = logits[:, :1].contiguous(), scores[:, :1].contiguous()
+            check(ssm.ssm_beam_select(*one, k), select(*one, k), one[1])
+            check(ssm.ssm_beam_select(logits, scores, k), select(logits, scores, k), scores)
+
+
+@pytest.mark.parametrize("dtype", [BF, F])
 def test_rows_of_equal_values_tie_at_any_alignment(dtype):
     """An odd vocabulary puts each row at another alignment; equal rows have equal values all the same."""
     row = rand((1, 1, 20011), dtype, 3)[0][0, 0]
