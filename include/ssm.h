@@ -712,6 +712,9 @@ SSM_API ssm_status_t ssm_cache_load_q8(int64_t count, int64_t rows, int64_t dsta
  *
  * The rows are cut into tiles that run in parallel and hand each other their
  * states through the caller's workspace; the results do not depend on timing.
+ * A state (or, backward, an adjoint) that has become infinite stays infinite in
+ * tiles as step by step, unless the decay of one step rounds to zero, which
+ * makes it NaN.
  * workspace: at least ssm_gated_scan_workspace bytes, 16-byte aligned, the
  * caller's until the call's work is done (each call that may run at the same
  * time needs its own); may be NULL where that is 0.  Packed prompts need that of

@@ -332,6 +332,29 @@ __device__ __forceinline__ void no_row(Run<BF16, V>& r, bool off, bool closed) {
   for (int i = 0; i < Run<BF16, V>::kWords; ++i) r.w[i] = off ? (closed ? (BF16 ? 0xff80ff80u : 0xff800000u) : 0u) : r.w[i];
 }
 
+// The decay of a stretch of steps, from the product of theirs and the least of them: 0 only if a step's is.  The
+// product alone rounds to 0 after a few dozen ordinary steps and would make a NaN of an infinite state that each of
+// them keeps, here or there as tiles happen to begin.  2^-149 in its place adds to a finite state what a rounding
+// would.  (No decay exceeds 1, so the product is at most the least and the middle one of the three is meant.)
+__device__ __forceinline__ float stretch_decay(float product, float least) {
+  return __builtin_amdgcn_fmed3f(product, least, 0x1p-149f);
+}
+__device__ __forceinline__ float compose_decay(float a, float b) { return stretch_decay(a * b, fminf(a, b)); }
+template <int V, int R>
+__device__ __forceinline__ void compose_decays(const float (&a)[R][V], float (&out)[V]) {
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    float least = a[0][v];
+    out[v] = a[0][v];
+#pragma unroll
+    for (int j = 1; j < R; ++j) {
+      out[v] *= a[j][v];
+      least = fminf(least, a[j][v]);
+    }
+    out[v] = stretch_decay(out[v], least);
+  }
+}
+
 // The maps of a channel's lanes in the LDS, then what enters each of them.
 template <int PARTS>
 struct PartMaps {
@@ -456,7 +479,6 @@ __global__ __launch_bounds__(kGatedThreads) void gated_scan_kernel(const GatedAr
     float a[R][V], b[R][V], A[V], B[V], kl[V], kp[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      A[v] = 1.0f;
       B[v] = 0.0f;
       kl[v] = rate[lane * V + v] * kLog2e;
       kp[v] = rate[lane * V + v] * -2.0f;
@@ -483,10 +505,8 @@ __global__ __launch_bounds__(kGatedThreads) void gated_scan_kernel(const GatedAr
 #pragma unroll
     for (int j = 0; j < R; ++j)
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
-        A[v] *= a[j][v];
-        B[v] = EDGES && (in.first >> j & 1) ? b[j][v] : fmaf(a[j][v], B[v], b[j][v]);
-      }
+      for (int v = 0; v < V; ++v) B[v] = EDGES && (in.first >> j & 1) ? b[j][v] : fmaf(a[j][v], B[v], b[j][v]);
+    compose_decays(a, A);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       maps.a[part][lane * V + v] = A[v];
@@ -510,7 +530,7 @@ __global__ __launch_bounds__(kGatedThreads) void gated_scan_kernel(const GatedAr
         maps.b[i][c] = tb;
         const bool starts = EDGES && maps.own[i];
         own |= starts;
-        ta *= pa;
+        ta = compose_decay(ta, pa);
         tb = starts ? pb : fmaf(pa, tb, pb);
       }
       float h = 0.0f;
@@ -711,14 +731,12 @@ __global__ __launch_bounds__(kGatedThreads, 3) void gated_scan_bwd_kernel(const 
     }
     float A[V], B[V], C[V];  // C: a G of the row that the part begins with
 #pragma unroll
-    for (int v = 0; v < V; ++v) A[v] = 1.0f, B[v] = C[v] = 0.0f;
+    for (int v = 0; v < V; ++v) B[v] = C[v] = 0.0f;
 #pragma unroll
     for (int j = 0; j < R; ++j)
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
-        A[v] *= a[j][v];
-        B[v] = EDGES && (in.first >> j & 1) ? h[j][v] : fmaf(a[j][v], B[v], h[j][v]);
-      }
+      for (int v = 0; v < V; ++v) B[v] = EDGES && (in.first >> j & 1) ? h[j][v] : fmaf(a[j][v], B[v], h[j][v]);
+    compose_decays(a, A);
 #pragma unroll
     for (int j = R - 1; j >= 0; --j)
 #pragma unroll
@@ -758,7 +776,7 @@ __global__ __launch_bounds__(kGatedThreads, 3) void gated_scan_bwd_kernel(const 
           const bool stops = EDGES && ends[q];
           const float pa = fwd.a[q][c], pb = back[q][c];
           own |= stops;
-          ta *= pa;
+          ta = compose_decay(ta, pa);
           tb = stops ? pb : fmaf(pa, tb, pb);
         }
         float s = 0.0f;

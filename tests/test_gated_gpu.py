@@ -11,6 +11,7 @@ from gpu_util import say
 
 pytestmark = pytest.mark.gpu
 BF, F = torch.bfloat16, torch.float32
+INF = float("inf")
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -310,6 +311,86 @@ def test_a_parameter_that_is_no_number():
         for clean, got in zip(*outs):
             assert torch.equal(clean[..., other], got[..., other])
             assert got[..., 3].isnan().all()
+
+
+def infinite_case(batch, rows, dim, dtype, seed, z=False):
+    """Channels whose decays of one step run from 0.99 to e^-85 (fp32's least normal number is e^-87.3): no step's is
+    0 in fp32, that of most stretches is.  All gates near 0.5 to 1, x of either sign."""
+    t = make((batch, rows, dim), dtype, seed, z=z, bias=False)
+    t["a_gate"], t["x_gate"] = t["a_gate"].abs(), t["x_gate"].abs()
+    rate = torch.logspace(-2, 1.02, dim, dtype=torch.float64)  # softplus(a_param): at most 10.5, times 8 at most 84
+    t["a_param"] = torch.log(torch.expm1(rate)).float().cuda()
+    return t
+
+
+def kinds(v):
+    """Each value's kind: finite 0, +inf 1, -inf 2, NaN 3."""
+    return (v == float("inf")).int() + 2 * (v == float("-inf")).int() + 3 * v.isnan().int()
+
+
+@pytest.mark.parametrize("batch,rows,dim", [(1, 700, 70), (3, 700, 65), (5, 40, 70), (3, 90, 70), (1, 1400, 5), (2, 300, 3), (2, 300, 1)])
+@pytest.mark.parametrize("dtype", [BF, F])
+def test_an_infinite_state_stays(batch, rows, dim, dtype):
+    """A state that has become infinite (by an input or from the start) stays so in batches, packed prompts and their
+    states, wherever stretches and tiles begin, as it does token by token; and so does an infinite adjoint."""
+    say(f"[case] gated infinite {batch} x {rows} x {dim} {dtype}")
+    t = infinite_case(batch, rows, dim, dtype, dim)
+    for at, sign in ((3, 1.0), (rows // 2, -1.0), (-1, 1.0)):
+        x = t["x"].clone()
+        h0 = torch.zeros(batch, dim, device="cuda")
+        if at < 0:
+            h0[0] = sign * INF
+        else:
+            x[0, at] = sign * INF
+        d = dict(t, x=x)
+        y, last, saved = ssm.ssm_gated_scan_fwd_ckpt(**d, initial_state=h0)
+        want = torch.zeros(batch, rows, dim, dtype=torch.int32, device="cuda")
+        want[0, max(at, 0):] = 1 if sign > 0 else 2
+        assert torch.equal(kinds(y), want) and torch.equal(kinds(last), want[:, -1]), at
+        kept = want[:, 63::64].reshape(-1, dim) if batch > 1 and rows >= 256 else want.view(-1, dim)[63::64]
+        assert torch.equal(kinds(saved), kept), at
+        flat = {k: (v.view(batch * rows, dim) if v is not None and v.dim() == 3 else v) for k, v in d.items()}
+        cu = torch.arange(0, batch * rows + 1, rows, dtype=torch.int32).cuda()
+        cache = h0.clone()
+        yp = ssm.ssm_gated_scan_packed_fwd(**flat, cu_seqlens=cu, cache=cache, has_initial=torch.ones(batch, dtype=torch.bool).cuda())
+        assert torch.equal(kinds(yp), want.view(-1, dim)) and torch.equal(kinds(cache), want[:, -1]), at
+        # the states that the backward works out again: dz is dy h silu'(z)
+        z, dy = torch.ones_like(x), torch.ones_like(x)
+        dz = ssm.ssm_gated_scan_bwd_ckpt(**dict(d, z=z), dy=dy, checkpoints=saved, initial_state=h0)["dz"]
+        assert torch.equal(kinds(dz), want), at
+        # an infinite gradient of the last state, or of a row
+        dlast = torch.zeros(batch, dim, device="cuda")
+        if at < 0:
+            dlast[0] = sign * INF
+        else:
+            dy[0, at] = sign * INF
+        fwd = ssm.ssm_gated_scan_fwd_ckpt(**t)
+        got = ssm.ssm_gated_scan_bwd_ckpt(**t, dy=dy, checkpoints=fwd[2], dlast_state=dlast, initial_state=torch.zeros_like(dlast))
+        want.zero_()
+        want[0, :at + 1 if at >= 0 else rows] = 1 if sign > 0 else 2
+        assert torch.equal(kinds(got["dx"]), want) and torch.equal(kinds(got["dinitial_state"]), want[:, 0]), at
+
+
+@pytest.mark.parametrize("dtype", [BF, F])
+def test_an_infinite_state_meets_a_step_without_decay_left(dtype):
+    """A step whose decay is 0 in fp32 makes an infinite state NaN, in a prompt at the same row as token by token,
+    whatever stretch or tile that row lies in; a finite state is forgotten."""
+    rows, dim, start = 420, 66, 50
+    for at in (51, 64, 130, 383):
+        t = infinite_case(1, rows, dim, dtype, at)
+        t["x"][0, start, ::2] = INF
+        t["a_gate"][0, at, ::3] = INF  # a rate of 1e3 on top of it: every such step's decay is 0
+        t["a_param"][::3] = 125.0
+        t["a_gate"][0, :, ::3][t["a_gate"][0, :, ::3] != INF] = -5.0  # (of 6.7 elsewhere: e^-6.7)
+        flat = {k: (v[0] if v is not None and v.dim() == 3 else v) for k, v in t.items()}
+        cu, cache = packed([rows])[0], torch.zeros(1, dim).cuda()
+        y = ssm.ssm_gated_scan_packed_fwd(**flat, cu_seqlens=cu, cache=cache)
+        alone = torch.zeros(1, dim).cuda()
+        ys = [ssm.ssm_gated_update_cache(alone, None, **{k: (v[n:n + 1] if v is not None and v.dim() == 2 else v)
+                                                         for k, v in flat.items()}) for n in range(rows)]
+        assert torch.equal(kinds(y), kinds(torch.cat(ys))) and torch.equal(kinds(cache), kinds(alone)), at
+        k = kinds(y)
+        assert (k[start:, 2::6] == 1).all() and (k[start:at, ::6] == 1).all() and (k[at:, ::6] == 3).all() and (k[:, 1::2] == 0).all()
 
 
 @pytest.mark.parametrize("dim,dtype,cdtype", [(66, BF, F), (65, BF, BF), (67, BF, F), (65, F, BF), (129, BF, BF), (194, BF, F)])
