@@ -708,7 +708,8 @@ SSM_API ssm_status_t ssm_cache_load_q8(int64_t count, int64_t rows, int64_t dsta
  * states are fp32 unless a cache is bf16.  The calls allocate nothing, keep
  * nothing between calls, enqueue kernels only and may be captured into a HIP
  * graph.  At most 2^31 - 1 rows (batch * seqlen, total or batch); dim and the
- * row strides of packed prompts are below 2^23 (else SSM_ERR_UNSUPPORTED).
+ * row strides of packed prompts of several rows are below 2^23 (else
+ * SSM_ERR_UNSUPPORTED).
  *
  * The rows are cut into tiles that run in parallel and hand each other their
  * states through the caller's workspace; the results do not depend on timing.

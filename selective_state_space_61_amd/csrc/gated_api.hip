@@ -298,9 +298,11 @@ ssm_status_t ssm_gated_scan_packed_fwd(const ssm_packed_t* seqs, int64_t dim, ss
   Rows t[] = {{x, dim, &rs.x, "x", 0}, {a_gate, dim, &rs.a_gate, "a_gate", 0}, {x_gate, dim, &rs.x_gate, "x_gate", 0},
               {z, dim, &rs.z, "z", 0}, {y, dim, &rs.y, "y", 0}};
   SSM_TRY(check_rows(t, 5, seqs->total, es));
-  for (const Rows& r : t)
+  for (const Rows& r : t) {
+    if (seqs->total <= 1) *r.stride = dim;  // there is no next row, whatever the distance to it
     if (*r.stride >= kMaxRowStride)
       return fail(SSM_ERR_UNSUPPORTED, "row stride %lld of %s is not below 2^23", (long long)*r.stride, r.name);
+  }
   if (seqs->total == 0 || seqs->sequences == 0 || dim == 0) return SSM_OK;
   if (!x || !a_gate || !x_gate || !a_param || !y)
     return fail(SSM_ERR_INVALID_ARG, "NULL required pointer (x, a_gate, x_gate, a_param and y)");

@@ -194,6 +194,23 @@ def test_packed(n, dtype, cdtype, dim):
     assert (wide_y[rest.cuda()] == 7).all() and (wide_y[:, :2] == 7).all() and (wide_y[:, 2 + dim:] == 7).all()
 
 
+@pytest.mark.parametrize("dtype", [BF, F])
+def test_one_row_of_a_large_projection(dtype):
+    """The last row of a long text's projections: its distance to the next row, which is not there, does not matter."""
+    dim, g = 72, torch.Generator().manual_seed(1)
+    whole = torch.randn((1, 2048, 5120), generator=g).to(dtype).cuda()
+    last = whole[:, -1]
+    cols = {k: last[:, n * dim:(n + 1) * dim] for n, k in enumerate(("x", "a_gate", "x_gate", "z"))}
+    assert cols["x"].stride(0) > 2 ** 23
+    param, cache = torch.full((dim,), -4.0).cuda(), torch.randn(1, dim, generator=g).cuda()
+    y = torch.empty((1, 2048, 5120), dtype=dtype, device="cuda")[:, -1, 8:8 + dim]
+    before, yes = cache.clone(), torch.ones(1, dtype=torch.bool).cuda()
+    ssm.ssm_gated_scan_packed_fwd(**cols, a_param=param, cu_seqlens=packed([1])[0], cache=cache, has_initial=yes, y=y)
+    yr, ey, h, eh = R.forward(**host(dict(cols, a_param=param, a_bias=None, x_bias=None)), h0=R.f64(before[0]))
+    R.check(y, yr, ey, dtype, "y")
+    R.check(cache[0], h[-1], eh[-1], F, "state")
+
+
 def test_packed_without_a_cache_is_the_batch():
     """Equal lengths packed are the rows of a batch: the same tiles, the same bits."""
     t = make((6, 90, 100), BF, 4)

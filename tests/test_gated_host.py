@@ -119,6 +119,16 @@ def test_row_strides(lib, call, name):  # noqa: F811
         assert call(lib, st=ssm.GatedStrides(**{name: 1 << 23})) == UNSUPPORTED
 
 
+@pytest.mark.parametrize("name", ["x", "a_gate", "x_gate", "z", "y"])
+def test_one_row_has_no_stride(lib, name):  # noqa: F811
+    """Whatever the distance to a row that is not there, a prompt of one row gets past the strides (here to the
+    pointers)."""
+    for n in (1 << 23, 1 << 40):
+        st = ssm.GatedStrides(**{name: n})
+        assert prompt(lib, seqs=packed(total=1, sequences=1), st=st, param=None) == INVALID and "NULL" in err(lib)
+        assert prompt(lib, seqs=packed(total=2, sequences=1), st=st, param=None) == UNSUPPORTED
+
+
 @pytest.mark.parametrize("call", [prompt, step])
 @pytest.mark.parametrize("kw,status", [(dict(reserved=1), INVALID), (dict(slots=-1), INVALID), (dict(slots=1 << 31), INVALID),
                                        (dict(slot_stride=5), INVALID), (dict(data=None), INVALID), (dict(dtype=7), UNSUPPORTED)])
