@@ -19,6 +19,14 @@ from . import SSM_BF16, SSM_F32, Entries, _check, load_library
 from .serving import _dense, _row_stride, _run
 
 
+def _code(dtype: torch.dtype) -> int:
+    if dtype is torch.bfloat16:
+        return SSM_BF16
+    if dtype is torch.float32:
+        return SSM_F32
+    raise TypeError(f"logits must be float32 or bfloat16, got {dtype}")
+
+
 @functools.lru_cache(maxsize=256)  # of the sizes alone, and a call into the library costs a microsecond
 def _workspace_bytes(batch: int, rows: int, vocab: int, beams: int, code: int) -> int:
     n = ctypes.c_int64(0)
@@ -38,13 +46,7 @@ def ssm_beam_select(logits: torch.Tensor, scores: torch.Tensor, beams: int, *, f
     if logits is None or logits.dim() != 3:
         raise ValueError("logits must be (batch, rows, vocab)")
     batch, rows, vocab = logits.shape
-    dev = logits.get_device()
-    if logits.dtype is torch.bfloat16:
-        code = SSM_BF16
-    elif logits.dtype is torch.float32:
-        code = SSM_F32
-    else:
-        raise TypeError(f"logits must be float32 or bfloat16, got {logits.dtype}")
+    dev, code = logits.get_device(), _code(logits.dtype)
     sb, sr, sv = logits.stride()
     if vocab > 1 and sv != 1:
         raise ValueError("the rows of logits must be contiguous")
@@ -82,7 +84,7 @@ def ssm_beam_select(logits: torch.Tensor, scores: torch.Tensor, beams: int, *, f
 
 def ssm_beam_select_workspace(batch: int, rows: int, vocab: int, beams: int, dtype: torch.dtype) -> int:
     """Bytes of workspace of ssm_beam_select for these sizes."""
-    return _workspace_bytes(batch, rows, vocab, beams, SSM_BF16 if dtype == torch.bfloat16 else SSM_F32)
+    return _workspace_bytes(batch, rows, vocab, beams, _code(dtype))
 
 
 def ssm_cache_reorder(caches: Union[torch.Tensor, Sequence[torch.Tensor]], cache_slots: Optional[torch.Tensor],

@@ -25,12 +25,12 @@ from . import SSM_BF16, SSM_F32, GatedStrides, _check, load_library
 from .serving import _cache, _dense, _indices, _optional, _packed, _refuse, _row_stride, _run
 
 
-def _code(x: torch.Tensor) -> int:
-    if x.dtype is torch.bfloat16:
+def _code(dtype: torch.dtype) -> int:
+    if dtype is torch.bfloat16:
         return SSM_BF16
-    if x.dtype is torch.float32:
+    if dtype is torch.float32:
         return SSM_F32
-    raise TypeError(f"x must be float32 or bfloat16, got {x.dtype}")
+    raise TypeError(f"x must be float32 or bfloat16, got {dtype}")
 
 
 def _param_ptrs(a_param, a_bias, x_bias, dim: int, dev: int):
@@ -48,7 +48,7 @@ def _workspace_bytes(batch: int, seqlen: int, dim: int, code: int, backward: int
 
 def ssm_gated_scan_workspace(batch: int, seqlen: int, dim: int, dtype: torch.dtype, backward: bool = False) -> int:
     """Bytes of workspace of a forward or backward over a batch (packed prompts: one sequence of all rows)."""
-    return _workspace_bytes(batch, seqlen, dim, SSM_BF16 if dtype == torch.bfloat16 else SSM_F32, int(bool(backward)))
+    return _workspace_bytes(batch, seqlen, dim, _code(dtype), int(bool(backward)))
 
 
 def _workspace(given: Optional[torch.Tensor], x: torch.Tensor, batch: int, seqlen: int, code: int, backward: int):
@@ -72,7 +72,7 @@ def _batch(x, a_gate, x_gate, a_param, a_bias, x_bias, z, initial_state):
     if x is None or x.dim() != 3:
         raise ValueError("x must be (batch, seqlen, dim)")
     batch, seqlen, dim = shape = x.shape
-    dev, ty, code = x.get_device(), x.dtype, _code(x)
+    dev, ty, code = x.get_device(), x.dtype, _code(x.dtype)
     f = torch.float32
     px, pa, pg = (_dense(t, n, shape, ty, dev) for t, n in ((x, "x"), (a_gate, "a_gate"), (x_gate, "x_gate")))
     pp, pab, pxb = _param_ptrs(a_param, a_bias, x_bias, dim, dev)
@@ -187,7 +187,7 @@ def _rows(x, a_gate, x_gate, a_param, a_bias, x_bias, z, y):
     if x is None or x.dim() != 2:
         raise ValueError("x must be (rows, dim)")
     shape = x.shape
-    dev, ty, code = x.get_device(), x.dtype, _code(x)
+    dev, ty, code = x.get_device(), x.dtype, _code(x.dtype)
     strides = GatedStrides(_row2(x, "x", shape, ty, dev), _row2(a_gate, "a_gate", shape, ty, dev),
                            _row2(x_gate, "x_gate", shape, ty, dev), 0 if z is None else _row2(z, "z", shape, ty, dev),
                            0 if y is None else _row2(y, "y", shape, ty, dev))

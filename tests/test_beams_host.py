@@ -119,3 +119,9 @@ def test_host_tensors_are_refused():
         ssm.ssm_beam_select(t(2, 3, 50), t(2, 3), 4)
     with pytest.raises(ValueError, match="expected a GPU"):
         ssm.ssm_cache_reorder(t(9, 5), None, t(2, 4, dtype=torch.int32))
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.float64, torch.int8])
+def test_no_workspace_for_types_that_the_call_refuses(dtype):
+    with pytest.raises(TypeError, match="float32 or bfloat16"):
+        ssm.ssm_beam_select_workspace(2, 3, 50, 4, dtype)

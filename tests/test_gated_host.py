@@ -224,3 +224,10 @@ def test_host_tensors_are_refused():
 def test_checkpoint_shapes():
     assert ssm.gated_checkpoint_shape(1, 2000, 7) == (31, 7) and ssm.gated_checkpoint_shape(3, 300, 7) == (12, 7)
     assert ssm.gated_checkpoint_shape(3, 200, 7) == (9, 7) and ssm.gated_checkpoint_shape(2, 5, 7) == (0, 7)
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.float64, torch.int8])
+def test_no_workspace_for_types_that_the_calls_refuse(dtype):
+    for backward in (False, True):
+        with pytest.raises(TypeError, match="float32 or bfloat16"):
+            ssm.ssm_gated_scan_workspace(2, 500, 64, dtype, backward)
