@@ -29,7 +29,7 @@ struct BeamArgs {
   const float* scores;      // (batch, rows)
   const uint8_t* finished;  // (batch, rows) or NULL
   int32_t rows, beams, eos;
-  int64_t batch, vocab;
+  int64_t vocab;
   int32_t chunks, blocks;   // stretches of a row, 16-byte blocks of a stretch
   uint64_t* best;           // (batch * rows, beams, chunks): key and token, a stretch's largest first
   float* stats;             // (batch * rows, chunks, waves, 2): largest logit, sum of exp(logit - it)

@@ -108,7 +108,7 @@ ssm_status_t ssm_beam_select(int64_t batch, int64_t rows, int64_t vocab, int64_t
   ssm::BeamArgs a{};
   a.logits = logits; a.sb = stride_batch; a.sr = stride_row; a.scores = scores; a.finished = finished;
   a.rows = static_cast<int32_t>(rows); a.beams = static_cast<int32_t>(beams); a.eos = static_cast<int32_t>(eos);
-  a.batch = batch; a.vocab = vocab;
+  a.vocab = vocab;
   a.chunks = static_cast<int32_t>(s.chunks); a.blocks = static_cast<int32_t>(s.blocks);
   a.best = static_cast<uint64_t*>(workspace);
   a.stats = reinterpret_cast<float*>(a.best + s.words * beams);
