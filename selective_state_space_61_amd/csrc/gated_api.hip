@@ -29,7 +29,8 @@ Tiled backward_of(bool z) {
 }
 
 // The forward's shape: 8 bytes of a bf16 row or of an fp32 row a lane; the backward's two channels of 64 rows, what
-// its registers hold.  Single channels where dim has fewer.
+// its registers hold.  Single channels below 4 (backward 2), since a lane's must lie in the row: 64 x 16384 x 3 bf16 rows
+// take 391 us forward, in tiles of 32 rows, and 332 backward; of 4 channels, in tiles of 128, 147 and 309.
 Tiled forward_kernel(bool bf16, int64_t dim, bool z) {
   if (dim < 4) return bf16 ? forward_of<true, 1, 8>(z) : forward_of<false, 1, 8>(z);
   return bf16 ? forward_of<true, 4, 8>(z) : forward_of<false, 2, 8>(z);
@@ -44,7 +45,14 @@ Tiled backward_kernel(bool bf16, int64_t dim, bool z) {
 // tile waits: 2000 x 40 x 1024 bf16 rows forward, 120 of 128, 207 us for 218, 60 x 40 x 1024 15 for 20; backward, 40
 // of 64, 496 for 401); else of all rows, which may share tiles.  The tiles and the bytes that they publish through
 // (0 where no tile enters another).
-constexpr int64_t kOwnTiles = 256;  // rows of a sequence from which on it has tiles of its own
+//
+// Rows of a sequence from which on it has tiles of its own.  64 sequences of 1536 channels (bf16, us forward and backward) in
+// tiles of their own and across sequences: 192 rows 67 and 97 for 58 and 100, 200 rows 67 and 113 for 61 and 104;
+// 256 rows 71 and 121 for 72 and 125, 384 rows 98 and 170 for 101 and 178, 700 rows 169 and 288 for 171 and 325, 32 of
+// 1024 rows 120 and 218 for 128 and 235.  Lengths whose last tile is nearly empty lose up to about 600 rows: 260 rows 89 and
+// 138 for 74 and 129, 400 rows 118 and 190 for 105 and 186; so does the backward in fp32, 200 x 256 x 256 61 and 117 for 61 and
+// 108, 200 x 700 x 256 147 and 276 for 151 and 275.  (The checkpoints' layout goes by this length.)
+constexpr int64_t kOwnTiles = 256;
 struct Cut {
   int64_t tiles, each, pitch, published, words;  // each: of a sequence (0: shared); words: where they begin
 };

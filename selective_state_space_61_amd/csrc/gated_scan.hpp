@@ -334,8 +334,9 @@ __device__ __forceinline__ void no_row(Run<BF16, V>& r, bool off, bool closed) {
 
 // The decay of a stretch of steps, from the product of theirs and the least of them: 0 only if a step's is.  The
 // product alone rounds to 0 after a few dozen ordinary steps and would make a NaN of an infinite state that each of
-// them keeps, here or there as tiles happen to begin.  2^-149 in its place adds to a finite state what a rounding
-// would.  (No decay exceeds 1, so the product is at most the least and the middle one of the three is meant.)
+// them keeps, here or there as tiles happen to begin.  2^-149 in its place keeps that much of a finite state, twice what
+// a product down there is rounded by: below 2^-24 up to states of 4e37.  (No decay exceeds 1, so the product is at
+// most the least and the middle one of the three is meant.)
 __device__ __forceinline__ float stretch_decay(float product, float least) {
   return __builtin_amdgcn_fmed3f(product, least, 0x1p-149f);
 }
@@ -435,8 +436,8 @@ __device__ __forceinline__ int64_t checkpoint_after(const GatedArgs& p, const Tu
 }
 
 // Forward.  Bound by the memory, as far as loading, composing, waiting and storing of three workgroups a CU overlap:
-// 8 x 2048 x 1536 bf16 take 64 us (251 MB, 3.9 TB/s, VALU 53% busy), 30011 x 2560 179 (4.3 TB/s), 12288 x 5120 packed
-// columns of a wider tensor 160 (5.2 TB/s of what moves: rows that begin anywhere share lines).  Tiles of 128 rows
+// 8 x 2048 x 1536 bf16 take 64 us (251 MB, 3.9 TB/s, VALU 53% busy), 30011 x 2560 181 (4.3 TB/s), 12288 x 5120 packed
+// columns of a wider tensor 161 (5.2 TB/s of what moves: rows that begin anywhere share lines).  Tiles of 128 rows
 // and 64 channels: of half the rows 30% slower, workgroups of 384 or 512 threads 20% and more.
 template <bool BF16, bool Z, int V, int R>
 __global__ __launch_bounds__(kGatedThreads) void gated_scan_kernel(const GatedArgs p) {
@@ -615,7 +616,7 @@ __global__ __launch_bounds__(kGatedThreads) void gated_scan_kernel(const GatedAr
 // E is 0 where w is (a = 1): l / w -> 0 as l -> 0, so the product has that limit though dw/dl has none.
 // The states come from the checkpoint before the tile and the tile's own rows; a G is carried from tile
 // to tile like the forward's state, tiles taken from the last one on.
-// Bound like the forward: 8 x 2048 x 1536 bf16 take 104 us (453 MB, 4.4 TB/s, VALU 61% busy), 30011 x 2560 329 (4.2
+// Bound like the forward: 8 x 2048 x 1536 bf16 take 104 us (453 MB, 4.4 TB/s, VALU 61% busy), 30011 x 2560 331 (4.2
 // TB/s); with the arithmetic taken out the loads and stores alone took nine tenths of the time.
 
 // Stores the sum over all rows of quantity k: E (da_param), da_gate (da_bias) or dx_gate (dx_bias).
